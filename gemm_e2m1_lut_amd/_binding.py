@@ -60,6 +60,10 @@ def load_library() -> ctypes.CDLL:
         "nm_spmm": (ctypes.c_int, [vp, vp, vp, vp, i32, i64, i64, i64, i32, i32, vp]),
         "mxfp4_quantize": (ctypes.c_int, [vp, vp, vp, i64, i64, vp]),
         "nvfp4_quantize": (ctypes.c_int, [vp, vp, vp, vp, i64, i64, vp]),
+        "int8_quantize": (ctypes.c_int, [vp, i32, vp, vp, i64, i64, vp]),
+        "rmsnorm_int8_quantize": (ctypes.c_int, [vp, vp, vp, i32, ctypes.c_float, vp, vp, vp, i64, i64, vp]),
+        "silu_mul_int8_quantize": (ctypes.c_int, [vp, i32, vp, vp, i64, i64, vp]),
+        "int8_gemm": (ctypes.c_int, [vp, vp, vp, vp, vp, vp, i32, i64, i64, i64, vp]),
         "ternary_gemv": (ctypes.c_int, [vp, vp, vp, vp, i64, i64, vp]),
         "ternary_gemm_workspace_size": (sz, [i64, i64, i64]),
         "ternary_gemm": (ctypes.c_int, [vp, vp, vp, vp, vp, sz, i64, i64, i64, vp]),
@@ -284,6 +288,151 @@ def nvfp4_quantize(x: torch.Tensor, global_scale: torch.Tensor,
     _need(out[1], "out[1]", _SCALE8, (rows, k // 16))
     _check("nvfp4_quantize", load_library().nvfp4_quantize(_ptr(x), _ptr(global_scale), _ptr(out[0]),
                                                             _ptr(out[1]), rows, k, _stream(stream)))
+    return out
+
+
+# ------------------------------------------------------------------- int8 --
+# Called for every layer of every token, so one test accepts a good tensor and
+# only a bad one goes through the checks that say what is wrong.
+
+_FLOAT_CODE = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
+INT8_MAX_K = 131056
+
+
+def _need_on(t, name: str, dtype: torch.dtype, shape: tuple, device: torch.device) -> int:
+    """_need, and on `device`; the tensor's address."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device
+            and t.is_contiguous()):
+        _need(t, name, (dtype,), shape)
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    return t.data_ptr()
+
+
+def _float_rows(x, name: str) -> tuple:
+    """(rows, columns, dtype code, device) of a [rows, k] fp32 or bf16 tensor."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError(f"{name} must be a [rows, k] tensor")
+    code = _FLOAT_CODE.get(x.dtype)
+    if code is None or not x.is_cuda or not x.is_contiguous():
+        _need(x, name, tuple(_FLOAT_CODE))
+    rows, k = x.shape
+    return rows, k, code, x.device
+
+
+def _stream_on(stream, device: torch.device):
+    """The torch stream a call on `device` runs on."""
+    if stream is None:
+        return torch.cuda.current_stream(device)
+    if not hasattr(stream, "cuda_stream"):
+        handle = int(stream)
+        return torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+    if stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
+    return stream
+
+
+def _new(shapes, device: torch.device, given, stream) -> list:
+    """Outputs [(shape, dtype), ...]; those for a stream of the caller's are allocated for that stream, so their
+    memory is not still in use by work queued on another one."""
+    if given is None:
+        return [torch.empty(s, dtype=d, device=device) for s, d in shapes]
+    with torch.cuda.stream(stream):
+        return [torch.empty(s, dtype=d, device=device) for s, d in shapes]
+
+
+def _call_on(device: torch.device, stream, name: str, *args) -> None:
+    fn = getattr(load_library(), name)
+    if torch.cuda.current_device() == device.index:
+        status = fn(*args, stream.cuda_stream)
+    else:   # the launch goes to the tensors' device, whichever is current
+        with torch.cuda.device(device):
+            status = fn(*args, stream.cuda_stream)
+    if status != 0:
+        _check(name, status)
+
+
+def _codes_out(out, rows: int, k: int, device: torch.device, given, stream):
+    if out is None:
+        out = tuple(_new((((rows, k), torch.int8), ((rows,), torch.float32)), device, given, stream))
+    q, scale = out
+    return (out, _need_on(q, "out[0]", torch.int8, (rows, k), device),
+            _need_on(scale, "out[1]", torch.float32, (rows,), device))
+
+
+def int8_quantize(x: torch.Tensor, out: tuple[torch.Tensor, torch.Tensor] | None = None,
+                  stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """bf16 or fp32 [rows, k] -> (codes int8 [rows, k], scale fp32 [rows]); x is about codes * scale."""
+    rows, k, code, device = _float_rows(x, "x")
+    on = _stream_on(stream, device)
+    out, qp, sp = _codes_out(out, rows, k, device, stream, on)
+    _call_on(device, on, "int8_quantize", x.data_ptr(), code, qp, sp, rows, k)
+    return out
+
+
+def rmsnorm_int8_quantize(x: torch.Tensor, weight: torch.Tensor, eps: float, residual: torch.Tensor | None = None,
+                          residual_out: torch.Tensor | None = None,
+                          out: tuple[torch.Tensor, torch.Tensor] | None = None, stream=None) -> tuple:
+    """Codes and scales of rmsnorm(x + residual) * weight: x, residual [rows, k] and weight [k], all bf16 or all fp32.
+
+    Returns (codes int8 [rows, k], scale fp32 [rows]), and with a residual also residual_out = x + residual in the
+    input type (allocated when not given; it may be residual itself)."""
+    rows, k, code, device = _float_rows(x, "x")
+    wp = _need_on(weight, "weight", x.dtype, (k,), device)
+    on = _stream_on(stream, device)
+    rp = hp = None
+    if residual is not None:
+        rp = _need_on(residual, "residual", x.dtype, (rows, k), device)
+        if residual_out is None:
+            residual_out, = _new((((rows, k), x.dtype),), device, stream, on)
+        hp = _need_on(residual_out, "residual_out", x.dtype, (rows, k), device)
+    elif residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    out, qp, sp = _codes_out(out, rows, k, device, stream, on)
+    _call_on(device, on, "rmsnorm_int8_quantize", x.data_ptr(), rp, wp, code, eps, hp, qp, sp, rows, k)
+    return out if residual is None else (*out, residual_out)
+
+
+def silu_mul_int8_quantize(gate_up: torch.Tensor, out: tuple[torch.Tensor, torch.Tensor] | None = None,
+                           stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """bf16 or fp32 [rows, 2 inter], gate then up -> codes int8 [rows, inter] and scale fp32 [rows] of silu(gate) * up."""
+    rows, both, code, device = _float_rows(gate_up, "gate_up")
+    if both % 2 != 0:
+        raise ValueError(f"gate_up has {both} columns, expected gate and up of one width")
+    inter = both // 2
+    on = _stream_on(stream, device)
+    out, qp, sp = _codes_out(out, rows, inter, device, stream, on)
+    _call_on(device, on, "silu_mul_int8_quantize", gate_up.data_ptr(), code, qp, sp, rows, inter)
+    return out
+
+
+def int8_gemm(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
+              bias: torch.Tensor | None = None, out: torch.Tensor | None = None,
+              out_dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+    """y[m, n] = (x . w^T) * x_scale[m] * w_scale[n] + bias[n]: x int8 [m, k], w int8 [n, k], scales and bias fp32,
+    exact int32 sums, y fp32 or bf16 (the type of `out` where it is given)."""
+    for t, name in ((x, "x"), (w, "w")):
+        if not isinstance(t, torch.Tensor) or t.dim() != 2:
+            raise ValueError(f"{name} must be a 2-dimensional tensor")
+    m, k = x.shape
+    n = w.shape[0]
+    device = w.device
+    if not w.is_cuda:
+        raise ValueError(f"w must be on a GPU, got {device}")
+    xp = _need_on(x, "x", torch.int8, (m, k), device)
+    wp = _need_on(w, "w", torch.int8, (n, k), device)
+    xsp = _need_on(x_scale, "x_scale", torch.float32, (m,), device)
+    wsp = _need_on(w_scale, "w_scale", torch.float32, (n,), device)
+    bp = None if bias is None else _need_on(bias, "bias", torch.float32, (n,), device)
+    if out is not None:
+        out_dtype = out.dtype
+    code = _FLOAT_CODE.get(out_dtype)
+    if code is None:
+        raise TypeError("the output must be torch.float32 or torch.bfloat16")
+    on = _stream_on(stream, device)
+    if out is None:
+        out, = _new((((m, n), out_dtype),), device, stream, on)
+    yp = _need_on(out, "out", out_dtype, (m, n), device)
+    _call_on(device, on, "int8_gemm", xp, xsp, wp, wsp, bp, yp, code, m, n, k)
     return out
 
 

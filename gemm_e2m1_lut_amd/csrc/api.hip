@@ -2,6 +2,7 @@
 // include/e2m1lut.h): host-side validation, then one asynchronous launch
 // sequence on the caller's stream. Nothing here allocates, copies or
 // synchronises; on a negative status nothing was launched.
+#include <float.h>
 #include <limits.h>
 
 #include <mutex>
@@ -32,6 +33,8 @@ inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintp
 
 // a * b without signed overflow, for non-negative operands.
 inline bool mul_ok(int64_t a, int64_t b) { return a == 0 || b <= INT64_MAX / a; }
+
+constexpr int64_t kMaxInt8Rows = (int64_t)1 << 34;   // a grid of 2^20 x 2^14 workgroups
 
 inline int launch_status(hipError_t e) { return e == hipSuccess ? E2M1_OK : E2M1_ERR_LAUNCH; }
 
@@ -204,6 +207,68 @@ int nvfp4_quantize(const uint16_t* x_bf16, const float* global_scale, uint8_t* p
     if (!aligned(x_bf16, 16) || !aligned(packed, 8) || !aligned(global_scale, 4)) return E2M1_ERR_ALIGN;
     return launch_status(e2m1::launch_nvfp4_quantize(x_bf16, global_scale, packed, block_scale_e4m3,
                                                      rows * (k / 16), as_stream(stream)));
+}
+
+static bool int8_rows_ok(int64_t rows, int64_t k, int64_t kmax) {
+    return rows >= 0 && k >= 0 && k % 16 == 0 && k < kmax && rows <= kMaxInt8Rows && mul_ok(rows, 8 * k);
+}
+
+// k == 0: every scale is 0 and there is no code.
+static int int8_no_columns(float* scale, int64_t rows, void* stream) {
+    if (!scale) return E2M1_ERR_NULL;
+    if (!aligned(scale, 4)) return E2M1_ERR_ALIGN;
+    return launch_status(fill_zero_bytes(scale, rows * 4, as_stream(stream)));
+}
+
+int int8_quantize(const void* x, int x_dtype, int8_t* q, float* scale, int64_t rows, int64_t k, void* stream) {
+    if (x_dtype != E2M1_DTYPE_F32 && x_dtype != E2M1_DTYPE_BF16) return E2M1_ERR_DTYPE;
+    if (!int8_rows_ok(rows, k, (int64_t)1 << 31)) return E2M1_ERR_SHAPE;
+    if (rows == 0) return E2M1_OK;
+    if (k == 0) return int8_no_columns(scale, rows, stream);
+    if (!x || !q || !scale) return E2M1_ERR_NULL;
+    if (!aligned(x, 16) || !aligned(q, 16) || !aligned(scale, 4)) return E2M1_ERR_ALIGN;
+    return launch_status(e2m1::launch_int8_quantize(x, x_dtype == E2M1_DTYPE_BF16, q, scale, rows, k,
+                                                    as_stream(stream)));
+}
+
+int rmsnorm_int8_quantize(const void* x, const void* residual, const void* weight, int dtype, float eps,
+                          void* residual_out, int8_t* q, float* scale, int64_t rows, int64_t k, void* stream) {
+    if (dtype != E2M1_DTYPE_F32 && dtype != E2M1_DTYPE_BF16) return E2M1_ERR_DTYPE;
+    if (!int8_rows_ok(rows, k, (int64_t)1 << 31) || !(eps >= 0.f && eps <= FLT_MAX)) return E2M1_ERR_SHAPE;
+    if (rows == 0) return E2M1_OK;
+    if (k == 0) return int8_no_columns(scale, rows, stream);
+    if (!x || !weight || !q || !scale || !residual != !residual_out) return E2M1_ERR_NULL;
+    if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(residual_out, 16) ||
+        !aligned(q, 16) || !aligned(scale, 4))
+        return E2M1_ERR_ALIGN;
+    return launch_status(e2m1::launch_rmsnorm_int8_quantize(x, residual, weight, dtype == E2M1_DTYPE_BF16, eps,
+                                                            residual_out, q, scale, rows, k, as_stream(stream)));
+}
+
+int silu_mul_int8_quantize(const void* gate_up, int dtype, int8_t* q, float* scale, int64_t rows, int64_t inter,
+                           void* stream) {
+    if (dtype != E2M1_DTYPE_F32 && dtype != E2M1_DTYPE_BF16) return E2M1_ERR_DTYPE;
+    if (!int8_rows_ok(rows, inter, (int64_t)1 << 30)) return E2M1_ERR_SHAPE;
+    if (rows == 0) return E2M1_OK;
+    if (inter == 0) return int8_no_columns(scale, rows, stream);
+    if (!gate_up || !q || !scale) return E2M1_ERR_NULL;
+    if (!aligned(gate_up, 16) || !aligned(q, 16) || !aligned(scale, 4)) return E2M1_ERR_ALIGN;
+    return launch_status(e2m1::launch_silu_mul_int8_quantize(gate_up, dtype == E2M1_DTYPE_BF16, q, scale, rows,
+                                                             inter, as_stream(stream)));
+}
+
+int int8_gemm(const int8_t* x, const float* x_scale, const int8_t* w, const float* w_scale, const float* bias,
+              void* y, int y_dtype, int64_t m, int64_t n, int64_t k, void* stream) {
+    if (y_dtype != E2M1_DTYPE_F32 && y_dtype != E2M1_DTYPE_BF16) return E2M1_ERR_DTYPE;
+    if (m < 0 || n < 0 || k < 0 || k % 16 != 0 || k > E2M1_INT8_MAX_K || m > INT_MAX || n > INT_MAX ||
+        !mul_ok(m, 4 * n))
+        return E2M1_ERR_SHAPE;
+    if (m == 0 || n == 0) return E2M1_OK;
+    if (!y || !x_scale || !w_scale || (k > 0 && (!x || !w))) return E2M1_ERR_NULL;
+    if (!aligned(x, 16) || !aligned(w, 16) || !aligned(y, y_dtype == E2M1_DTYPE_F32 ? 4 : 2) || !aligned(x_scale, 4) || !aligned(w_scale, 4) || !aligned(bias, 4))
+        return E2M1_ERR_ALIGN;
+    return launch_status(e2m1::launch_int8_gemm(x, x_scale, w, w_scale, bias, y, y_dtype == E2M1_DTYPE_BF16, m, n, k,
+                                                as_stream(stream)));
 }
 
 int ternary_gemv(const uint32_t* packed, const float* row_scale, const float* x, float* y,

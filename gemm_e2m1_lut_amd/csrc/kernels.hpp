@@ -43,6 +43,20 @@ hipError_t launch_gemm(const uint8_t* packed, const uint8_t* scales, const uint1
 hipError_t launch_nm_spmm(const uint16_t* values, const uint32_t* meta, const uint16_t* x, void* y, bool out_bf16,
                           int64_t batch, int64_t rows, int64_t k, int nn, int mm, hipStream_t stream);
 
+// bf16 (or fp32) rows -> int8 codes and one scale per row; k % 16 == 0, k >= 16.
+hipError_t launch_int8_quantize(const void* x, bool bf16, int8_t* q, float* scale, int64_t rows, int64_t k,
+                                hipStream_t stream);
+// residual (and then residual_out) may be null
+hipError_t launch_rmsnorm_int8_quantize(const void* x, const void* residual, const void* weight, bool bf16, float eps,
+                                        void* residual_out, int8_t* q, float* scale, int64_t rows, int64_t k,
+                                        hipStream_t stream);
+hipError_t launch_silu_mul_int8_quantize(const void* gate_up, bool bf16, int8_t* q, float* scale, int64_t rows,
+                                         int64_t inter, hipStream_t stream);
+
+hipError_t launch_int8_gemm(const int8_t* x, const float* x_scale, const int8_t* w, const float* w_scale,
+                            const float* bias, void* y, bool out_bf16, int64_t m, int64_t n, int64_t k,
+                            hipStream_t stream);
+
 hipError_t launch_ternary(const uint32_t* packed, const float* row_scale, const float* x, float* y,
                           int64_t n, int64_t k, hipStream_t stream);
 

@@ -62,7 +62,7 @@ extern "C" {
 #define E2M1_ERR_WORKSPACE (-5) /* workspace missing or smaller than required */
 #define E2M1_ERR_LAUNCH (-6)    /* the HIP runtime reported an error at launch (e.g. no gfx950 code for the device) */
 
-/* Output dtype codes for dequant_gemv. */
+/* Dtype codes of outputs (dequant_gemv and its like) and of the int8 quantizers' inputs. */
 #define E2M1_DTYPE_F32 0
 #define E2M1_DTYPE_BF16 1
 
@@ -221,6 +221,83 @@ int mxfp4_quantize(const uint16_t* x_bf16, uint8_t* packed, uint8_t* scale_e8m0,
  */
 int nvfp4_quantize(const uint16_t* x_bf16, const float* global_scale, uint8_t* packed,
                    uint8_t* block_scale_e4m3, int64_t rows, int64_t k, void* stream);
+
+/*
+ * int8_quantize -- rows of bf16 or fp32 values to int8 codes with one fp32
+ * scale per row: activations per token, weights per output channel (the
+ * encode side of int8_gemm).
+ * Operation, per row: pmax = max |x|; q = the integer nearest to 127 x / pmax,
+ * decided on the exact quotient, ties to even (so |q| <= 127 and the largest
+ * element gets +/-127); scale = fl32(pmax / 127). A row of zeros (and k == 0)
+ * gets codes 0 and scale 0. A row that holds a NaN or an infinity gets codes
+ * 0 and scale NaN, so whatever is computed from it shows it.
+ *   x       [rows, k], fp32 (x_dtype = E2M1_DTYPE_F32) or bf16 (E2M1_DTYPE_BF16), 16-byte aligned
+ *   q       int8 [rows, k], overwritten (16-byte aligned)
+ *   scale   fp32 [rows], overwritten (4-byte aligned)
+ * Requires rows, k >= 0, k % 16 == 0, k below 2^31.
+ */
+int int8_quantize(const void* x, int x_dtype, int8_t* q, float* scale, int64_t rows, int64_t k, void* stream);
+
+/*
+ * rmsnorm_int8_quantize -- residual addition, root-mean-square norm and the
+ * int8 codes of the normed rows in one pass.
+ * Operation, per row: h = fl32(x + residual) (h = x without a residual);
+ * p = fl32(h * weight); codes of p as in int8_quantize (the norm's factor
+ * cancels in 127 p / pmax); scale = fl32(pmax / (127 sqrt(mean(h^2) + eps))),
+ * the mean summed in 64 bits; residual_out = h rounded to the input type, for
+ * the next residual addition. The norm sees h before that rounding.
+ * Zero and non-finite rows (of p) as in int8_quantize; residual_out is h
+ * whatever the row holds.
+ *   x             [rows, k], dtype E2M1_DTYPE_F32 or E2M1_DTYPE_BF16 (16-byte aligned)
+ *   residual      [rows, k] of the same type (16-byte aligned), or NULL
+ *   weight        [k] of the same type (16-byte aligned)
+ *   residual_out  [rows, k] of the same type (16-byte aligned), overwritten; may be
+ *                 residual itself (updated in place), otherwise it overlaps
+ *                 no input. NULL exactly when residual is NULL.
+ *   q, scale      as for int8_quantize
+ * Requires rows, k >= 0, k % 16 == 0, k below 2^31, eps finite and >= 0.
+ */
+int rmsnorm_int8_quantize(const void* x, const void* residual, const void* weight, int dtype, float eps,
+                          void* residual_out, int8_t* q, float* scale, int64_t rows, int64_t k, void* stream);
+
+/*
+ * silu_mul_int8_quantize -- silu(gate) * up of a gated MLP and the int8 codes
+ * of its rows (the left operand of the down projection).
+ * Operation, per row: P = gate / (1 + exp(-gate)) * up, not rounded;
+ * Pmax = max |P|; q = the integer nearest to 127 P / Pmax, P evaluated in
+ * 64 bits wherever that decides a code; scale = fl32(Pmax / 127).
+ * Non-finite rows as in int8_quantize, a |P| of 2^127 or more among them. A
+ * row whose P are all below the fp32 range counts as a row of zeros.
+ *   gate_up  [rows, 2 inter], fp32 or bf16 (dtype), columns [0, inter) gate and
+ *            [inter, 2 inter) up, as one product over W13 leaves them (16-byte aligned)
+ *   q        int8 [rows, inter], overwritten (16-byte aligned)
+ *   scale    fp32 [rows], overwritten
+ * Requires rows, inter >= 0, inter % 16 == 0, inter below 2^30.
+ */
+int silu_mul_int8_quantize(const void* gate_up, int dtype, int8_t* q, float* scale, int64_t rows, int64_t inter,
+                           void* stream);
+
+/*
+ * int8_gemm -- y = (x . w^T) with int8 operands, an fp32 scale per row of x
+ * (token) and per row of w (output channel), and an optional bias.
+ * Operation: y[i][j] = fl32(fl32(fl32(sum) * x_scale[i]) * w_scale[j]) (+
+ * bias[j] in fp32), sum = sum over k of x[i][k] w[j][k], exact in int32, the
+ * result rounded to the output type to nearest even. Every int8 value is
+ * accepted, -128 included.
+ *   x        int8 [m, k]  (16-byte aligned)
+ *   x_scale  fp32 [m]
+ *   w        int8 [n, k]  (16-byte aligned)
+ *   w_scale  fp32 [n]
+ *   bias     fp32 [n], or NULL
+ *   y        [m, n], fp32 (y_dtype = E2M1_DTYPE_F32) or bf16 bit patterns
+ *            (E2M1_DTYPE_BF16), overwritten; aligned to its elements (rows
+ *            that start 16-byte aligned are stored widest)
+ * Requires m, n >= 0 and below 2^31, k >= 0, k % 16 == 0, k <= E2M1_INT8_MAX_K
+ * (sums stay below 2^31). k == 0 gives the bias, or zeros.
+ */
+#define E2M1_INT8_MAX_K 131056
+int int8_gemm(const int8_t* x, const float* x_scale, const int8_t* w, const float* w_scale, const float* bias,
+              void* y, int y_dtype, int64_t m, int64_t n, int64_t k, void* stream);
 
 /*
  * ternary_gemv -- y[i] = row_scale[i] * sum_k t(i,k) * x[k], t in {-1, 0, +1}.
