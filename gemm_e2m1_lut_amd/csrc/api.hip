@@ -260,12 +260,13 @@ int silu_mul_int8_quantize(const void* gate_up, int dtype, int8_t* q, float* sca
 int int8_gemm(const int8_t* x, const float* x_scale, const int8_t* w, const float* w_scale, const float* bias,
               void* y, int y_dtype, int64_t m, int64_t n, int64_t k, void* stream) {
     if (y_dtype != E2M1_DTYPE_F32 && y_dtype != E2M1_DTYPE_BF16) return E2M1_ERR_DTYPE;
-    if (m < 0 || n < 0 || k < 0 || k % 16 != 0 || k > E2M1_INT8_MAX_K || m > INT_MAX || n > INT_MAX ||
+    if (m < 0 || n < 0 || k < 0 || k % 16 != 0 || k > E2M1_INT8_MAX_K || m > INT_MAX - 255 || n > INT_MAX - 255 ||
         !mul_ok(m, 4 * n))
         return E2M1_ERR_SHAPE;
     if (m == 0 || n == 0) return E2M1_OK;
     if (!y || !x_scale || !w_scale || (k > 0 && (!x || !w))) return E2M1_ERR_NULL;
-    if (!aligned(x, 16) || !aligned(w, 16) || !aligned(y, y_dtype == E2M1_DTYPE_F32 ? 4 : 2) || !aligned(x_scale, 4) || !aligned(w_scale, 4) || !aligned(bias, 4))
+    if (!aligned(x, 16) || !aligned(w, 16) || !aligned(y, y_dtype == E2M1_DTYPE_F32 ? 4 : 2) || !aligned(x_scale, 4) ||
+        !aligned(w_scale, 4) || !aligned(bias, 4))
         return E2M1_ERR_ALIGN;
     return launch_status(e2m1::launch_int8_gemm(x, x_scale, w, w_scale, bias, y, y_dtype == E2M1_DTYPE_BF16, m, n, k,
                                                 as_stream(stream)));

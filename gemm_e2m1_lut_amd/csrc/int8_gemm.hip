@@ -5,6 +5,19 @@
 // The sum is exact: int8 products in int32 accumulators (|sum| <= 2^14 k, below
 // 2^31 for k <= 131056). It is rounded to fp32 once, then multiplied by the two
 // scales and added to the bias in fp32, and rounded to the output type once.
+//
+// gfx950 design. Few rows of x: the bytes of w bound the product, and the stream
+// form reads them at 5.4 to 5.8 TB/s (4096 x 14336: 10.1 us for one row of x,
+// 10.4 for 16; a plain read of the same bytes takes 8.8). Many rows: the matrix
+// cores bound it, and under full load their energy does: with the operands of
+// real matrices the chip lowers its clock (1.3 GHz was measured, 2.4 with
+// constant operands). 16x16x64 tiles take less of it than 32x32x32
+// ones (matrix cores alone, normal codes: 4.09 against 3.42 PFLOP/s; 8192^3:
+// 441 against 494 us), so they are used throughout. Both forms feed the matrix
+// cores from LDS rings that direct-to-LDS loads fill in 128-byte row segments
+// (64-byte ones read at half the L2 rate: 66 against 130 GB/s a compute unit).
+// What bounds a tile of 64 x 64 is the latency of its ring (128 KB in flight),
+// not its barriers: two groups of waves that halve the steps gained nothing.
 #include "device.hpp"
 #include "kernels.hpp"
 
@@ -14,10 +27,6 @@ namespace {
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 
 constexpr uint32_t kOutOfRange = 0xFFFFFFF0u;   // a buffer offset past any resource's range
-
-__device__ __forceinline__ i32x4 load16(__amdgpu_buffer_rsrc_t rsrc, uint32_t off) {
-    return __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, off, 0, 0));
-}
 
 // Four outputs of row m from column n0 on.
 template <bool kBf16Out>
@@ -39,92 +48,28 @@ __device__ __forceinline__ void store4(void* y, int64_t idx, const f32x4& v, int
     }
 }
 
-// ------------------------------------------------------------ split form --
-// A workgroup owns 16 NT rows of w and 16 MT rows of x; its waves split K
-// (128-column steps dealt in turn) and the partial sums meet in LDS. Operands
-// go straight from memory into the matrix cores' registers: lane 16 g + r holds
-// columns 16 g .. + 15 of row r of a 64-column block.
+// ----------------------------------------------------------- direct to LDS --
 
-template <int MT, int NT, bool kBf16Out>
-__global__ __launch_bounds__(1024) void int8_gemm_split_kernel(
-    const int8_t* __restrict__ x, const float* __restrict__ xs, const int8_t* __restrict__ w,
-    const float* __restrict__ ws, const float* __restrict__ bias, void* __restrict__ y, int m, int n, int k) {
-    extern __shared__ __attribute__((aligned(16))) int32_t part[];   // [wave][tile][lane][4]
-    constexpr int kTiles = MT * NT;
-    const int nwaves = blockDim.x / kWave;
-    const int lane = threadIdx.x % kWave;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int r = lane & 15, g = lane >> 4;
-    const int64_t tile_id = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
-    const int tiles_n = (n + 16 * NT - 1) / (16 * NT);
-    const int n0 = (int)(tile_id % tiles_n) * 16 * NT;
-    const int64_t mstart = tile_id / tiles_n * 16 * MT;
-    if (mstart >= m) return;   // the grid's last row may run past the tiles
-    const int m0 = (int)mstart;
-    const int nt = min(16 * NT, n - n0), mt = min(16 * MT, m - m0);
-    const __amdgpu_buffer_rsrc_t wres = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<int8_t*>(w + (int64_t)n0 * k), 0, nt * k, kBufferWord3);
-    const __amdgpu_buffer_rsrc_t xres = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<int8_t*>(x + (int64_t)m0 * k), 0, mt * k, kBufferWord3);
-    i32x4 acc[NT][MT];
-#pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int j = 0; j < MT; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
-
-    const int steps = (k + 127) / 128;
-    constexpr int kAhead = NT + MT <= 2 ? 4 : 2;   // steps whose loads are in flight together
-    for (int s = wave; s < steps; s += nwaves * kAhead) {
-        i32x4 a[kAhead][2][NT], b[kAhead][2][MT];
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int c = 128 * (s + u * nwaves) + 64 * h + 16 * g;
-                const bool live = c < k;   // past the row's end: zeros, no memory access
-#pragma unroll
-                for (int i = 0; i < NT; ++i)
-                    a[u][h][i] = load16(wres, live && 16 * i + r < nt ? (uint32_t)((16 * i + r) * k + c) : kOutOfRange);
-#pragma unroll
-                for (int j = 0; j < MT; ++j)
-                    b[u][h][j] = load16(xres, live && 16 * j + r < mt ? (uint32_t)((16 * j + r) * k + c) : kOutOfRange);
-            }
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int i = 0; i < NT; ++i)
-#pragma unroll
-                    for (int j = 0; j < MT; ++j)
-                        acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[u][h][i], b[u][h][j], acc[i][j], 0, 0, 0);
-    }
-#pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int j = 0; j < MT; ++j)
-            *reinterpret_cast<i32x4*>(part + ((wave * kTiles + i * MT + j) * kWave + lane) * 4) = acc[i][j];
-    __syncthreads();
-    // one quad (row m, four columns n) per thread and turn
-    for (int qd = threadIdx.x; qd < kTiles * kWave; qd += blockDim.x) {
-        i32x4 sum = {0, 0, 0, 0};
-        for (int v = 0; v < nwaves; ++v) sum += *reinterpret_cast<const i32x4*>(part + (v * kTiles * kWave + qd) * 4);
-        const int tile = qd / kWave, l = qd % kWave;
-        const int mm = m0 + 16 * (tile % MT) + (l & 15);
-        const int nn = n0 + 16 * (tile / MT) + 4 * (l >> 4);
-        if (mm >= m || nn >= n) continue;
-        const int count = min(4, n - nn);
-        const float sx = xs[mm];
-        f32x4 v;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int c = min(nn + e, n - 1);
-            v[e] = (float)sum[e] * sx * ws[c];
-            if (bias != nullptr) v[e] += bias[c];
-        }
-        store4<kBf16Out>(y, (int64_t)mm * n + nn, v, count);
-    }
+// the lane's 16 bytes at byte offset voff of the buffer -> LDS lds + 16 * lane (M0 is set here and used
+// by nothing else in these kernels)
+__device__ __forceinline__ void lds_load16(__amdgpu_buffer_rsrc_t rsrc, uint32_t voff, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :: "s"(lds), "v"(voff), "s"(rsrc) : "memory");
 }
+
+// the lane's 4 bytes at p -> LDS lds + 4 * lane, active lanes only
+__device__ __forceinline__ void lds_load4(const float* p, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" :: "s"(lds), "v"(p) : "memory");
+}
+
+// At most kN of this wave's requests are in flight.
+template <int kN>
+__device__ __forceinline__ void wait_vm() {
+    asm volatile("s_waitcnt vmcnt(%0)" :: "n"(kN) : "memory");
+}
+
+// This wave's LDS accesses are done.
+__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
 // `tiles` workgroups in rows of 2^20 (a grid dimension holds fewer than 2^32 threads).
 dim3 grid_of(int64_t tiles) {
@@ -132,15 +77,194 @@ dim3 grid_of(int64_t tiles) {
     return dim3((unsigned)gx, (unsigned)((tiles + gx - 1) / gx));
 }
 
-template <int MT, int NT>
-hipError_t launch_split(const int8_t* x, const float* xs, const int8_t* w, const float* ws, const float* bias, void* y,
-                        bool out_bf16, int64_t m, int64_t n, int64_t k, int waves, hipStream_t stream) {
-    const dim3 grid = grid_of(((n + 16 * NT - 1) / (16 * NT)) * ((m + 16 * MT - 1) / (16 * MT)));
-    const unsigned lds = (unsigned)(waves * MT * NT * kWave * 16);
+// ----------------------------------------------------------- stream form --
+// For few rows of x: the weights' bytes bound it, so the kernel is a stream
+// of w. A workgroup takes tiles of 16 NT rows of w x 16 MT rows of x in turn; its W waves
+// deal the 128-column steps of K among themselves, each with an LDS ring of its
+// own (ST steps of its rows of w and of x, filled by direct-to-LDS requests of
+// 8 rows x 128 bytes), so that no wave waits for another inside a tile and the
+// requests of the next tile are under way while one ends. Lane 16 g + r takes
+// columns 16 g .. + 15 of row r of a 64-column half step; 16x16x64 matrix-core
+// tiles, A = w, B = x. The waves' sums meet in LDS.
+// Tiles start at different quarters of a wave's steps: with every workgroup at
+// the same column of rows 4096 bytes apart the memory channels are hit a few
+// at a time (14336 x 4096, one row of x: 12.7 us without, 10.8 with it).
+
+// Ring stages of a wave. Three or four, with one workgroup on a compute unit instead of two, measured 2 to 10 % slower.
+constexpr int ST = 2;
+
+// Areas for a tile's sums: two in turn (one barrier a tile) unless every wave adds up a block anyway.
+constexpr int stream_areas(int waves, int blocks) { return blocks < waves ? 2 : 1; }
+
+template <int W, int NT, int MT, bool kBf16Out>
+__global__ __launch_bounds__(kWave * W) void int8_gemm_stream_kernel(
+    const int8_t* __restrict__ x, const float* __restrict__ xs, const int8_t* __restrict__ w,
+    const float* __restrict__ ws, const float* __restrict__ bias, void* __restrict__ y, int m, int n, int k,
+    int tiles_n, int tiles_m, int grid_m, int grid_n) {
+    constexpr int kRequests = 2 * (NT + MT);            // 1 KB each: eight rows of w or of x
+    constexpr int kStage = 1024 * kRequests;
+    constexpr int kQuads = NT * MT;                     // 64 quads (four outputs) each
+    constexpr int kArea = (W - 1) * kQuads * 1024;      // sums of the waves but the one that adds them up
+    constexpr int kAreas = stream_areas(W, kQuads);
+    static_assert(kQuads <= W && MT <= 2, "one block a wave, its scales in 64 lanes");
+    __shared__ __attribute__((aligned(256))) uint8_t lds[W * ST * kStage + kAreas * kArea + W * 256];
+    const int lane = threadIdx.x % kWave;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int r = lane & 15, g = lane >> 4;
+    const int steps = (k + 127) / 128;
+    const int per = max((steps + W - 1) / W, 1);        // steps of a wave (its last may lie past K)
+    uint8_t* const ring = lds + wave * ST * kStage;
+    const uint32_t base = (uint32_t)(uintptr_t)ring;
+
+    // request j of an operand fills rows 8 j .. + 7: lane l slot l % 8 of row l / 8, which holds chunk
+    // l % 8 ^ (row / 2 % 8), so that an operand read (16 rows, one chunk) meets every LDS bank once
+    const int col = 16 * ((lane % 8) ^ (lane >> 4));
+    const uint32_t off = (uint32_t)(lane / 8) * (uint32_t)k;
+    // A workgroup's tiles, along w first, then along x: every grid-th, grid = grid_m * tiles_n + grid_n.
+    struct Tile {
+        int m, n;
+    };
+    auto next = [&](Tile& t) __attribute__((always_inline)) {
+        t.m += grid_m;
+        t.n += grid_n;
+        if (t.n >= tiles_n) {
+            t.n -= tiles_n;
+            ++t.m;
+        }
+    };
+    const int tile_m = __builtin_amdgcn_readfirstlane(blockIdx.x / (uint32_t)tiles_n);
+    const Tile start = {tile_m, (int)blockIdx.x - tile_m * tiles_n};
+    // the next request: its tile, the steps left there, its step and ring slot
+    Tile at = start;
+    int left_i = 0, step_i = 0, slot_i = 0;
+    __amdgpu_buffer_rsrc_t wres, xres;
+    auto enter = [&]() __attribute__((always_inline)) {
+        const bool live = at.m < tiles_m;
+        const int n0 = live ? at.n * 16 * NT : 0, m0 = live ? at.m * 16 * MT : 0;
+        const int nt = live ? min(16 * NT, n - n0) : 0;   // rows past them are out of range: zeros
+        const int mt = live ? min(16 * MT, m - m0) : 0;
+        wres = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(w + (int64_t)n0 * k), 0, nt * k, kBufferWord3);
+        xres = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(x + (int64_t)m0 * k), 0, mt * k, kBufferWord3);
+        step_i = (at.n & 3) < per ? at.n & 3 : 0;
+        left_i = per;
+    };
+    auto issue = [&]() __attribute__((always_inline)) {
+        const int c0 = 128 * (wave + W * step_i);
+        const uint32_t even = c0 + col < k ? off + (uint32_t)(c0 + col) : kOutOfRange;
+        const uint32_t odd = c0 + (col ^ 64) < k ? off + (uint32_t)(c0 + (col ^ 64)) : kOutOfRange;
+        const uint32_t into = base + slot_i * kStage;
+#pragma unroll
+        for (int j = 0; j < kRequests; ++j) {
+            const int jj = j < 2 * NT ? j : j - 2 * NT;
+            const uint32_t o = j & 1 ? odd : even;
+            // (selected once more: "out of range" plus a row offset would wrap)
+            const uint32_t v = jj == 0 || o == kOutOfRange ? o : o + (uint32_t)(8 * jj) * (uint32_t)k;
+            lds_load16(j < 2 * NT ? wres : xres, v, __builtin_amdgcn_readfirstlane(into + 1024u * (uint32_t)j));
+        }
+        slot_i = slot_i + 1 == ST ? 0 : slot_i + 1;
+        step_i = step_i + 1 == per ? 0 : step_i + 1;
+        if (--left_i == 0) {
+            next(at);
+            enter();
+        }
+    };
+    enter();
+    const int slot[2] = {r * 128 + 16 * (g ^ (r >> 1)), r * 128 + 16 * ((4 + g) ^ (r >> 1))};
+
+    const float* const sc = reinterpret_cast<const float*>(lds + W * ST * kStage + kAreas * kArea + wave * 256);
+#pragma unroll
+    for (int i = 0; i < ST - 1; ++i) issue();
+    uint8_t* const areas = lds + W * ST * kStage;
+    int ring_slot = 0, turn = 0;
+    for (Tile tile = start; tile.m < tiles_m; next(tile), ++turn) {
+        const int n0 = tile.n * 16 * NT, m0 = tile.m * 16 * MT;
+        const int mine = (wave + turn) % W;       // the block of quads this wave adds up (if there is one)
+        if (mine < kQuads) {
+            // The block's scales and biases, requested like the operands: a wait for a vector load would wait for
+            // the whole ring too. w_scale of the block's 16 rows in lanes 0 .. 15, bias in 16 .. 31, x_scale of
+            // the tile's rows of x from lane 32 on. With two stages the wait of the tile's first step covers it.
+            const int c = n0 + 16 * (mine / MT) + (lane & 15), row = m0 + (lane & 31);
+            const uint32_t into = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)sc);
+            const float* p = lane < 16 ? ws : bias;
+            if (lane < 32 && c < n && p != nullptr) lds_load4(p + c, into);
+            if (lane >= 32 && row < m) lds_load4(xs + row, into);
+        }
+        i32x4 acc[NT][MT];
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int j = 0; j < MT; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+        for (int s = 0; s < per; ++s) {
+            issue();                              // into the slot read in the last turn of this loop
+            wait_vm<kRequests*(ST - 1)>();        // this step's rows are in LDS
+            const uint8_t* p = ring + ring_slot * kStage;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                i32x4 a[NT], b[MT];
+#pragma unroll
+                for (int i = 0; i < NT; ++i) a[i] = *reinterpret_cast<const i32x4*>(p + 2048 * i + slot[h]);
+#pragma unroll
+                for (int j = 0; j < MT; ++j) b[j] = *reinterpret_cast<const i32x4*>(p + 2048 * (NT + j) + slot[h]);
+#pragma unroll
+                for (int i = 0; i < NT; ++i)
+#pragma unroll
+                    for (int j = 0; j < MT; ++j)
+                        acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[i], b[j], acc[i][j], 0, 0, 0);
+            }
+            wait_lds();                           // read: the slot may be filled again
+            ring_slot = ring_slot + 1 == ST ? 0 : ring_slot + 1;
+        }
+        i32x4 sum = {0, 0, 0, 0};
+        uint8_t* const part = areas + (kAreas > 1 ? turn & 1 : 0) * kArea + lane * 16;   // [block][other waves][lane]
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int j = 0; j < MT; ++j) {
+                const int block = i * MT + j;
+                if (mine == block) sum = acc[i][j];
+                else *reinterpret_cast<i32x4*>(part + 1024 * (block * (W - 1) + (mine < block ? mine : mine - 1))) = acc[i][j];
+            }
+        // the sums are in LDS (with two areas one is written again only after the next tile's barrier, which its
+        // readers pass after reading it)
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        if (mine < kQuads) {
+#pragma unroll
+            for (int v = 0; v < W - 1; ++v)
+                sum += *reinterpret_cast<const i32x4*>(part + 1024 * (mine * (W - 1) + v));
+            const f32x4 sw = *reinterpret_cast<const f32x4*>(sc + 4 * g);
+            const f32x4 sb = *reinterpret_cast<const f32x4*>(sc + 16 + 4 * g);
+            const float sx = sc[32 + 16 * (mine % MT) + r];
+            const int mm = m0 + 16 * (mine % MT) + r, nn = n0 + 16 * (mine / MT) + 4 * g;
+            f32x4 v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                v[e] = (float)sum[e] * sx * sw[e];
+                if (bias != nullptr) v[e] += sb[e];
+            }
+            if (mm < m && nn < n) store4<kBf16Out>(y, (int64_t)mm * n + nn, v, min(4, n - nn));
+            wait_lds();   // read: the next tile's scales may land there
+        }
+        if constexpr (kAreas == 1) asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    }
+    wait_vm<0>();   // the requests past the last tile have landed before the workgroup's LDS is released
+}
+
+template <int W, int NT, int MT>
+hipError_t launch_stream(const int8_t* x, const float* xs, const int8_t* w, const float* ws, const float* bias,
+                         void* y, bool out_bf16, int64_t m, int64_t n, int64_t k, hipStream_t stream) {
+    // as many workgroups as the compute units hold at once (by LDS); each takes every grid-th tile
+    constexpr int kLds = W * ST * 2048 * (NT + MT) + stream_areas(W, NT * MT) * (W - 1) * NT * MT * 1024 + W * 256;
+    constexpr int kPerCu = 160 * 1024 / kLds;
+    const int64_t tiles_n = (n + 16 * NT - 1) / (16 * NT), tiles_m = (m + 16 * MT - 1) / (16 * MT);
+    const int64_t most = (int64_t)device_cu_count() * kPerCu, tiles = tiles_n * tiles_m;
+    const int grid = (int)(tiles < most ? tiles : most);
+    const int grid_m = (int)(grid / tiles_n), grid_n = (int)(grid % tiles_n);
     if (out_bf16)
-        int8_gemm_split_kernel<MT, NT, true><<<grid, waves * kWave, lds, stream>>>(x, xs, w, ws, bias, y, (int)m, (int)n, (int)k);
+        int8_gemm_stream_kernel<W, NT, MT, true><<<grid, kWave * W, 0, stream>>>(
+            x, xs, w, ws, bias, y, (int)m, (int)n, (int)k, (int)tiles_n, (int)tiles_m, grid_m, grid_n);
     else
-        int8_gemm_split_kernel<MT, NT, false><<<grid, waves * kWave, lds, stream>>>(x, xs, w, ws, bias, y, (int)m, (int)n, (int)k);
+        int8_gemm_stream_kernel<W, NT, MT, false><<<grid, kWave * W, 0, stream>>>(
+            x, xs, w, ws, bias, y, (int)m, (int)n, (int)k, (int)tiles_n, (int)tiles_m, grid_m, grid_n);
     return hipGetLastError();
 }
 
@@ -160,13 +284,6 @@ hipError_t launch_split(const int8_t* x, const float* xs, const int8_t* w, const
 // NS into the buffer that is now free and reads the first slice of step s + 1.
 // The sums leave through LDS too, one 16-row band of x at a time in an area of
 // the wave's own, so that whole rows of y are scaled and stored.
-
-// the lane's 16 bytes at byte offset voff of the buffer -> LDS lds + 16 * lane (M0 is set here and used
-// by nothing else in these kernels)
-__device__ __forceinline__ void lds_load16(__amdgpu_buffer_rsrc_t rsrc, uint32_t voff, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                 :: "s"(lds), "v"(voff), "s"(rsrc) : "memory");
-}
 
 // This wave's LDS reads are done and at most kN of its requests are in flight; then the workgroup's barrier.
 template <int kN>
@@ -230,6 +347,7 @@ __global__ __launch_bounds__(kWave * kWN * kWM) void int8_gemm_tile_kernel(
     for (int i = 0; i < kXLoads; ++i)
         xoff[i] = (uint32_t)(8 * (kXLoads * wave + i) + lane / 8) * (uint32_t)k + (uint32_t)xcol(i);
     const uint32_t base = (uint32_t)(uintptr_t)&lds[0];
+    const int steps = (k + KS - 1) / KS;
     auto issue = [&](int st, int b) __attribute__((always_inline)) {
         const int c0 = st * KS;   // below 2^18: st <= steps + NS
         const uint32_t at = base + b * kBufBytes;
@@ -260,7 +378,6 @@ __global__ __launch_bounds__(kWave * kWN * kWM) void int8_gemm_tile_kernel(
 #pragma unroll
         for (int j = 0; j < TM; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
 
-    const int steps = (k + KS - 1) / KS;
     constexpr int kPerStep = kWLoads + kXLoads;
 #pragma unroll
     for (int st = 0; st < NS; ++st) issue(st, st);
@@ -356,28 +473,25 @@ hipError_t launch_tile(const int8_t* x, const float* xs, const int8_t* w, const 
     return hipGetLastError();
 }
 
-// Tile shapes and what one 128-column step of a tile takes with every compute unit busy (us, int8 codes of
-// normal values; the two large ones at the clock the chip keeps under that load). The shape whose rounds of
-// tiles over the compute units sum to the least is taken. Measured against it (us; 256 x 256, 256 x 128,
-// 128 x 128, 64 x 128, 64 x 64 rows of w x x):
-//   m 256,  n 4096,  k 4096:   49.0  29.9  23.3  15.5  10.9      m 128, n 14336, k 4096:  57.7  37.5  29.8  22.7  27.1
-//   m 512,  n 4096,  k 4096:   49.5  30.3  24.1  16.6  19.3      m 256, n 14336, k 4096:  58.7  37.2  29.7  36.7  48.2
-//   m 1024, n 4096,  k 4096:   50.5  30.9  25.5  30.7  36.1      m 512, n 14336, k 4096:  60.0  39.0  53.9  68.6  80.2
-//   m 1024, n 14336, k 4096:   64.5  74.0  102.8 117.8 156.8     m 8192, n 8192, k 8192:  441   529   -     -     -
-struct TileShape {
+// The forms and tile shapes, and what a round of tiles over the compute units takes: round_us + step_us for every
+// 128 columns (us; fitted to whole calls with int8 codes of normal values; the two largest tiles at the clock that
+// the chip keeps under their load). The shape whose rounds sum to the least is taken.
+struct Shape {
     int rows_w, rows_x;
-    float step_us;
+    float round_us, step_us;
     hipError_t (*launch)(const int8_t*, const float*, const int8_t*, const float*, const float*, void*, bool, int64_t,
                          int64_t, int64_t, hipStream_t);
 };
-constexpr float kTileFixedUs = 2.5f;   // a round's first requests and its stores
 
-const TileShape kShapes[] = {
-    {256, 256, 1.6f, launch_tile<2, 4, 8, 4, 2>},
-    {256, 128, 0.95f, launch_tile<4, 2, 4, 4, 3>},
-    {128, 128, 0.66f, launch_tile<2, 2, 4, 4, 4>},
-    {64, 128, 0.47f, launch_tile<2, 2, 2, 4, 6>},
-    {64, 64, 0.28f, launch_tile<2, 2, 2, 2, 8>},
+const Shape kShapes[] = {
+    {16, 16, 0.6f, 0.055f, launch_stream<8, 1, 1>},
+    {16, 32, 0.7f, 0.068f, launch_stream<4, 1, 2>},
+    {32, 32, 1.5f, 0.086f, launch_stream<4, 2, 2>},
+    {64, 64, 3.2f, 0.20f, launch_tile<2, 2, 2, 2, 8>},
+    {64, 128, 5.0f, 0.33f, launch_tile<2, 2, 2, 4, 6>},
+    {128, 128, 7.0f, 0.53f, launch_tile<2, 2, 4, 4, 4>},
+    {256, 128, 8.0f, 0.80f, launch_tile<4, 2, 4, 4, 3>},
+    {256, 256, 12.0f, 1.40f, launch_tile<2, 4, 8, 4, 2>},
 };
 
 }  // namespace
@@ -385,17 +499,13 @@ const TileShape kShapes[] = {
 hipError_t launch_int8_gemm(const int8_t* x, const float* x_scale, const int8_t* w, const float* w_scale,
                             const float* bias, void* y, bool out_bf16, int64_t m, int64_t n, int64_t k,
                             hipStream_t stream) {
-    const int64_t steps = (k + 127) / 128;
-    if (m <= 16) {
-        const int waves = steps >= 64 ? 16 : steps >= 16 ? 8 : 4;
-        return launch_split<1, 1>(x, x_scale, w, w_scale, bias, y, out_bf16, m, n, k, waves, stream);
-    }
     const int64_t cus = device_cu_count();
-    const TileShape* best = nullptr;
+    const float steps = (float)((k + 127) / 128);
+    const Shape* best = nullptr;
     float best_us = 0.f;
-    for (const TileShape& s : kShapes) {
+    for (const Shape& s : kShapes) {
         const int64_t tiles = ((n + s.rows_w - 1) / s.rows_w) * ((m + s.rows_x - 1) / s.rows_x);
-        const float us = (float)((tiles + cus - 1) / cus) * ((float)steps * s.step_us + kTileFixedUs);
+        const float us = (float)((tiles + cus - 1) / cus) * (s.round_us + steps * s.step_us);
         if (best == nullptr || us < best_us) {
             best = &s;
             best_us = us;

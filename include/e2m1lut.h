@@ -292,7 +292,7 @@ int silu_mul_int8_quantize(const void* gate_up, int dtype, int8_t* q, float* sca
  *   y        [m, n], fp32 (y_dtype = E2M1_DTYPE_F32) or bf16 bit patterns
  *            (E2M1_DTYPE_BF16), overwritten; aligned to its elements (rows
  *            that start 16-byte aligned are stored widest)
- * Requires m, n >= 0 and below 2^31, k >= 0, k % 16 == 0, k <= E2M1_INT8_MAX_K
+ * Requires 0 <= m, n <= 2^31 - 256, k >= 0, k % 16 == 0, k <= E2M1_INT8_MAX_K
  * (sums stay below 2^31). k == 0 gives the bias, or zeros.
  */
 #define E2M1_INT8_MAX_K 131056
