@@ -7,8 +7,9 @@
 // scales and added to the bias in fp32, and rounded to the output type once.
 //
 // gfx950 design. Few rows of x: the bytes of w bound the product, and the stream
-// form reads them at 5.4 to 5.8 TB/s (4096 x 14336: 10.1 us for one row of x,
-// 10.4 for 16; a plain read of the same bytes takes 8.8). Many rows: the matrix
+// form reads them at 5.0 to 5.7 TB/s (4096 x 14336: 10.3 us for one row of x,
+// 10.9 for 16, 14336 x 4096: 11.2 and 11.4; a plain read of the same bytes
+// takes 8.8). Many rows: the matrix
 // cores bound it, and under full load their energy does: with the operands of
 // real matrices the chip lowers its clock (1.3 GHz was measured, 2.4 with
 // constant operands). 16x16x64 tiles take less of it than 32x32x32
@@ -79,80 +80,59 @@ dim3 grid_of(int64_t tiles) {
 
 // ----------------------------------------------------------- stream form --
 // For few rows of x: the weights' bytes bound it, so the kernel is a stream
-// of w. A workgroup takes tiles of 16 NT rows of w x 16 MT rows of x in turn; its W waves
-// deal the 128-column steps of K among themselves, each with an LDS ring of its
-// own (ST steps of its rows of w and of x, filled by direct-to-LDS requests of
-// 8 rows x 128 bytes), so that no wave waits for another inside a tile and the
-// requests of the next tile are under way while one ends. Lane 16 g + r takes
-// columns 16 g .. + 15 of row r of a 64-column half step; 16x16x64 matrix-core
-// tiles, A = w, B = x. The waves' sums meet in LDS.
-// Tiles start at different quarters of a wave's steps: with every workgroup at
-// the same column of rows 4096 bytes apart the memory channels are hit a few
-// at a time (14336 x 4096, one row of x: 12.7 us without, 10.8 with it).
+// of w. A workgroup takes a tile of 16 NT rows of w x 16 MT rows of x. Its W
+// waves split K, a run of 128-column steps each (runs spread a workgroup's
+// requests over the row, and so over the memory channels: with the steps dealt
+// out one by one, every workgroup is at the same columns of rows that lie 4096
+// bytes apart, and 14336 x 4096 takes 13.2 us instead of 11.8). Each wave has
+// an LDS ring of its own (kStages steps of its rows of w and of x, filled by
+// direct-to-LDS requests of 8 rows x 128 bytes), so that no wave waits for
+// another before the end. Lane 16 g + r takes columns 16 g .. + 15 of row r of
+// a 64-column half step; 16x16x64 matrix-core tiles, A = w, B = x. The waves'
+// sums meet in LDS. (Workgroups that go on to further tiles, with the requests
+// of the next under way while one ends, measured the same.)
 
 // Ring stages of a wave. Three or four, with one workgroup on a compute unit instead of two, measured 2 to 10 % slower.
-constexpr int ST = 2;
-
-// Areas for a tile's sums: two in turn (one barrier a tile) unless every wave adds up a block anyway.
-constexpr int stream_areas(int waves, int blocks) { return blocks < waves ? 2 : 1; }
+constexpr int kStages = 2;
 
 template <int W, int NT, int MT, bool kBf16Out>
 __global__ __launch_bounds__(kWave * W) void int8_gemm_stream_kernel(
     const int8_t* __restrict__ x, const float* __restrict__ xs, const int8_t* __restrict__ w,
     const float* __restrict__ ws, const float* __restrict__ bias, void* __restrict__ y, int m, int n, int k,
-    int tiles_n, int tiles_m, int grid_m, int grid_n) {
+    int tiles_n, int tiles_m) {
     constexpr int kRequests = 2 * (NT + MT);            // 1 KB each: eight rows of w or of x
     constexpr int kStage = 1024 * kRequests;
     constexpr int kQuads = NT * MT;                     // 64 quads (four outputs) each
-    constexpr int kArea = (W - 1) * kQuads * 1024;      // sums of the waves but the one that adds them up
-    constexpr int kAreas = stream_areas(W, kQuads);
     static_assert(kQuads <= W && MT <= 2, "one block a wave, its scales in 64 lanes");
-    __shared__ __attribute__((aligned(256))) uint8_t lds[W * ST * kStage + kAreas * kArea + W * 256];
+    __shared__ __attribute__((aligned(256))) uint8_t lds[W * kStages * kStage + (W - 1) * kQuads * 1024 + W * 256];
     const int lane = threadIdx.x % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int r = lane & 15, g = lane >> 4;
+    // tiles along w first, then along x
+    const uint32_t tile = blockIdx.y * gridDim.x + blockIdx.x;
+    const int tile_m = __builtin_amdgcn_readfirstlane(tile / (uint32_t)tiles_n);
+    if (tile_m >= tiles_m) return;                      // the grid's last row may run past the tiles
+    const int n0 = (int)(tile - (uint32_t)tile_m * (uint32_t)tiles_n) * 16 * NT, m0 = tile_m * 16 * MT;
+    // rows past n or m are out of range: zeros, no memory access
+    const __amdgpu_buffer_rsrc_t wres = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<int8_t*>(w + (int64_t)n0 * k), 0, min(16 * NT, n - n0) * k, kBufferWord3);
+    const __amdgpu_buffer_rsrc_t xres = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<int8_t*>(x + (int64_t)m0 * k), 0, min(16 * MT, m - m0) * k, kBufferWord3);
     const int steps = (k + 127) / 128;
-    const int per = max((steps + W - 1) / W, 1);        // steps of a wave (its last may lie past K)
-    uint8_t* const ring = lds + wave * ST * kStage;
+    const int per = max((steps + W - 1) / W, 1);        // steps of a wave: wave * per on (some may lie past K)
+    uint8_t* const ring = lds + wave * kStages * kStage;
     const uint32_t base = (uint32_t)(uintptr_t)ring;
 
     // request j of an operand fills rows 8 j .. + 7: lane l slot l % 8 of row l / 8, which holds chunk
     // l % 8 ^ (row / 2 % 8), so that an operand read (16 rows, one chunk) meets every LDS bank once
     const int col = 16 * ((lane % 8) ^ (lane >> 4));
     const uint32_t off = (uint32_t)(lane / 8) * (uint32_t)k;
-    // A workgroup's tiles, along w first, then along x: every grid-th, grid = grid_m * tiles_n + grid_n.
-    struct Tile {
-        int m, n;
-    };
-    auto next = [&](Tile& t) __attribute__((always_inline)) {
-        t.m += grid_m;
-        t.n += grid_n;
-        if (t.n >= tiles_n) {
-            t.n -= tiles_n;
-            ++t.m;
-        }
-    };
-    const int tile_m = __builtin_amdgcn_readfirstlane(blockIdx.x / (uint32_t)tiles_n);
-    const Tile start = {tile_m, (int)blockIdx.x - tile_m * tiles_n};
-    // the next request: its tile, the steps left there, its step and ring slot
-    Tile at = start;
-    int left_i = 0, step_i = 0, slot_i = 0;
-    __amdgpu_buffer_rsrc_t wres, xres;
-    auto enter = [&]() __attribute__((always_inline)) {
-        const bool live = at.m < tiles_m;
-        const int n0 = live ? at.n * 16 * NT : 0, m0 = live ? at.m * 16 * MT : 0;
-        const int nt = live ? min(16 * NT, n - n0) : 0;   // rows past them are out of range: zeros
-        const int mt = live ? min(16 * MT, m - m0) : 0;
-        wres = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(w + (int64_t)n0 * k), 0, nt * k, kBufferWord3);
-        xres = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(x + (int64_t)m0 * k), 0, mt * k, kBufferWord3);
-        step_i = (at.n & 3) < per ? at.n & 3 : 0;
-        left_i = per;
-    };
-    auto issue = [&]() __attribute__((always_inline)) {
-        const int c0 = 128 * (wave + W * step_i);
-        const uint32_t even = c0 + col < k ? off + (uint32_t)(c0 + col) : kOutOfRange;
-        const uint32_t odd = c0 + (col ^ 64) < k ? off + (uint32_t)(c0 + (col ^ 64)) : kOutOfRange;
-        const uint32_t into = base + slot_i * kStage;
+    auto issue = [&](int st) __attribute__((always_inline)) {
+        const int c0 = 128 * (wave * per + st);
+        const bool live = st < per;
+        const uint32_t even = live && c0 + col < k ? off + (uint32_t)(c0 + col) : kOutOfRange;
+        const uint32_t odd = live && c0 + (col ^ 64) < k ? off + (uint32_t)(c0 + (col ^ 64)) : kOutOfRange;
+        const uint32_t into = base + (st % kStages) * kStage;
 #pragma unroll
         for (int j = 0; j < kRequests; ++j) {
             const int jj = j < 2 * NT ? j : j - 2 * NT;
@@ -161,110 +141,91 @@ __global__ __launch_bounds__(kWave * W) void int8_gemm_stream_kernel(
             const uint32_t v = jj == 0 || o == kOutOfRange ? o : o + (uint32_t)(8 * jj) * (uint32_t)k;
             lds_load16(j < 2 * NT ? wres : xres, v, __builtin_amdgcn_readfirstlane(into + 1024u * (uint32_t)j));
         }
-        slot_i = slot_i + 1 == ST ? 0 : slot_i + 1;
-        step_i = step_i + 1 == per ? 0 : step_i + 1;
-        if (--left_i == 0) {
-            next(at);
-            enter();
-        }
     };
-    enter();
-    const int slot[2] = {r * 128 + 16 * (g ^ (r >> 1)), r * 128 + 16 * ((4 + g) ^ (r >> 1))};
 
-    const float* const sc = reinterpret_cast<const float*>(lds + W * ST * kStage + kAreas * kArea + wave * 256);
 #pragma unroll
-    for (int i = 0; i < ST - 1; ++i) issue();
-    uint8_t* const areas = lds + W * ST * kStage;
-    int ring_slot = 0, turn = 0;
-    for (Tile tile = start; tile.m < tiles_m; next(tile), ++turn) {
-        const int n0 = tile.n * 16 * NT, m0 = tile.m * 16 * MT;
-        const int mine = (wave + turn) % W;       // the block of quads this wave adds up (if there is one)
-        if (mine < kQuads) {
-            // The block's scales and biases, requested like the operands: a wait for a vector load would wait for
-            // the whole ring too. w_scale of the block's 16 rows in lanes 0 .. 15, bias in 16 .. 31, x_scale of
-            // the tile's rows of x from lane 32 on. With two stages the wait of the tile's first step covers it.
-            const int c = n0 + 16 * (mine / MT) + (lane & 15), row = m0 + (lane & 31);
-            const uint32_t into = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)sc);
-            const float* p = lane < 16 ? ws : bias;
-            if (lane < 32 && c < n && p != nullptr) lds_load4(p + c, into);
-            if (lane >= 32 && row < m) lds_load4(xs + row, into);
-        }
-        i32x4 acc[NT][MT];
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-            for (int j = 0; j < MT; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
-        for (int s = 0; s < per; ++s) {
-            issue();                              // into the slot read in the last turn of this loop
-            wait_vm<kRequests*(ST - 1)>();        // this step's rows are in LDS
-            const uint8_t* p = ring + ring_slot * kStage;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                i32x4 a[NT], b[MT];
-#pragma unroll
-                for (int i = 0; i < NT; ++i) a[i] = *reinterpret_cast<const i32x4*>(p + 2048 * i + slot[h]);
-#pragma unroll
-                for (int j = 0; j < MT; ++j) b[j] = *reinterpret_cast<const i32x4*>(p + 2048 * (NT + j) + slot[h]);
-#pragma unroll
-                for (int i = 0; i < NT; ++i)
-#pragma unroll
-                    for (int j = 0; j < MT; ++j)
-                        acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[i], b[j], acc[i][j], 0, 0, 0);
-            }
-            wait_lds();                           // read: the slot may be filled again
-            ring_slot = ring_slot + 1 == ST ? 0 : ring_slot + 1;
-        }
-        i32x4 sum = {0, 0, 0, 0};
-        uint8_t* const part = areas + (kAreas > 1 ? turn & 1 : 0) * kArea + lane * 16;   // [block][other waves][lane]
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-            for (int j = 0; j < MT; ++j) {
-                const int block = i * MT + j;
-                if (mine == block) sum = acc[i][j];
-                else *reinterpret_cast<i32x4*>(part + 1024 * (block * (W - 1) + (mine < block ? mine : mine - 1))) = acc[i][j];
-            }
-        // the sums are in LDS (with two areas one is written again only after the next tile's barrier, which its
-        // readers pass after reading it)
-        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        if (mine < kQuads) {
-#pragma unroll
-            for (int v = 0; v < W - 1; ++v)
-                sum += *reinterpret_cast<const i32x4*>(part + 1024 * (mine * (W - 1) + v));
-            const f32x4 sw = *reinterpret_cast<const f32x4*>(sc + 4 * g);
-            const f32x4 sb = *reinterpret_cast<const f32x4*>(sc + 16 + 4 * g);
-            const float sx = sc[32 + 16 * (mine % MT) + r];
-            const int mm = m0 + 16 * (mine % MT) + r, nn = n0 + 16 * (mine / MT) + 4 * g;
-            f32x4 v;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                v[e] = (float)sum[e] * sx * sw[e];
-                if (bias != nullptr) v[e] += sb[e];
-            }
-            if (mm < m && nn < n) store4<kBf16Out>(y, (int64_t)mm * n + nn, v, min(4, n - nn));
-            wait_lds();   // read: the next tile's scales may land there
-        }
-        if constexpr (kAreas == 1) asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    for (int i = 0; i < kStages - 1; ++i) issue(i);
+    // Wave b < kQuads adds up block b. Its scales and biases are requested like the operands (a wait for a vector
+    // load would wait for the whole ring too): w_scale of the block's 16 rows in lanes 0 .. 15, bias in 16 .. 31,
+    // x_scale of the tile's rows of x from lane 32 on. They have landed when the last step's rows have.
+    uint8_t* const areas = lds + W * kStages * kStage;
+    const float* const sc = reinterpret_cast<const float*>(areas + (W - 1) * kQuads * 1024 + wave * 256);
+    if (wave < kQuads) {
+        const int c = n0 + 16 * (wave / MT) + (lane & 15), row = m0 + (lane & 31);
+        const uint32_t into = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)sc);
+        const float* p = lane < 16 ? ws : bias;
+        if (lane < 32 && c < n && p != nullptr) lds_load4(p + c, into);
+        if (lane >= 32 && row < m) lds_load4(xs + row, into);
     }
-    wait_vm<0>();   // the requests past the last tile have landed before the workgroup's LDS is released
+
+    const int slot[2] = {r * 128 + 16 * (g ^ (r >> 1)), r * 128 + 16 * ((4 + g) ^ (r >> 1))};
+    i32x4 acc[NT][MT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = 0; j < MT; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+    for (int s = 0; s < per; ++s) {
+        issue(s + kStages - 1);                   // into the slot read in the last turn of this loop
+        wait_vm<kRequests*(kStages - 1)>();       // this step's rows are in LDS
+        const uint8_t* p = ring + (s % kStages) * kStage;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            i32x4 a[NT], b[MT];
+#pragma unroll
+            for (int i = 0; i < NT; ++i) a[i] = *reinterpret_cast<const i32x4*>(p + 2048 * i + slot[h]);
+#pragma unroll
+            for (int j = 0; j < MT; ++j) b[j] = *reinterpret_cast<const i32x4*>(p + 2048 * (NT + j) + slot[h]);
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int j = 0; j < MT; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[i], b[j], acc[i][j], 0, 0, 0);
+        }
+        wait_lds();                               // read: the slot may be filled again
+    }
+
+    i32x4 sum = {0, 0, 0, 0};
+    uint8_t* const part = areas + lane * 16;      // [block][the other waves][lane]
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+            const int block = i * MT + j;
+            if (wave == block) sum = acc[i][j];
+            else
+                *reinterpret_cast<i32x4*>(part + 1024 * (block * (W - 1) + (wave < block ? wave : wave - 1))) = acc[i][j];
+        }
+    wait_vm<0>();   // the requests past the last step have landed before the workgroup's LDS is released
+    wait_lds();
+    __syncthreads();
+    if (wave >= kQuads) return;
+#pragma unroll
+    for (int v = 0; v < W - 1; ++v) sum += *reinterpret_cast<const i32x4*>(part + 1024 * (wave * (W - 1) + v));
+    const f32x4 sw = *reinterpret_cast<const f32x4*>(sc + 4 * g);
+    const f32x4 sb = *reinterpret_cast<const f32x4*>(sc + 16 + 4 * g);
+    const float sx = sc[32 + 16 * (wave % MT) + r];
+    const int mm = m0 + 16 * (wave % MT) + r, nn = n0 + 16 * (wave / MT) + 4 * g;
+    if (mm >= m || nn >= n) return;
+    f32x4 v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        v[e] = (float)sum[e] * sx * sw[e];
+        if (bias != nullptr) v[e] += sb[e];
+    }
+    store4<kBf16Out>(y, (int64_t)mm * n + nn, v, min(4, n - nn));
 }
 
 template <int W, int NT, int MT>
 hipError_t launch_stream(const int8_t* x, const float* xs, const int8_t* w, const float* ws, const float* bias,
                          void* y, bool out_bf16, int64_t m, int64_t n, int64_t k, hipStream_t stream) {
-    // as many workgroups as the compute units hold at once (by LDS); each takes every grid-th tile
-    constexpr int kLds = W * ST * 2048 * (NT + MT) + stream_areas(W, NT * MT) * (W - 1) * NT * MT * 1024 + W * 256;
-    constexpr int kPerCu = 160 * 1024 / kLds;
     const int64_t tiles_n = (n + 16 * NT - 1) / (16 * NT), tiles_m = (m + 16 * MT - 1) / (16 * MT);
-    const int64_t most = (int64_t)device_cu_count() * kPerCu, tiles = tiles_n * tiles_m;
-    const int grid = (int)(tiles < most ? tiles : most);
-    const int grid_m = (int)(grid / tiles_n), grid_n = (int)(grid % tiles_n);
+    const dim3 grid = grid_of(tiles_n * tiles_m);
     if (out_bf16)
         int8_gemm_stream_kernel<W, NT, MT, true><<<grid, kWave * W, 0, stream>>>(
-            x, xs, w, ws, bias, y, (int)m, (int)n, (int)k, (int)tiles_n, (int)tiles_m, grid_m, grid_n);
+            x, xs, w, ws, bias, y, (int)m, (int)n, (int)k, (int)tiles_n, (int)tiles_m);
     else
         int8_gemm_stream_kernel<W, NT, MT, false><<<grid, kWave * W, 0, stream>>>(
-            x, xs, w, ws, bias, y, (int)m, (int)n, (int)k, (int)tiles_n, (int)tiles_m, grid_m, grid_n);
+            x, xs, w, ws, bias, y, (int)m, (int)n, (int)k, (int)tiles_n, (int)tiles_m);
     return hipGetLastError();
 }
 
