@@ -22,10 +22,12 @@
 // most 32 bits). Outside 2^-100 <= pmax <= 2^100 the row is first multiplied by
 // 2^64 or 2^-64, so that neither 127 / pmax nor a product leaves the fp32
 // range; elements that this flushes are below half a code.
-// silu(gate) up is not an fp32 number. Its fp32 evaluation is within 2^-20 of
-// it (relatively), so the largest magnitude is taken in fp64 over the elements
-// within 2^-18 of the largest fp32 value, and codes whose v is within
-// kNearAct of a half-integer are decided in fp64 (one element in 3000).
+// silu(gate) up is not an fp32 number. Its fp32 evaluation is within 8.4 * 2^-24
+// of it (relatively; the sum of the roundings of exp2, of 1 + e^-a, of the
+// reciprocal, one ulp each for the hardware's, and of four products), so the
+// largest magnitude is taken in fp64 over the elements within 2^-18 of the
+// largest fp32 value, and codes whose v (then within 127 * 11.4 * 2^-24 < 2^-13.5)
+// is within kNearAct of a half-integer are decided in fp64 (one element in 5000).
 //
 // The largest magnitude is an integer maximum of the magnitude patterns: a NaN
 // has the largest pattern, so a row that holds a NaN or an infinity (or whose
@@ -33,9 +35,13 @@
 //
 // gfx950 design. All three stream memory: 3 bytes an element (plain, bf16), 7
 // (norm with residual), 5 (act). A row is held in registers between the
-// reduction and the codes, so every input is read once; a thread takes units
-// of 8 columns (16-byte loads, 8-byte stores), all of its loads are issued before the
-// first is used.
+// reduction and the codes, so every input is read once (rows of more than
+// 16384 columns are read again for the codes); a thread takes units of 8 columns
+// (16-byte loads, 8-byte stores), all of its loads are issued before the first
+// is used. Measured: plain 14336 x 4096 32.1 us (5.5 TB/s), norm with residual
+// 8192 x 4096 43.5 us (5.4 TB/s), both what a copy with that mix of reads and
+// writes takes; act 2048 x 14336 36.2 us (4.1 TB/s; 31.6 without the fp64
+// decisions, which wait for their two values from memory again).
 #include "device.hpp"
 #include "kernels.hpp"
 
@@ -45,7 +51,7 @@ namespace {
 enum Op { kPlain, kNorm, kNormRes, kAct };
 
 constexpr float kNear = 0x1p-14f;
-constexpr float kNearAct = 0x1.4p-13f;
+constexpr float kNearAct = 0x1.ap-14f;
 constexpr uint32_t kInfBits = 0x7F800000u;
 
 // ------------------------------------------------------------ reductions --
@@ -147,16 +153,23 @@ struct Unit<float> {
 
 // silu(g) u in fp32, within 2^-20 of the exact value relatively wherever that
 // is a normal fp32 number: with a = |g|, e^-a = w 2^t, t = ceil(-a log2 e) and
-// w in (0.5, 1] (the argument's rounding error carried in a second word), it is
-// u g / (1 + e^-a) for g >= 0 and u w 2^t g / (1 + e^-a) for g < 0. The power
-// of two joins u last, so neither a very negative gate nor a large `up`
-// overflows on the way. a is capped at 1000 (e^-1000 times any fp32 is 0 in fp32);
-// the factor g keeps NaN and infinity.
+// w in (0.5, 1], it is u g / (1 + e^-a) for g >= 0 and u w 2^t g / (1 + e^-a)
+// for g < 0. The power of two joins u last, so neither a very negative gate nor
+// a large `up` overflows on the way. The exponent's argument takes two words of
+// log2 e: with a bf16 gate the product with the first (16 bits) is exact, with
+// an fp32 gate its rounding error is carried along. a is capped at 1000 (e^-1000
+// times any fp32 is 0 in fp32); the factor g keeps NaN and infinity.
+template <bool kBf16>
 __device__ __forceinline__ float silu_mul(float g, float u) {
     const float a = fminf(fabsf(g), 1000.f);
-    const float kL = -0x1.715476p+0f, kLlo = -0x1.4ae0cp-26f;   // -log2 e in two words
-    const float hi = a * kL;
-    const float lo = fmaf(a, kLlo, fmaf(a, kL, -hi));
+    float hi, lo;
+    if constexpr (kBf16) {
+        hi = a * -0x1.7154p+0f;
+        lo = a * -0x1.d94ae0p-18f;
+    } else {
+        hi = a * -0x1.715476p+0f;
+        lo = fmaf(a, -0x1.4ae0cp-26f, fmaf(a, -0x1.715476p+0f, -hi));
+    }
     const float t = ceilf(hi);
     const float w = __builtin_amdgcn_exp2f((hi - t) + lo);
     const int ti = (int)t;
@@ -173,20 +186,24 @@ __device__ __forceinline__ double silu_mul_f64(double g, double u) { return g / 
 // nearest integer to 127 p / pm, ties to even, from v close to that quotient.
 __device__ __forceinline__ int exact_code(float p, double pm, float v) {
     const int j = (int)fabsf(v);
-    const double d = fma(254.0, (double)fabsf(p), -((double)(2 * j + 1) * pm));   // exact
+    const double d = fma(254.0, (double)fabsf(p), -((double)(2 * j + 1) * pm));   // its sign is exact
     const int q = d > 0.0 ? j + 1 : d < 0.0 ? j : j + (j & 1);
     return p < 0.f ? -q : q;
 }
 
 constexpr float kMagic = 12582912.f;   // 1.5 * 2^23: v + kMagic holds rint(v) in its low bits
 
+// Threads of a workgroup: one row, or four of one wave each.
+constexpr int rows_block(int threads_per_row) { return threads_per_row == kWave ? 4 * kWave : threads_per_row; }
+
 template <typename T, int kOp, int kTpr, int kUnits, bool kLong>
-__global__ __launch_bounds__(kTpr < 256 ? 256 : kTpr) void int8_rows_kernel(
+__global__ __launch_bounds__(rows_block(kTpr)) void int8_rows_kernel(
     const T* __restrict__ x, const T* residual, const T* __restrict__ weight, float eps, T* residual_out,
     int8_t* __restrict__ q, float* __restrict__ scale, int64_t rows, int k) {
-    constexpr int kRowsPerBlock = kTpr < 256 ? 256 / kTpr : 1;
+    constexpr int kRowsPerBlock = rows_block(kTpr) / kTpr;
     constexpr int kWaves = kTpr / kWave;
-    static_assert(kTpr % kWave == 0 && kUnits * 8 <= 64, "row layout");
+    constexpr bool kIsNorm = kOp == kNorm || kOp == kNormRes;
+    static_assert(kTpr % kWave == 0, "whole waves");
     const int t = kRowsPerBlock > 1 ? threadIdx.x % kTpr : threadIdx.x;
     const int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
     const int64_t row = block * kRowsPerBlock + (kRowsPerBlock > 1 ? threadIdx.x / kTpr : 0);
@@ -198,30 +215,35 @@ __global__ __launch_bounds__(kTpr < 256 ? 256 : kTpr) void int8_rows_kernel(
     int8_t* qr = q + row * (int64_t)k;
 
     float p[kUnits][8];
-    uint32_t m = 0;        // largest magnitude pattern
+    // largest patterns with the sign bit (as unsigned numbers: the largest magnitude among the negative values, NaN
+    // above all) and without (as signed numbers: among the others)
+    uint32_t mneg = 0;
+    int32_t mpos = 0;
     double ss = 0.0;       // sum of squares of h
     constexpr int span = kTpr * kUnits;   // units a pass of the threads covers
 
-    // p of the units base + t, base + t + kTpr, ...; zero past the row's end
+    // p of the units base + t, base + t + kTpr, ... A thread past the row's end repeats the row's last unit
+    // (which changes no maximum) and stores nothing.
     auto fetch = [&](int base, bool first) __attribute__((always_inline)) {
         Unit<T> a[kUnits], b[kUnits], c[kUnits];
 #pragma unroll
         for (int j = 0; j < kUnits; ++j) {
-            const int u = base + t + j * kTpr;
-            const int at = 8 * (u < units ? u : units - 1);   // past the end: read again, not used
+            if (j > 0 && base + j * kTpr >= units) continue;   // uniform: the whole pass is past the end
+            const int at = 8 * min(base + t + j * kTpr, units - 1);
             a[j].load(xr + at);
             if constexpr (kOp == kAct) b[j].load(xr + k + at);
             if constexpr (kOp == kNormRes) b[j].load(rr + at);
-            if constexpr (kOp == kNorm || kOp == kNormRes) c[j].load(weight + at);
+            if constexpr (kIsNorm) c[j].load(weight + at);
         }
 #pragma unroll
         for (int j = 0; j < kUnits; ++j) {
+            if (j > 0 && base + j * kTpr >= units) continue;
             const int u = base + t + j * kTpr;
             const bool live = u < units;
             float va[8], vb[8], vc[8];
             a[j].get(va);
             if constexpr (kOp == kAct || kOp == kNormRes) b[j].get(vb);
-            if constexpr (kOp == kNorm || kOp == kNormRes) c[j].get(vc);
+            if constexpr (kIsNorm) c[j].get(vc);
             if constexpr (kOp == kNormRes) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) va[i] += vb[i];
@@ -229,19 +251,19 @@ __global__ __launch_bounds__(kTpr < 256 ? 256 : kTpr) void int8_rows_kernel(
                 // a long row reads it twice and writes on the second pass
                 if (live && first != kLong) Unit<T>::put(hr + 8 * u, va);
             }
+            double s = 0.0;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                float v = va[i];
-                if constexpr (kOp == kAct) v = silu_mul(va[i], vb[i]);
-                if constexpr (kOp == kNorm || kOp == kNormRes) v = va[i] * vc[i];
-                p[j][i] = live ? v : 0.f;
+                if constexpr (kOp == kAct) p[j][i] = silu_mul<sizeof(T) == 2>(va[i], vb[i]);
+                else p[j][i] = kIsNorm ? va[i] * vc[i] : va[i];
+                if constexpr (kIsNorm) s = fma((double)va[i], (double)va[i], s);
                 if (first) {
-                    m = max(m, __float_as_uint(p[j][i]) & 0x7FFFFFFFu);
-                    if constexpr (kOp == kNorm || kOp == kNormRes) {
-                        const double h = live ? (double)va[i] : 0.0;
-                        ss = fma(h, h, ss);
-                    }
+                    mneg = max(mneg, __float_as_uint(p[j][i]));
+                    mpos = max(mpos, __float_as_int(p[j][i]));
                 }
+            }
+            if constexpr (kIsNorm) {
+                if (first && live) ss += s;
             }
         }
     };
@@ -252,29 +274,38 @@ __global__ __launch_bounds__(kTpr < 256 ? 256 : kTpr) void int8_rows_kernel(
         fetch(0, true);
     }
 
-    m = wave_max_u32(m);
-    if constexpr (kOp == kNorm || kOp == kNormRes) ss = wave_sum_f64(ss);
+    // the thread's largest magnitude pattern, then the row's
+    const uint32_t mine = max(mneg > 0x7FFFFFFFu ? mneg & 0x7FFFFFFFu : 0u, (uint32_t)mpos);
+    uint32_t m = wave_max_u32(mine);
+    if constexpr (kIsNorm) ss = wave_sum_f64(ss);
     if constexpr (kWaves > 1) {
         __shared__ uint32_t wm[kWaves];
-        __shared__ double wss[kWaves];
+        __shared__ double wss[kIsNorm ? kWaves : 1];
         const int lane = t % kWave;
         if (lane == 0) {
             wm[t / kWave] = m;
-            wss[t / kWave] = ss;
+            if constexpr (kIsNorm) wss[t / kWave] = ss;
         }
         __syncthreads();
         m = wm[lane % kWaves];
 #pragma unroll
         for (int d = kWaves / 2; d > 0; d >>= 1) m = max(m, (uint32_t)__shfl_xor(m, d, kWave));
-        if constexpr (kOp == kNorm || kOp == kNormRes) {
+        if constexpr (kIsNorm) {
             ss = wss[lane % kWaves];
 #pragma unroll
             for (int d = kWaves / 2; d > 0; d >>= 1) ss += shfl_f64(ss, d);
         }
     }
 
-    const bool bad = m >= kInfBits, zero = m == 0;   // row-uniform, as all that follows
+    // row-uniform from here on
     const float top = __uint_as_float(m);
+    if (m >= kInfBits || m == 0) {   // non-finite, or all zero
+        if constexpr (kOp == kNormRes && kLong)   // h is still to be written
+            for (int base = 0; base < units; base += span) fetch(base, false);
+        for (int u = t; u < units; u += kTpr) *reinterpret_cast<uint2*>(qr + 8 * u) = make_uint2(0u, 0u);
+        if (t == 0) scale[row] = m == 0 ? 0.f : __uint_as_float(0x7FC00000u);
+        return;
+    }
     // rows outside the range where fl32 steps are safe are multiplied by a power of two first
     const float pre = top > 0x1p100f ? 0x1p-64f : top < 0x1p-100f ? 0x1p64f : 1.f;
 
@@ -282,24 +313,28 @@ __global__ __launch_bounds__(kTpr < 256 ? 256 : kTpr) void int8_rows_kernel(
     double pm = (double)(top * pre);
     double pm_act = 0.0;
     const bool tiny = kOp == kAct && top < 0x1p-60f;   // fp32 values may be subnormal: every element in fp64
+    // |silu(gate) up| of the unit's elements whose bit is set in mask
+    auto largest = [&](int u, uint32_t mask) __attribute__((always_inline)) {
+        while (mask != 0) {
+            const int c = 8 * u + __builtin_ctz(mask);
+            mask &= mask - 1;
+            pm_act = fmax(pm_act, fabs(silu_mul_f64(Unit<T>::one(xr + c), Unit<T>::one(xr + k + c))));
+        }
+    };
     if constexpr (kOp == kAct) {
         const float near = tiny ? 0.f : top * (1.f - 0x1p-18f);
         auto scan = [&](int base) __attribute__((always_inline)) {
-            uint64_t mask = 0;
 #pragma unroll
-            for (int j = 0; j < kUnits; ++j)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) mask |= (uint64_t)(fabsf(p[j][i]) >= near) << (8 * j + i);
-            while (mask != 0) {
-                const int b = __builtin_ctzll(mask);
-                mask &= mask - 1;
-                const int u = base + t + (b >> 3) * kTpr;
+            for (int j = 0; j < kUnits; ++j) {
+                const int u = base + t + j * kTpr;
                 if (u >= units) continue;
-                const int c = 8 * u + (b & 7);
-                pm_act = fmax(pm_act, fabs(silu_mul_f64(Unit<T>::one(xr + c), Unit<T>::one(xr + k + c))));
+                uint32_t mask = 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) mask |= (uint32_t)(fabsf(p[j][i]) >= near) << i;
+                largest(u, mask);
             }
         };
-        if (!bad && !zero) {
+        if (__uint_as_float(mine) >= near) {   // few threads have such an element
             if constexpr (kLong) {
                 for (int base = 0; base < units; base += span) {
                     fetch(base, false);
@@ -324,32 +359,30 @@ __global__ __launch_bounds__(kTpr < 256 ? 256 : kTpr) void int8_rows_kernel(
 
     if (t == 0) {
         double s;
-        if (bad) s = (double)__uint_as_float(0x7FC00000u);
-        else if (zero) s = 0.0;
-        else if constexpr (kOp == kAct) s = pm_act / 127.0;
+        if constexpr (kOp == kAct) s = pm_act / 127.0;
         else if constexpr (kOp == kPlain) s = (double)top / 127.0;
         else s = (double)top / (127.0 * sqrt(ss / (double)k + (double)eps));
         scale[row] = (float)s;
     }
 
-    const bool flat = bad || zero;
-    const float inv = flat ? 0.f : 127.f / (float)pm;
+    const float inv = 127.f / (float)pm;
     auto codes = [&](int base) __attribute__((always_inline)) {
-        uint64_t mask = 0;
 #pragma unroll
         for (int j = 0; j < kUnits; ++j) {
             const int u = base + t + j * kTpr;
+            if (u >= units) continue;
+            if (pre != 1.f) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) p[j][i] *= pre;
+            }
             uint32_t c[8];
             float off = 0.f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                p[j][i] = flat ? 0.f : p[j][i] * pre;
                 const float v = p[j][i] * inv;
                 const float z = v + kMagic;
-                const float d = fabsf(v - (z - kMagic));
+                off = fmaxf(off, fabsf(v - (z - kMagic)));
                 c[i] = __float_as_uint(z);
-                if constexpr (kOp == kAct) mask |= (uint64_t)(d > 0.5f - kNearAct || tiny) << (8 * j + i);
-                else off = fmaxf(off, d);
             }
             if constexpr (kOp != kAct) {
                 if (off > 0.5f - kNear) {
@@ -362,18 +395,22 @@ __global__ __launch_bounds__(kTpr < 256 ? 256 : kTpr) void int8_rows_kernel(
                                                       __builtin_amdgcn_perm(c[1], c[0], 0x0C0C0400u), 0x05040100u);
             const uint32_t hi = __builtin_amdgcn_perm(__builtin_amdgcn_perm(c[7], c[6], 0x0C0C0400u),
                                                       __builtin_amdgcn_perm(c[5], c[4], 0x0C0C0400u), 0x05040100u);
-            if (u < units) *reinterpret_cast<uint2*>(qr + 8 * u) = make_uint2(lo, hi);
-        }
-        if constexpr (kOp == kAct) {
-            if (flat) return;
-            while (mask != 0) {   // codes near a border: the same thread writes the byte again
-                const int b = __builtin_ctzll(mask);
-                mask &= mask - 1;
-                const int u = base + t + (b >> 3) * kTpr;
-                if (u >= units) continue;
-                const int c = 8 * u + (b & 7);
-                const double v = silu_mul_f64(Unit<T>::one(xr + c), Unit<T>::one(xr + k + c)) * 127.0 / pm_act;
-                qr[c] = (int8_t)(int)rint(v);
+            *reinterpret_cast<uint2*>(qr + 8 * u) = make_uint2(lo, hi);
+            if constexpr (kOp == kAct) {
+                if (off > 0.5f - kNearAct || tiny) {   // codes near a border: the byte is written again
+                    uint32_t mask = 0;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float v = p[j][i] * inv;
+                        mask |= (uint32_t)(fabsf(v - rintf(v)) > 0.5f - kNearAct || tiny) << i;
+                    }
+                    while (mask != 0) {
+                        const int e = 8 * u + __builtin_ctz(mask);
+                        mask &= mask - 1;
+                        const double P = silu_mul_f64(Unit<T>::one(xr + e), Unit<T>::one(xr + k + e));
+                        qr[e] = (int8_t)(int)rint(P * 127.0 / pm_act);
+                    }
+                }
             }
         }
     };
@@ -392,11 +429,11 @@ constexpr int64_t kGridX = 1 << 20;   // times 1024 threads: below the 2^32 of a
 template <typename T, int kOp, int kTpr, int kUnits, bool kLong>
 void launch_rows(const T* x, const T* residual, const T* weight, float eps, T* residual_out, int8_t* q, float* scale,
                  int64_t rows, int64_t k, hipStream_t stream) {
-    constexpr int kRowsPerBlock = kTpr < 256 ? 256 / kTpr : 1;
+    constexpr int kRowsPerBlock = rows_block(kTpr) / kTpr;
     const int64_t blocks = (rows + kRowsPerBlock - 1) / kRowsPerBlock;
     const int64_t gx = blocks < kGridX ? blocks : kGridX;
     const dim3 grid((unsigned)gx, (unsigned)((blocks + gx - 1) / gx));
-    int8_rows_kernel<T, kOp, kTpr, kUnits, kLong><<<grid, kTpr < 256 ? 256 : kTpr, 0, stream>>>(
+    int8_rows_kernel<T, kOp, kTpr, kUnits, kLong><<<grid, rows_block(kTpr), 0, stream>>>(
         x, residual, weight, eps, residual_out, q, scale, rows, (int)k);
 }
 
@@ -410,18 +447,28 @@ hipError_t dispatch(const void* xv, const void* resv, const void* wv, float eps,
     const int64_t units = k / 8;
 #define E2M1_ROWS(TPR, UNITS, LONG) \
     launch_rows<T, kOp, TPR, UNITS, LONG>(x, r, w, eps, h, q, scale, rows, k, stream)
-    if (units <= 64 * 4 && rows >= 1024) {
-        if (units <= 64) E2M1_ROWS(64, 1, false);
-        else if (units <= 128) E2M1_ROWS(64, 2, false);
-        else E2M1_ROWS(64, 4, false);
+    // Few elements: as many threads a row as it has units, for the latency. Many: two units or more a thread, for
+    // the bytes in flight. (bf16, us, the one against the other: norm with residual, k 4096, 512 rows 5.4 / 5.5, 2000
+    // rows 12.6 / 12.3; plain, 14336 x 4096, 43.1 / 34.6; k 8192, 512 rows 5.5 / 5.4, 2000 rows 15.7 / 12.8; act,
+    // k 14336, 512 rows 12.5 / 13.1, 2000 rows 37.7 / 34.8; k 1024, 2000 rows 4.0 / 4.1, 20000 rows 16.3 / 14.8.)
+    const bool many = rows * k >= (int64_t)6 << 20;
+    if (units <= 64) {
+        E2M1_ROWS(64, 1, false);
+    } else if (units <= 128) {
+        if (many) E2M1_ROWS(64, 2, false);
+        else E2M1_ROWS(128, 1, false);
     } else if (units <= 256) {
-        E2M1_ROWS(256, 1, false);
+        if (many) E2M1_ROWS(128, 2, false);
+        else E2M1_ROWS(256, 1, false);
     } else if (units <= 512) {
-        E2M1_ROWS(512, 1, false);
+        if (many) E2M1_ROWS(256, 2, false);
+        else E2M1_ROWS(512, 1, false);
     } else if (units <= 1024) {
-        E2M1_ROWS(1024, 1, false);
+        if (many) E2M1_ROWS(512, 2, false);
+        else E2M1_ROWS(1024, 1, false);
     } else if (units <= 2048) {
-        E2M1_ROWS(1024, 2, false);
+        if (many) E2M1_ROWS(512, 4, false);
+        else E2M1_ROWS(1024, 2, false);
     } else {
         E2M1_ROWS(1024, 2, true);
     }

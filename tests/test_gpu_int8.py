@@ -71,10 +71,11 @@ def normal_rows(rows: int, k: int, seed: int) -> np.ndarray:
     return r.standard_normal((rows, k)) * 2.0 ** r.integers(-20, 20, (rows, 1))
 
 
-# Every row layout: one wave a row with one, two and four units a lane, one workgroup of each size, the
-# form that reads a row twice; ragged widths in each.
+# Every row layout: one wave a row, one workgroup of each size with one, two and four units a thread (the last six
+# shapes are large enough for more units a thread), the form that reads a row twice; ragged widths in each.
 SHAPES = [(1, 16), (3, 48), (1030, 496), (1025, 1008), (1027, 2032), (1024, 2048), (5, 2064), (2, 4096), (9, 2880),
-          (3, 4112), (2, 8192), (1100, 4096), (2, 14336), (1, 16384), (2, 16400), (3, 40000), (1, 131072)]
+          (3, 4112), (2, 8192), (1100, 4096), (2, 14336), (1, 16384), (2, 16400), (3, 40000), (1, 131072), (6301, 1008), (3100, 2032), (1700, 4080), (800, 8176), (450, 14336),
+          (385, 16384)]
 
 
 def check_quantize(g, a: np.ndarray, dtype: str):
