@@ -222,8 +222,8 @@ __global__ __launch_bounds__(rows_block(kTpr)) void int8_rows_kernel(
     double ss = 0.0;       // sum of squares of h
     constexpr int span = kTpr * kUnits;   // units a pass of the threads covers
 
-    // p of the units base + t, base + t + kTpr, ... A thread past the row's end repeats the row's last unit
-    // (which changes no maximum) and stores nothing.
+    // p of the units base + t, base + t + kTpr, ... A thread past the row's end repeats the row's last unit (which
+    // changes no maximum) and stores nothing; with a residual, whose last unit may be overwritten by then, its p are 0.
     auto fetch = [&](int base, bool first) __attribute__((always_inline)) {
         Unit<T> a[kUnits], b[kUnits], c[kUnits];
 #pragma unroll
@@ -256,6 +256,7 @@ __global__ __launch_bounds__(rows_block(kTpr)) void int8_rows_kernel(
             for (int i = 0; i < 8; ++i) {
                 if constexpr (kOp == kAct) p[j][i] = silu_mul<sizeof(T) == 2>(va[i], vb[i]);
                 else p[j][i] = kIsNorm ? va[i] * vc[i] : va[i];
+                if constexpr (kOp == kNormRes) p[j][i] = live ? p[j][i] : 0.f;
                 if constexpr (kIsNorm) s = fma((double)va[i], (double)va[i], s);
                 if (first) {
                     mneg = max(mneg, __float_as_uint(p[j][i]));
