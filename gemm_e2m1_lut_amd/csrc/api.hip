@@ -261,7 +261,7 @@ int int8_gemm(const int8_t* x, const float* x_scale, const int8_t* w, const floa
               void* y, int y_dtype, int64_t m, int64_t n, int64_t k, void* stream) {
     if (y_dtype != E2M1_DTYPE_F32 && y_dtype != E2M1_DTYPE_BF16) return E2M1_ERR_DTYPE;
     if (m < 0 || n < 0 || k < 0 || k % 16 != 0 || k > E2M1_INT8_MAX_K || m > INT_MAX - 255 || n > INT_MAX - 255 ||
-        !mul_ok(m, 4 * n))
+        m * n > E2M1_INT8_MAX_OUTPUTS)
         return E2M1_ERR_SHAPE;
     if (m == 0 || n == 0) return E2M1_OK;
     if (!y || !x_scale || !w_scale || (k > 0 && (!x || !w))) return E2M1_ERR_NULL;

@@ -72,7 +72,7 @@ __device__ __forceinline__ void wait_vm() {
 // This wave's LDS accesses are done.
 __device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
-// `tiles` workgroups in rows of 2^20 (a grid dimension holds fewer than 2^32 threads).
+// `tiles` workgroups (below 2^32) in rows of 2^20 (a grid dimension holds fewer than 2^32 threads).
 dim3 grid_of(int64_t tiles) {
     const int64_t gx = tiles < (1 << 20) ? tiles : 1 << 20;
     return dim3((unsigned)gx, (unsigned)((tiles + gx - 1) / gx));
@@ -256,11 +256,17 @@ constexpr int kXcds = 8;
 
 constexpr int KS = 128;   // columns per step: two slices (64-byte row segments read at half the L2 rate)
 
+template <int kWN, int kWM, int TN, int TM, int NS>
+constexpr int tile_lds_bytes() {
+    return NS * 16 * (TN * kWN + TM * kWM) * KS;
+}
+
+// The tile from row n0 of w and row m0 of x on.
 template <int kWN, int kWM, int TN, int TM, int NS, bool kBf16Out>
-__global__ __launch_bounds__(kWave * kWN * kWM) void int8_gemm_tile_kernel(
-    const int8_t* __restrict__ x, const float* __restrict__ xs, const int8_t* __restrict__ w,
-    const float* __restrict__ ws, const float* __restrict__ bias, void* __restrict__ y, int m, int n, int k,
-    int64_t tiles, int group_m) {
+__device__ __forceinline__ void tile_body(uint8_t* lds, const int8_t* __restrict__ x, const float* __restrict__ xs,
+                                          const int8_t* __restrict__ w, const float* __restrict__ ws,
+                                          const float* __restrict__ bias, void* __restrict__ y, int m, int n, int k,
+                                          int n0, int m0) {
     constexpr int kWaves = kWN * kWM;
     constexpr int NR = 16 * TN * kWN, MR = 16 * TM * kWM;
     constexpr int kWLoads = NR / 8 / kWaves, kXLoads = MR / 8 / kWaves;   // 1 KB requests (8 rows) per wave and step
@@ -269,21 +275,6 @@ __global__ __launch_bounds__(kWave * kWN * kWM) void int8_gemm_tile_kernel(
     constexpr int kBufBytes = (NR + MR) * KS;
     constexpr int kOutBytes = 16 * 16 * TN * 4;                           // a wave's band of sums
     static_assert(kWaves * kOutBytes <= NS * kBufBytes && NS * kBufBytes <= 160 * 1024, "LDS");
-    __shared__ __attribute__((aligned(256))) uint8_t lds[NS * kBufBytes];
-
-    // workgroup id -> tile: ids go round the XCDs, and each XCD gets a run of neighbouring tiles
-    // (group_m tiles along x, then along w), which share their operands in its L2
-    const int64_t per = (tiles + kXcds - 1) / kXcds;
-    const int64_t id = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
-    const int64_t tile = id % kXcds * per + id / kXcds;
-    if (id / kXcds >= per || tile >= tiles) return;   // the whole workgroup
-    const int tn = (n + NR - 1) / NR, tm = (m + MR - 1) / MR;
-    const int64_t band = (int64_t)group_m * tn;
-    const int mfirst = (int)(tile / band) * group_m;
-    const int msize = min(group_m, tm - mfirst);
-    const int n0 = (int)(tile % band / msize) * NR;
-    const int m0 = (mfirst + (int)(tile % band % msize)) * MR;
-
     const int lane = threadIdx.x % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int r = lane & 15, g = lane >> 4;
@@ -418,19 +409,103 @@ __global__ __launch_bounds__(kWave * kWN * kWM) void int8_gemm_tile_kernel(
     }
 }
 
+// Tiles along x that workgroups of one XCD take before they go on along w.
+constexpr int kBand = 4;
+
+// First rows of tile `tile` (rows_w x rows_x of them each), numbered along x inside bands of kBand tiles, then along w.
+__device__ __forceinline__ void tile_rows(uint32_t tile, int m, int n, int rows_w, int rows_x, int& n0, int& m0) {
+    const uint32_t tn = (uint32_t)(n + rows_w - 1) / (uint32_t)rows_w, tm = (uint32_t)(m + rows_x - 1) / (uint32_t)rows_x;
+    const uint32_t band = tile / (kBand * tn), in = tile - band * (kBand * tn);
+    const uint32_t size = min((uint32_t)kBand, tm - band * kBand);
+    n0 = __builtin_amdgcn_readfirstlane(in / size * (uint32_t)rows_w);
+    m0 = __builtin_amdgcn_readfirstlane((band * kBand + in % size) * (uint32_t)rows_x);
+}
+
+// Workgroup id -> number: ids go round the XCDs, and each XCD gets a run of neighbouring numbers, whose tiles share
+// operands in its L2. Not below count: no work.
+__device__ __forceinline__ uint32_t xcd_number(uint32_t id, uint32_t count) {
+    const uint32_t per = (count + kXcds - 1) / kXcds;
+    return id / kXcds < per ? id % kXcds * per + id / kXcds : count;
+}
+
+template <int kWN, int kWM, int TN, int TM, int NS, bool kBf16Out>
+__global__ __launch_bounds__(kWave * kWN * kWM) void int8_gemm_tile_kernel(
+    const int8_t* __restrict__ x, const float* __restrict__ xs, const int8_t* __restrict__ w,
+    const float* __restrict__ ws, const float* __restrict__ bias, void* __restrict__ y, int m, int n, int k,
+    uint32_t tiles) {
+    __shared__ __attribute__((aligned(256))) uint8_t lds[tile_lds_bytes<kWN, kWM, TN, TM, NS>()];
+    const uint32_t tile = xcd_number(blockIdx.y * gridDim.x + blockIdx.x, tiles);
+    if (tile >= tiles) return;   // the whole workgroup
+    int n0, m0;
+    tile_rows(tile, m, n, 16 * TN * kWN, 16 * TM * kWM, n0, m0);
+    tile_body<kWN, kWM, TN, TM, NS, kBf16Out>(lds, x, xs, w, ws, bias, y, m, n, k, n0, m0);
+}
+
+// 256 x 256 tiles whose last round would leave at least half of the compute units idle: the last tiles, those from
+// `whole` on, as two halves of 256 x 128 each. 2048 x 28672 x 4096 (896 tiles on 256 compute units): 239 us with
+// whole tiles, 219 with 128 of them halved.
+template <bool kBf16Out>
+__global__ __launch_bounds__(512) void int8_gemm_mixed_kernel(
+    const int8_t* __restrict__ x, const float* __restrict__ xs, const int8_t* __restrict__ w,
+    const float* __restrict__ ws, const float* __restrict__ bias, void* __restrict__ y, int m, int n, int k,
+    uint32_t tiles, uint32_t whole) {
+    constexpr int kLds = tile_lds_bytes<2, 4, 8, 4, 2>() > tile_lds_bytes<4, 2, 4, 4, 3>()
+                             ? tile_lds_bytes<2, 4, 8, 4, 2>() : tile_lds_bytes<4, 2, 4, 4, 3>();
+    __shared__ __attribute__((aligned(256))) uint8_t lds[kLds];
+    const uint32_t id = blockIdx.y * gridDim.x + blockIdx.x;
+    const uint32_t ids = (whole + kXcds - 1) / kXcds * kXcds;   // of the whole tiles
+    int n0, m0;
+    if (id < ids) {
+        const uint32_t tile = xcd_number(id, whole);
+        if (tile >= whole) return;   // the whole workgroup
+        tile_rows(tile, m, n, 256, 256, n0, m0);
+        tile_body<2, 4, 8, 4, 2, kBf16Out>(lds, x, xs, w, ws, bias, y, m, n, k, n0, m0);
+    } else {
+        const uint32_t half = xcd_number(id - ids, 2 * (tiles - whole));
+        if (half >= 2 * (tiles - whole)) return;
+        tile_rows(whole + half / 2, m, n, 256, 256, n0, m0);
+        m0 += 128 * (int)(half % 2);
+        if (m0 >= m) return;
+        tile_body<4, 2, 4, 4, 3, kBf16Out>(lds, x, xs, w, ws, bias, y, m, n, k, n0, m0);
+    }
+}
+
 template <int kWN, int kWM, int TN, int TM, int NS>
 hipError_t launch_tile(const int8_t* x, const float* xs, const int8_t* w, const float* ws, const float* bias, void* y,
                        bool out_bf16, int64_t m, int64_t n, int64_t k, hipStream_t stream) {
     constexpr int NR = 16 * TN * kWN, MR = 16 * TM * kWM;
     const int64_t tiles = ((n + NR - 1) / NR) * ((m + MR - 1) / MR);
     const dim3 grid = grid_of((tiles + kXcds - 1) / kXcds * kXcds);
-    constexpr int kGroupM = 4;
     if (out_bf16)
         int8_gemm_tile_kernel<kWN, kWM, TN, TM, NS, true>
-            <<<grid, kWave * kWN * kWM, 0, stream>>>(x, xs, w, ws, bias, y, (int)m, (int)n, (int)k, tiles, kGroupM);
+            <<<grid, kWave * kWN * kWM, 0, stream>>>(x, xs, w, ws, bias, y, (int)m, (int)n, (int)k, (uint32_t)tiles);
     else
         int8_gemm_tile_kernel<kWN, kWM, TN, TM, NS, false>
-            <<<grid, kWave * kWN * kWM, 0, stream>>>(x, xs, w, ws, bias, y, (int)m, (int)n, (int)k, tiles, kGroupM);
+            <<<grid, kWave * kWN * kWM, 0, stream>>>(x, xs, w, ws, bias, y, (int)m, (int)n, (int)k, (uint32_t)tiles);
+    return hipGetLastError();
+}
+
+// Whether the last of several rounds of 256 x 256 tiles fills at most half of the compute units.
+bool halves_last_round(int64_t tiles, int64_t cus) {
+    return tiles > cus && tiles % cus != 0 && 2 * (tiles % cus) <= cus;
+}
+
+// 256 x 256 tiles, such a last round's halved.
+hipError_t launch_largest(const int8_t* x, const float* xs, const int8_t* w, const float* ws, const float* bias,
+                          void* y, bool out_bf16, int64_t m, int64_t n, int64_t k, hipStream_t stream) {
+    const int64_t tiles = ((n + 255) / 256) * ((m + 255) / 256), cus = device_cu_count();
+    const int64_t rest = tiles % cus, whole = tiles - rest;
+    if (!halves_last_round(tiles, cus))
+        return launch_tile<2, 4, 8, 4, 2>(x, xs, w, ws, bias, y, out_bf16, m, n, k, stream);
+    const dim3 grid = grid_of((whole + kXcds - 1) / kXcds * kXcds + (2 * rest + kXcds - 1) / kXcds * kXcds);
+    if (out_bf16)
+        int8_gemm_mixed_kernel<true>
+            <<<grid, 512, 0, stream>>>(x, xs, w, ws, bias, y, (int)m, (int)n, (int)k, (uint32_t)tiles,
+                                      (uint32_t)whole);
+    else
+        int8_gemm_mixed_kernel<false>
+            <<<grid, 512, 0, stream>>>(x, xs, w, ws, bias, y, (int)m, (int)n, (int)k, (uint32_t)tiles,
+                                      (uint32_t)whole);
     return hipGetLastError();
 }
 
@@ -451,8 +526,8 @@ const Shape kShapes[] = {
     {64, 64, 3.2f, 0.20f, launch_tile<2, 2, 2, 2, 8>},
     {64, 128, 5.0f, 0.33f, launch_tile<2, 2, 2, 4, 6>},
     {128, 128, 7.0f, 0.53f, launch_tile<2, 2, 4, 4, 4>},
-    {256, 128, 8.0f, 0.80f, launch_tile<4, 2, 4, 4, 3>},
-    {256, 256, 12.0f, 1.40f, launch_tile<2, 4, 8, 4, 2>},
+    {256, 128, 8.0f, 0.80f, launch_tile<4, 2, 4, 4, 3>},   // and the halves of the last shape's last round
+    {256, 256, 12.0f, 1.40f, launch_largest},
 };
 
 }  // namespace
@@ -466,7 +541,9 @@ hipError_t launch_int8_gemm(const int8_t* x, const float* x_scale, const int8_t*
     float best_us = 0.f;
     for (const Shape& s : kShapes) {
         const int64_t tiles = ((n + s.rows_w - 1) / s.rows_w) * ((m + s.rows_x - 1) / s.rows_x);
-        const float us = (float)((tiles + cus - 1) / cus) * (s.round_us + steps * s.step_us);
+        float us = (float)((tiles + cus - 1) / cus) * (s.round_us + steps * s.step_us);
+        if (s.launch == launch_largest && halves_last_round(tiles, cus))   // by the shape before it
+            us -= s.round_us + steps * s.step_us - (kShapes[6].round_us + steps * kShapes[6].step_us);
         if (best == nullptr || us < best_us) {
             best = &s;
             best_us = us;

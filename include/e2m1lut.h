@@ -292,10 +292,11 @@ int silu_mul_int8_quantize(const void* gate_up, int dtype, int8_t* q, float* sca
  *   y        [m, n], fp32 (y_dtype = E2M1_DTYPE_F32) or bf16 bit patterns
  *            (E2M1_DTYPE_BF16), overwritten; aligned to its elements (rows
  *            that start 16-byte aligned are stored widest)
- * Requires 0 <= m, n <= 2^31 - 256, k >= 0, k % 16 == 0, k <= E2M1_INT8_MAX_K
- * (sums stay below 2^31). k == 0 gives the bias, or zeros.
+ * Requires 0 <= m, n <= 2^31 - 256, m n <= E2M1_INT8_MAX_OUTPUTS, k >= 0, k % 16 == 0,
+ * k <= E2M1_INT8_MAX_K (sums stay below 2^31). k == 0 gives the bias, or zeros.
  */
 #define E2M1_INT8_MAX_K 131056
+#define E2M1_INT8_MAX_OUTPUTS ((int64_t)1 << 39)
 int int8_gemm(const int8_t* x, const float* x_scale, const int8_t* w, const float* w_scale, const float* bias,
               void* y, int y_dtype, int64_t m, int64_t n, int64_t k, void* stream);
 

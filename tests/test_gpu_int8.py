@@ -299,6 +299,7 @@ GEMM_SHAPES = [
     (17, 31, 80), (31, 97, 528), (33, 64, 512), (64, 256, 1024), (65, 129, 2896), (100, 48, 4112), (128, 128, 128),
     (130, 1003, 1040), (255, 257, 272), (256, 256, 384), (257, 511, 640), (300, 2881, 1536), (513, 770, 2880),
     (1000, 300, 16), (700, 1030, 4096), (4099, 65, 96), (20, 8200, 160),
+    (4100, 4100, 1040),   # more largest tiles than compute units, the last round's halved
 ]
 
 

@@ -114,6 +114,7 @@ def test_int8_gemm_validation(lib):
     assert call(m=-1) == E_SHAPE
     assert call(n=2**31) == E_SHAPE
     assert call(m=2**31) == E_SHAPE
+    assert call(m=2**30, n=2**30) == E_SHAPE   # more outputs than any memory holds
     assert call(m=0, x=NULL, xs=NULL, y=NULL) == E2M1_OK
     assert call(n=0, w=NULL, ws=NULL, y=NULL) == E2M1_OK
     for arg in ("x", "xs", "w", "ws", "y"):
