@@ -397,7 +397,7 @@ def rmsnorm_int8_quantize(x: torch.Tensor, weight: torch.Tensor, eps: float, res
 
 def silu_mul_int8_quantize(gate_up: torch.Tensor, out: tuple[torch.Tensor, torch.Tensor] | None = None,
                            stream=None) -> tuple[torch.Tensor, torch.Tensor]:
-    """bf16 or fp32 [rows, 2 inter], gate then up -> codes int8 [rows, inter] and scale fp32 [rows] of silu(gate) * up."""
+    """bf16 or fp32 [rows, 2 inter], gate then up -> int8 [rows, inter] and fp32 [rows] of silu(gate) * up."""
     rows, both, code, device = _float_rows(gate_up, "gate_up")
     if both % 2 != 0:
         raise ValueError(f"gate_up has {both} columns, expected gate and up of one width")

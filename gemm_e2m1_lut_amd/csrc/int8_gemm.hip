@@ -193,7 +193,7 @@ __global__ __launch_bounds__(kWave * W) void int8_gemm_stream_kernel(
             const int block = i * MT + j;
             if (wave == block) sum = acc[i][j];
             else
-                *reinterpret_cast<i32x4*>(part + 1024 * (block * (W - 1) + (wave < block ? wave : wave - 1))) = acc[i][j];
+                *reinterpret_cast<i32x4*>(part + 1024 * (block * (W - 1) + wave - (wave > block))) = acc[i][j];
         }
     wait_vm<0>();   // the requests past the last step have landed before the workgroup's LDS is released
     wait_lds();
@@ -257,8 +257,8 @@ constexpr int kXcds = 8;
 constexpr int KS = 128;   // columns per step: two slices (64-byte row segments read at half the L2 rate)
 
 template <int kWN, int kWM, int TN, int TM, int NS>
-constexpr int tile_lds_bytes() {
-    return NS * 16 * (TN * kWN + TM * kWM) * KS;
+constexpr int tile_lds_bytes() {   // the ring; w_scale, bias and x_scale of the tile's rows
+    return NS * 16 * (TN * kWN + TM * kWM) * KS + 4 * 16 * (2 * TN * kWN + TM * kWM);
 }
 
 // The tile from row n0 of w and row m0 of x on.
@@ -274,7 +274,8 @@ __device__ __forceinline__ void tile_body(uint8_t* lds, const int8_t* __restrict
     static_assert(kWLoads * 8 * kWaves == NR && kXLoads * 8 * kWaves == MR, "requests");
     constexpr int kBufBytes = (NR + MR) * KS;
     constexpr int kOutBytes = 16 * 16 * TN * 4;                           // a wave's band of sums
-    static_assert(kWaves * kOutBytes <= NS * kBufBytes && NS * kBufBytes <= 160 * 1024, "LDS");
+    static_assert(kWaves * kOutBytes <= NS * kBufBytes && tile_lds_bytes<kWN, kWM, TN, TM, NS>() <= 160 * 1024, "LDS");
+    static_assert(NR % kWave == 0 && MR % kWave == 0, "scales: whole requests");
     const int lane = threadIdx.x % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int r = lane & 15, g = lane >> 4;
@@ -300,6 +301,18 @@ __device__ __forceinline__ void tile_body(uint8_t* lds, const int8_t* __restrict
         xoff[i] = (uint32_t)(8 * (kXLoads * wave + i) + lane / 8) * (uint32_t)k + (uint32_t)xcol(i);
     const uint32_t base = (uint32_t)(uintptr_t)&lds[0];
     const int steps = (k + KS - 1) / KS;
+
+    // w_scale [NR], bias [NR], x_scale [MR]: requested like the operands and before them, so landed with the first
+    // step (loads in the epilogue would wait for its stores: their count is one)
+    float* const factors = reinterpret_cast<float*>(lds + NS * kBufBytes);
+    for (int q = wave; q < (2 * NR + MR) / kWave; q += kWaves) {
+        const bool of_x = q >= 2 * NR / kWave, of_bias = q >= NR / kWave && !of_x;
+        const int row = kWave * (of_x ? q - 2 * NR / kWave : of_bias ? q - NR / kWave : q) + lane;
+        const float* const from = of_x ? xs + m0 : of_bias ? bias + n0 : ws + n0;
+        if ((!of_bias || bias != nullptr) && row < (of_x ? mt : nt))
+            lds_load4(from + row, __builtin_amdgcn_readfirstlane(base + NS * kBufBytes + 4u * kWave * (uint32_t)q));
+    }
+
     auto issue = [&](int st, int b) __attribute__((always_inline)) {
         const int c0 = st * KS;   // below 2^18: st <= steps + NS
         const uint32_t at = base + b * kBufBytes;
@@ -373,35 +386,60 @@ __device__ __forceinline__ void tile_body(uint8_t* lds, const int8_t* __restrict
     static_assert(TN >= 2, "eight chunks in a band's row");
     constexpr int kLanesPerRow = 4 * TN;                 // lanes that store one row of the band, four outputs each
     constexpr int kRowsPer = kWave / kLanesPerRow;
-    int32_t* area = reinterpret_cast<int32_t*>(lds + wave * kOutBytes);
+    float* area = reinterpret_cast<float*>(lds + wave * kOutBytes);
     const int chunk = lane % kLanesPerRow;
     const int nn = n0 + wn + 4 * chunk;
-    const int count = min(4, n - nn);                    // <= 0: nothing to store
+    // Rows of y that start off the vector's alignment: one output a lane and store, side by side across the lanes
+    // (2048 x 4097 x 512: 28.7 us with four a lane, stored one by one, 24.1 so; 2048 x 4100 x 512, in vectors: 19.0).
+    constexpr int kSide = 16 * TN < kWave ? 16 * TN : kWave;
+    constexpr int kSides = 16 * TN / kSide;
+    const bool whole = n % 4 == 0 && (reinterpret_cast<uintptr_t>(y) & (kBf16Out ? 7 : 15)) == 0;
     float sw[4], bb[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        const int col = min(nn + e, n - 1);
-        sw[e] = ws[col];
-        bb[e] = bias != nullptr ? bias[col] : 0.f;
+        const int row = wn + (whole ? 4 * chunk + e : lane % kSide + kSide * (e % kSides));
+        sw[e] = factors[row];
+        bb[e] = bias != nullptr ? factors[NR + row] : 0.f;
     }
 #pragma unroll
     for (int j = 0; j < TM; ++j) {
+        const float sx = factors[2 * NR + wm + 16 * j + r];
 #pragma unroll
-        for (int i = 0; i < TN; ++i)
-            *reinterpret_cast<i32x4*>(area + r * 16 * TN + 4 * ((4 * i + g) ^ mix(r))) = acc[i][j];
+        for (int i = 0; i < TN; ++i) {
+            f32x4 v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = (float)acc[i][j][e] * sx;
+            *reinterpret_cast<f32x4*>(area + r * 16 * TN + 4 * ((4 * i + g) ^ mix(r))) = v;
+        }
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
         __builtin_amdgcn_wave_barrier();
+        if (whole) {
 #pragma unroll
-        for (int t = 0; t < 16 / kRowsPer; ++t) {
-            const int br = t * kRowsPer + lane / kLanesPerRow;
-            const int mm = m0 + wm + 16 * j + br;
-            const i32x4 sum = *reinterpret_cast<const i32x4*>(area + br * 16 * TN + 4 * (chunk ^ mix(br)));
-            if (mm < m && count > 0) {
-                const float sx = xs[mm];
-                f32x4 v;
+            for (int t = 0; t < 16 / kRowsPer; ++t) {
+                const int br = t * kRowsPer + lane / kLanesPerRow;
+                const int mm = m0 + wm + 16 * j + br;
+                f32x4 v = *reinterpret_cast<const f32x4*>(area + br * 16 * TN + 4 * (chunk ^ mix(br)));
+                if (mm < m && nn < n) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = (float)sum[e] * sx * sw[e] + bb[e];
-                store4<kBf16Out>(y, (int64_t)mm * n + nn, v, count);
+                    for (int e = 0; e < 4; ++e) v[e] = v[e] * sw[e] + bb[e];
+                    store4<kBf16Out>(y, (int64_t)mm * n + nn, v, 4);
+                }
+            }
+        } else {
+#pragma unroll 4
+            for (int t = 0; t < 16 * kSide / kWave; ++t) {
+                const int br = t * (kWave / kSide) + lane / kSide;
+                const int mm = m0 + wm + 16 * j + br;
+#pragma unroll
+                for (int e = 0; e < kSides; ++e) {
+                    const int c = lane % kSide + kSide * e;
+                    const float v = area[br * 16 * TN + 4 * ((c / 4) ^ mix(br)) + c % 4] * sw[e] + bb[e];
+                    const int64_t at = (int64_t)mm * n + (n0 + wn + c);
+                    if (mm < m && n0 + wn + c < n) {
+                        if constexpr (kBf16Out) reinterpret_cast<uint16_t*>(y)[at] = (uint16_t)f32_to_bf16_rne(v);
+                        else reinterpret_cast<float*>(y)[at] = v;
+                    }
+                }
             }
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
@@ -414,7 +452,8 @@ constexpr int kBand = 4;
 
 // First rows of tile `tile` (rows_w x rows_x of them each), numbered along x inside bands of kBand tiles, then along w.
 __device__ __forceinline__ void tile_rows(uint32_t tile, int m, int n, int rows_w, int rows_x, int& n0, int& m0) {
-    const uint32_t tn = (uint32_t)(n + rows_w - 1) / (uint32_t)rows_w, tm = (uint32_t)(m + rows_x - 1) / (uint32_t)rows_x;
+    const uint32_t tn = (uint32_t)(n + rows_w - 1) / (uint32_t)rows_w;
+    const uint32_t tm = (uint32_t)(m + rows_x - 1) / (uint32_t)rows_x;
     const uint32_t band = tile / (kBand * tn), in = tile - band * (kBand * tn);
     const uint32_t size = min((uint32_t)kBand, tm - band * kBand);
     n0 = __builtin_amdgcn_readfirstlane(in / size * (uint32_t)rows_w);
