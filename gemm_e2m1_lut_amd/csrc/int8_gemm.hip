@@ -245,6 +245,15 @@ hipError_t launch_stream(const int8_t* x, const float* xs, const int8_t* w, cons
 // NS into the buffer that is now free and reads the first slice of step s + 1.
 // The sums leave through LDS too, one 16-row band of x at a time in an area of
 // the wave's own, so that whole rows of y are scaled and stored.
+// Waves: as many as the registers and a band's width allow, though small ones
+// read an operand from LDS more often; a step's latency (barrier, LDS reads,
+// matrix instructions) is hidden by the other waves alone. 130 x 4096 x 4096 in
+// 64 x 64 tiles: 13.0 us with two waves, 10.7 with four, 9.2 with eight; one
+// round of 128 x 128 tiles of 4096 columns 35.6, 22.4 and, with sixteen, 15.7.
+// A workgroup alone passes 41 LDS bytes a cycle for them (64 x 64: 16 KB in 375
+// cycles), the stream form 57, the direct-to-LDS path at most 64. Ring buffers:
+// as few as let a second workgroup onto the compute unit (64 x 64 with eight
+// instead of four: 512 x 4096 x 4096 18.2 instead of 15.8 us).
 
 // This wave's LDS reads are done and at most kN of its requests are in flight; then the workgroup's barrier.
 template <int kN>
@@ -275,7 +284,6 @@ __device__ __forceinline__ void tile_body(uint8_t* lds, const int8_t* __restrict
     constexpr int kBufBytes = (NR + MR) * KS;
     constexpr int kOutBytes = 16 * 16 * TN * 4;                           // a wave's band of sums
     static_assert(kWaves * kOutBytes <= NS * kBufBytes && tile_lds_bytes<kWN, kWM, TN, TM, NS>() <= 160 * 1024, "LDS");
-    static_assert(NR % kWave == 0 && MR % kWave == 0, "scales: whole requests");
     const int lane = threadIdx.x % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int r = lane & 15, g = lane >> 4;
@@ -305,11 +313,12 @@ __device__ __forceinline__ void tile_body(uint8_t* lds, const int8_t* __restrict
     // w_scale [NR], bias [NR], x_scale [MR]: requested like the operands and before them, so landed with the first
     // step (loads in the epilogue would wait for its stores: their count is one)
     float* const factors = reinterpret_cast<float*>(lds + NS * kBufBytes);
-    for (int q = wave; q < (2 * NR + MR) / kWave; q += kWaves) {
-        const bool of_x = q >= 2 * NR / kWave, of_bias = q >= NR / kWave && !of_x;
-        const int row = kWave * (of_x ? q - 2 * NR / kWave : of_bias ? q - NR / kWave : q) + lane;
-        const float* const from = of_x ? xs + m0 : of_bias ? bias + n0 : ws + n0;
-        if ((!of_bias || bias != nullptr) && row < (of_x ? mt : nt))
+    for (int q = wave; q < (2 * NR + MR + kWave - 1) / kWave; q += kWaves) {
+        const int at = kWave * q + lane;
+        const bool of_w = at < NR, of_bias = !of_w && at < 2 * NR;
+        const int row = of_w ? at : of_bias ? at - NR : at - 2 * NR;
+        const float* const from = of_w ? ws + n0 : of_bias ? bias + n0 : xs + m0;
+        if ((!of_bias || bias != nullptr) && row < (of_w || of_bias ? nt : mt))   // mt <= MR: nor past the area
             lds_load4(from + row, __builtin_amdgcn_readfirstlane(base + NS * kBufBytes + 4u * kWave * (uint32_t)q));
     }
 
@@ -548,26 +557,30 @@ hipError_t launch_largest(const int8_t* x, const float* xs, const int8_t* w, con
     return hipGetLastError();
 }
 
-// The forms and tile shapes, and what a round of tiles over the compute units takes: round_us + step_us for every
-// 128 columns (us; fitted to whole calls with int8 codes of normal values; the two largest tiles at the clock that
-// the chip keeps under their load). The shape whose rounds sum to the least is taken.
+// The forms and tile shapes, and what a call takes: call_us, and round_us + step_us for every 128 columns of each
+// round of tiles over the compute units (us; fitted to 310 calls of random sizes from 1 x 256 x 256 to 8192 x 32768 x
+// 16384, with int8 codes of normal values; the largest at the clock that the chip keeps under that load). The least is
+// taken: over those calls 0.7 % above the fastest shape's time, and each shape, left out, would cost 0.5 to 1.6 %.
 struct Shape {
     int rows_w, rows_x;
-    float round_us, step_us;
+    float call_us, round_us, step_us;
     hipError_t (*launch)(const int8_t*, const float*, const int8_t*, const float*, const float*, void*, bool, int64_t,
                          int64_t, int64_t, hipStream_t);
 };
 
 const Shape kShapes[] = {
-    {16, 16, 0.6f, 0.055f, launch_stream<8, 1, 1>},
-    {16, 32, 0.7f, 0.068f, launch_stream<4, 1, 2>},
-    {32, 32, 1.5f, 0.086f, launch_stream<4, 2, 2>},
-    {64, 64, 3.2f, 0.20f, launch_tile<2, 2, 2, 2, 8>},
-    {64, 128, 5.0f, 0.33f, launch_tile<2, 2, 2, 4, 6>},
-    {128, 128, 7.0f, 0.53f, launch_tile<2, 2, 4, 4, 4>},
-    {256, 128, 8.0f, 0.80f, launch_tile<4, 2, 4, 4, 3>},   // and the halves of the last shape's last round
-    {256, 256, 12.0f, 1.40f, launch_largest},
+    {16, 16, 2.1f, 0.8f, 0.052f, launch_stream<8, 1, 1>},
+    {16, 32, 2.2f, 0.6f, 0.071f, launch_stream<4, 1, 2>},
+    {32, 32, 2.3f, 0.7f, 0.118f, launch_stream<4, 2, 2>},
+    {64, 64, 2.3f, 1.1f, 0.202f, launch_tile<2, 4, 2, 1, 4>},
+    {64, 128, 2.3f, 1.5f, 0.311f, launch_tile<2, 4, 2, 2, 3>},
+    {128, 128, 0.4f, 4.0f, 0.468f, launch_tile<4, 4, 2, 2, 3>},
+    {256, 128, 0.4f, 6.5f, 0.772f, launch_tile<4, 4, 4, 2, 3>},
+    {256, 256, 0.1f, 12.7f, 1.39f, launch_largest},
 };
+
+// A last round of halves takes this part of a round of 256 x 256 tiles.
+constexpr float kHalvesRound = 0.6f;
 
 }  // namespace
 
@@ -580,9 +593,9 @@ hipError_t launch_int8_gemm(const int8_t* x, const float* x_scale, const int8_t*
     float best_us = 0.f;
     for (const Shape& s : kShapes) {
         const int64_t tiles = ((n + s.rows_w - 1) / s.rows_w) * ((m + s.rows_x - 1) / s.rows_x);
-        float us = (float)((tiles + cus - 1) / cus) * (s.round_us + steps * s.step_us);
-        if (s.launch == launch_largest && halves_last_round(tiles, cus))   // by the shape before it
-            us -= s.round_us + steps * s.step_us - (kShapes[6].round_us + steps * kShapes[6].step_us);
+        float rounds = (float)((tiles + cus - 1) / cus);
+        if (s.launch == launch_largest && halves_last_round(tiles, cus)) rounds -= 1.f - kHalvesRound;
+        const float us = s.call_us + rounds * (s.round_us + steps * s.step_us);
         if (best == nullptr || us < best_us) {
             best = &s;
             best_us = us;
