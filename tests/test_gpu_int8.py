@@ -299,7 +299,10 @@ GEMM_SHAPES = [
     (17, 31, 80), (31, 97, 528), (33, 64, 512), (64, 256, 1024), (65, 129, 2896), (100, 48, 4112), (128, 128, 128),
     (130, 1003, 1040), (255, 257, 272), (256, 256, 384), (257, 511, 640), (300, 2881, 1536), (513, 770, 2880),
     (1000, 300, 16), (700, 1030, 4096), (4099, 65, 96), (20, 8200, 160),
-    (4100, 4100, 1040),   # more largest tiles than compute units, the last round's halved
+    # the larger tiles, with rows of y that are aligned and rows that are not; the last two: more of the largest
+    # tiles than compute units, the last round's halved
+    (700, 2052, 1040), (515, 2881, 2896), (1020, 4092, 1040), (1020, 4091, 528), (1025, 4100, 1040), (1500, 4097, 1040),
+    (2047, 8188, 400), (2047, 8191, 400), (4100, 4097, 1040), (4100, 4100, 1040),
 ]
 
 
