@@ -263,6 +263,19 @@ def test_act_every_bf16_gate(gpu):
     check_act(gpu, np.concatenate([p, u], axis=1), "bf16")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("k", [512, 4096])
+def test_act_moderate_gates(gpu, dtype, k):
+    """Units of eight whose gates all lie within 44, units with one beyond, subnormal gates, and `up` near both ends."""
+    r = np.random.default_rng(k)
+    g = np.stack([r.uniform(-44, 44, k), r.uniform(-44.5, 44.5, k), r.uniform(-44, -43, k), r.uniform(-4, 4, k),
+                  r.standard_normal(k) * 1e-39, r.uniform(40, 44, k), r.uniform(-46, -43, k), r.standard_normal(k)])
+    u = np.stack([r.standard_normal(k), r.standard_normal(k) * 1e30, r.standard_normal(k) * 1e37,
+                  r.standard_normal(k) * 1e-30, r.standard_normal(k) * 1e36, r.standard_normal(k) * 1e36,
+                  r.standard_normal(k) * 1e10, r.standard_normal(k) * 1e-16])
+    check_act(gpu, np.concatenate([g, u], axis=1), dtype)
+
+
 # ------------------------------------------------------------------- gemm --
 
 def random_codes(r, rows: int, k: int) -> np.ndarray:
