@@ -30,14 +30,22 @@ typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 constexpr uint32_t kOutOfRange = 0xFFFFFFF0u;   // a buffer offset past any resource's range
 
 // Four outputs of row m from column n0 on.
+typedef float f32x2v __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2v __attribute__((ext_vector_type(2)));
+
+// bf16 patterns of two floats, nearest even, in the conversion instruction
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2v{lo, hi}), bf16x2v));
+}
+
 template <bool kBf16Out>
 __device__ __forceinline__ void store4(void* y, int64_t idx, const f32x4& v, int count) {
     if constexpr (kBf16Out) {
         uint16_t* p = reinterpret_cast<uint16_t*>(y) + idx;
         if (count == 4 && (reinterpret_cast<uintptr_t>(p) & 7) == 0) {
-            *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+            *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
         } else {
-            for (int j = 0; j < count; ++j) p[j] = (uint16_t)f32_to_bf16_rne(v[j]);
+            for (int j = 0; j < count; ++j) p[j] = (uint16_t)pack_bf16(v[j], 0.f);
         }
     } else {
         float* p = reinterpret_cast<float*>(y) + idx;
@@ -445,7 +453,7 @@ __device__ __forceinline__ void tile_body(uint8_t* lds, const int8_t* __restrict
                     const float v = area[br * 16 * TN + 4 * ((c / 4) ^ mix(br)) + c % 4] * sw[e] + bb[e];
                     const int64_t at = (int64_t)mm * n + (n0 + wn + c);
                     if (mm < m && n0 + wn + c < n) {
-                        if constexpr (kBf16Out) reinterpret_cast<uint16_t*>(y)[at] = (uint16_t)f32_to_bf16_rne(v);
+                        if constexpr (kBf16Out) reinterpret_cast<uint16_t*>(y)[at] = (uint16_t)pack_bf16(v, 0.f);
                         else reinterpret_cast<float*>(y)[at] = v;
                     }
                 }
