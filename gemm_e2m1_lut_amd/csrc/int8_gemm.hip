@@ -242,18 +242,19 @@ hipError_t launch_stream(const int8_t* x, const float* xs, const int8_t* w, cons
 // its kWN x kWM waves 16 TN x 16 TM of it in 16x16x64 matrix-core tiles (A = w, B = x).
 // K goes in steps of KS columns through a ring of NS LDS buffers that the
 // memory pipeline fills itself (buffer_load ... lds: no registers, no LDS
-// writes by the waves). In LDS a row's 16-byte chunks are permuted, chunk c of
-// row r at slot c ^ (r / (256 / KS) % (KS / 16)), so that an operand read (16 rows, one
-// chunk) meets every bank once; the requests' source addresses do that, as
-// the LDS side of a request is contiguous.
+// writes by the waves). In LDS a row's 16-byte chunks are permuted by the row,
+// so that an operand read (16 rows, one chunk) meets every bank once; the
+// requests' source addresses do that, as the LDS side of a request is contiguous.
 // Operands are read one 64-column slice ahead of their MFMAs, over the step's
 // border too: before the last slice's MFMAs of step s a wave waits until its own
 // reads of the buffer and its requests of step s + 1 are done, passes the step's
 // one barrier (with the previous slice's MFMAs still running), requests step s +
 // NS into the buffer that is now free and reads the first slice of step s + 1.
-// The sums leave through LDS too, one 16-row band of x at a time in an area of
-// the wave's own, so that whole rows of y are scaled and stored.
-// Waves: as many as the registers and a band's width allow, though small ones
+// A lane's sums of two operands of w are eight neighbouring columns of y, which
+// it scales and stores at once (through LDS instead, 4096 x 4096 x 512 took 17.5
+// us, so 16.3). Stores past the caches (nontemporal) took 58 us where these take
+// 57 (4096 x 4096 x 4096), and leave y for the next operator to fetch.
+// Waves: as many as the registers and pairs of operands allow, though small ones
 // read an operand from LDS more often; a step's latency (barrier, LDS reads,
 // matrix instructions) is hidden by the other waves alone. 130 x 4096 x 4096 in
 // 64 x 64 tiles: 13.0 us with two waves, 10.7 with four, 9.2 with eight; one
@@ -302,12 +303,12 @@ __device__ __forceinline__ void tile_body(uint8_t* lds, const int8_t* __restrict
     const __amdgpu_buffer_rsrc_t xres = __builtin_amdgcn_make_buffer_rsrc(
         const_cast<int8_t*>(x + (int64_t)m0 * k), 0, mt * k, kBufferWord3);
 
-    // request i of a wave fills rows 8 (kLoads wave + i) .. + 7 of its operand; lane l fills slot l % 8 of row
-    // l / 8, whose chunk is l % 8 ^ (row / 2 % 8): column col for every second request, col ^ 64 for the others.
-    // Rows past the matrix read out of range: zeros, no memory access.
-    const int col = 16 * ((lane % 8) ^ (lane >> 4));
-    auto wcol = [&](int i) __attribute__((always_inline)) { return col ^ (64 * ((kWLoads * wave + i) & 1)); };
-    auto xcol = [&](int i) __attribute__((always_inline)) { return col ^ (64 * ((kXLoads * wave + i) & 1)); };
+    // request q of an operand fills rows 8 q .. + 7; lane l fills slot l % 8 of row l / 8, whose chunk is
+    // l % 8 ^ (row / 2 % 8) for x and l % 8 ^ (2 (row / 8 % 4) + row / 2 % 2) for w. Rows past the matrix read out of
+    // range: zeros, no memory access.
+    const int colx = 16 * ((lane % 8) ^ (lane >> 4)), colw = 16 * ((lane % 8) ^ (lane >> 4 & 1));
+    auto wcol = [&](int i) __attribute__((always_inline)) { return colw ^ (32 * ((kWLoads * wave + i) & 3)); };
+    auto xcol = [&](int i) __attribute__((always_inline)) { return colx ^ (64 * ((kXLoads * wave + i) & 1)); };
     uint32_t woff[kWLoads], xoff[kXLoads];
 #pragma unroll
     for (int i = 0; i < kWLoads; ++i)
@@ -342,15 +343,19 @@ __device__ __forceinline__ void tile_body(uint8_t* lds, const int8_t* __restrict
             lds_load16(xres, c0 + xcol(i) < k ? xoff[i] + (uint32_t)c0 : kOutOfRange,
                        __builtin_amdgcn_readfirstlane(at + NR * KS + 1024u * (uint32_t)(kXLoads * wave + i)));
     };
-    // operand i of w / j of x: slice q of buffer b (row / 2 % 8 is r / 2 % 8: the tiles start at multiples of 16)
-    const uint8_t* wrow = lds + (wn + r) * KS;
+    // Operand i of w takes rows 32 (i / 2) + 8 (r / 4) + 4 (i % 2) + r % 4 of the wave's, so that a lane's sums of two
+    // operands are eight neighbouring columns of y; operand j of x rows 16 j + r.
+    static_assert(TN % 2 == 0, "operands of w in pairs");
+    const uint8_t* wrow = lds + (wn + 8 * (r >> 2) + (r & 3)) * KS;
     const uint8_t* xrow = lds + NR * KS + (wm + r) * KS;
-    const int slot[2] = {16 * (g ^ (r >> 1)), 16 * ((4 + g) ^ (r >> 1))};
+    const int wslot = 2 * (r >> 2) + (r >> 1 & 1), xslot = r >> 1;
+    const int wat[2] = {16 * (g ^ wslot), 16 * ((4 + g) ^ wslot)};
+    const int xat[2] = {16 * (g ^ xslot), 16 * ((4 + g) ^ xslot)};
     auto read_w = [&](int b, int q, int i) __attribute__((always_inline)) {
-        return *reinterpret_cast<const i32x4*>(wrow + slot[q] + (b * kBufBytes + 16 * i * KS));
+        return *reinterpret_cast<const i32x4*>(wrow + wat[q] + (b * kBufBytes + (32 * (i / 2) + 4 * (i % 2)) * KS));
     };
     auto read_x = [&](int b, int q, int j) __attribute__((always_inline)) {
-        return *reinterpret_cast<const i32x4*>(xrow + slot[q] + (b * kBufBytes + 16 * j * KS));
+        return *reinterpret_cast<const i32x4*>(xrow + xat[q] + (b * kBufBytes + 16 * j * KS));
     };
 
     i32x4 a[TN], c[2][TM];
@@ -395,26 +400,55 @@ __device__ __forceinline__ void tile_body(uint8_t* lds, const int8_t* __restrict
             }
         }
     }
+    // lane 16 g + r holds, of row wm + 16 j + r of x, columns wn + 32 (i / 2) + 8 g + 4 (i % 2) .. + 3 of y in acc[i][j]
+    if (n % 4 == 0 && (reinterpret_cast<uintptr_t>(y) & (kBf16Out ? 7 : 15)) == 0) {
+        const bool wide = kBf16Out && n % 8 == 0 && (reinterpret_cast<uintptr_t>(y) & 15) == 0;
+        float sx[TM];
+#pragma unroll
+        for (int j = 0; j < TM; ++j) sx[j] = factors[2 * NR + wm + 16 * j + r];
+#pragma unroll
+        for (int i = 0; i < TN; i += 2) {
+            const int row = wn + 16 * i + 8 * g, nn = n0 + row;
+            float sw[8], bb[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                sw[e] = factors[row + e];
+                bb[e] = bias != nullptr ? factors[NR + row + e] : 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < TM; ++j) {
+                const int mm = m0 + wm + 16 * j + r;
+                f32x4 v[2];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e / 4][e % 4] = (float)acc[i + e / 4][j][e % 4] * sx[j] * sw[e] + bb[e];
+                if (mm < m && nn < n) {
+                    const int64_t at = (int64_t)mm * n + nn;
+                    if (wide) {
+                        *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(y) + at) =
+                            make_uint4(pack_bf16(v[0][0], v[0][1]), pack_bf16(v[0][2], v[0][3]),
+                                       pack_bf16(v[1][0], v[1][1]), pack_bf16(v[1][2], v[1][3]));
+                    } else {
+                        store4<kBf16Out>(y, at, v[0], 4);
+                        if (nn + 4 < n) store4<kBf16Out>(y, at + 4, v[1], 4);
+                    }
+                }
+            }
+        }
+        wait_vm<0>();   // the requests past the last step have landed before the workgroup's LDS is released
+        return;
+    }
+    // Rows of y off the vector's alignment leave through LDS, one 16-row band of x at a time in an area of the wave's
+    // own, its chunks permuted like the operands', to be stored side by side across the lanes (2048 x 4097 x 512:
+    // 28.7 us with four a lane, stored one by one, 24.1 so; 2048 x 4100 x 512, in vectors: 19.0).
     step_barrier<0>();   // every request has landed and every read is done: the buffers are free
-
-    // lane 16 g + r holds, of row wm + 16 j + r of x, rows wn + 16 i + 4 g .. + 3 of w: chunk 4 i + g of the
-    // band's row, permuted like the operands' chunks so that 16 rows of one chunk meet every bank once
     auto mix = [](int row) __attribute__((always_inline)) { return TN >= 4 ? row : row >> 1; };
-    static_assert(TN >= 2, "eight chunks in a band's row");
-    constexpr int kLanesPerRow = 4 * TN;                 // lanes that store one row of the band, four outputs each
-    constexpr int kRowsPer = kWave / kLanesPerRow;
-    float* area = reinterpret_cast<float*>(lds + wave * kOutBytes);
-    const int chunk = lane % kLanesPerRow;
-    const int nn = n0 + wn + 4 * chunk;
-    // Rows of y that start off the vector's alignment: one output a lane and store, side by side across the lanes
-    // (2048 x 4097 x 512: 28.7 us with four a lane, stored one by one, 24.1 so; 2048 x 4100 x 512, in vectors: 19.0).
     constexpr int kSide = 16 * TN < kWave ? 16 * TN : kWave;
     constexpr int kSides = 16 * TN / kSide;
-    const bool whole = n % 4 == 0 && (reinterpret_cast<uintptr_t>(y) & (kBf16Out ? 7 : 15)) == 0;
-    float sw[4], bb[4];
+    float* area = reinterpret_cast<float*>(lds + wave * kOutBytes);
+    float sw[kSides], bb[kSides];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const int row = wn + (whole ? 4 * chunk + e : lane % kSide + kSide * (e % kSides));
+    for (int e = 0; e < kSides; ++e) {
+        const int row = wn + lane % kSide + kSide * e;
         sw[e] = factors[row];
         bb[e] = bias != nullptr ? factors[NR + row] : 0.f;
     }
@@ -426,36 +460,22 @@ __device__ __forceinline__ void tile_body(uint8_t* lds, const int8_t* __restrict
             f32x4 v;
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] = (float)acc[i][j][e] * sx;
-            *reinterpret_cast<f32x4*>(area + r * 16 * TN + 4 * ((4 * i + g) ^ mix(r))) = v;
+            *reinterpret_cast<f32x4*>(area + r * 16 * TN + 4 * ((8 * (i / 2) + 2 * g + i % 2) ^ mix(r))) = v;
         }
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
         __builtin_amdgcn_wave_barrier();
-        if (whole) {
-#pragma unroll
-            for (int t = 0; t < 16 / kRowsPer; ++t) {
-                const int br = t * kRowsPer + lane / kLanesPerRow;
-                const int mm = m0 + wm + 16 * j + br;
-                f32x4 v = *reinterpret_cast<const f32x4*>(area + br * 16 * TN + 4 * (chunk ^ mix(br)));
-                if (mm < m && nn < n) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] = v[e] * sw[e] + bb[e];
-                    store4<kBf16Out>(y, (int64_t)mm * n + nn, v, 4);
-                }
-            }
-        } else {
 #pragma unroll 4
-            for (int t = 0; t < 16 * kSide / kWave; ++t) {
-                const int br = t * (kWave / kSide) + lane / kSide;
-                const int mm = m0 + wm + 16 * j + br;
+        for (int t = 0; t < 16 * kSide / kWave; ++t) {
+            const int br = t * (kWave / kSide) + lane / kSide;
+            const int mm = m0 + wm + 16 * j + br;
 #pragma unroll
-                for (int e = 0; e < kSides; ++e) {
-                    const int c = lane % kSide + kSide * e;
-                    const float v = area[br * 16 * TN + 4 * ((c / 4) ^ mix(br)) + c % 4] * sw[e] + bb[e];
-                    const int64_t at = (int64_t)mm * n + (n0 + wn + c);
-                    if (mm < m && n0 + wn + c < n) {
-                        if constexpr (kBf16Out) reinterpret_cast<uint16_t*>(y)[at] = (uint16_t)pack_bf16(v, 0.f);
-                        else reinterpret_cast<float*>(y)[at] = v;
-                    }
+            for (int e = 0; e < kSides; ++e) {
+                const int c = lane % kSide + kSide * e;
+                const float v = area[br * 16 * TN + 4 * ((c / 4) ^ mix(br)) + c % 4] * sw[e] + bb[e];
+                const int64_t at = (int64_t)mm * n + (n0 + wn + c);
+                if (mm < m && n0 + wn + c < n) {
+                    if constexpr (kBf16Out) reinterpret_cast<uint16_t*>(y)[at] = (uint16_t)pack_bf16(v, 0.f);
+                    else reinterpret_cast<float*>(y)[at] = v;
                 }
             }
         }
