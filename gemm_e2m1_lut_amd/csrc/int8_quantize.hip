@@ -482,7 +482,7 @@ hipError_t dispatch(const void* xv, const void* resv, const void* wv, float eps,
     // Few elements: as many threads a row as it has units, for the latency. Many: two units or more a thread, for
     // the bytes in flight. (bf16, us, the one against the other: norm with residual, k 4096, 512 rows 5.4 / 5.5, 2000
     // rows 12.6 / 12.3; plain, 14336 x 4096, 43.1 / 34.6; k 8192, 512 rows 5.5 / 5.4, 2000 rows 15.7 / 12.8; act,
-    // k 14336, 512 rows 12.5 / 13.1, 2000 rows 37.7 / 34.8; k 1024, 2000 rows 4.0 / 4.1, 20000 rows 16.3 / 14.8.)
+    // k 14336, 512 rows 11.4 / 12.0, 2000 rows 34.7 / 32.7; k 1024, 2000 rows 4.0 / 4.1, 20000 rows 16.3 / 14.8.)
     const bool many = rows * k >= (int64_t)6 << 20;
     if (units <= 64) {
         E2M1_ROWS(64, 1, false);
