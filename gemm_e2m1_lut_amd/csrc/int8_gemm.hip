@@ -8,17 +8,16 @@
 //
 // gfx950 design. Few rows of x: the bytes of w bound the product, and the stream
 // form reads them at 5.0 to 5.7 TB/s (4096 x 14336: 10.3 us for one row of x,
-// 10.9 for 16, 14336 x 4096: 11.2 and 11.4; a plain read of the same bytes
-// takes 8.8). Many rows: the matrix
+// 10.6 for 16; a plain read of the same bytes takes 8.8). Many rows: the matrix
 // cores bound it, and under full load their energy does: with the operands of
 // real matrices the chip lowers its clock (1.3 GHz was measured, 2.4 with
 // constant operands). 16x16x64 tiles take less of it than 32x32x32
-// ones (matrix cores alone, normal codes: 4.09 against 3.42 PFLOP/s; 8192^3:
-// 441 against 494 us), so they are used throughout. Both forms feed the matrix
+// ones (matrix cores alone, normal codes: 4.09 against 3.42 POP/s; 8192^3: 441
+// against 494 us), so they are used throughout: 8192^3 takes 430 us, 2048 x 28672
+// x 4096 218. Both forms feed the matrix
 // cores from LDS rings that direct-to-LDS loads fill in 128-byte row segments
 // (64-byte ones read at half the L2 rate: 66 against 130 GB/s a compute unit).
-// What bounds a tile of 64 x 64 is the latency of its ring (128 KB in flight),
-// not its barriers: two groups of waves that halve the steps gained nothing.
+// What bounds the tiles in between is LDS traffic and a step's latency.
 #include "device.hpp"
 #include "kernels.hpp"
 
@@ -29,7 +28,6 @@ typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 
 constexpr uint32_t kOutOfRange = 0xFFFFFFF0u;   // a buffer offset past any resource's range
 
-// Four outputs of row m from column n0 on.
 typedef float f32x2v __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2v __attribute__((ext_vector_type(2)));
 
@@ -38,6 +36,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2v{lo, hi}), bf16x2v));
 }
 
+// v's first `count` (at most four) values to y from element idx on.
 template <bool kBf16Out>
 __device__ __forceinline__ void store4(void* y, int64_t idx, const f32x4& v, int count) {
     if constexpr (kBf16Out) {

@@ -360,6 +360,22 @@ def test_gemm_each_column_counts_once(gpu, m, n):
     check_gemm(gpu, x, w, "f32")
 
 
+@pytest.mark.parametrize("m", [1, 20, 130])
+@pytest.mark.parametrize("low", [0x0000, 0x7FFF, 0x8000, 0x8001])
+def test_gemm_rounds_to_the_nearest_bf16(gpu, m, low):
+    """Products of zero leave the bias (every upper half, subnormal, infinite and NaN ones too) for the rounding."""
+    bits = torch.arange(1 << 16, device="cuda", dtype=torch.int64) << 16 | low
+    bias = torch.where(bits < 1 << 31, bits, bits - (1 << 32)).to(torch.int32).view(torch.float32)
+    n = bias.numel()
+    y = gpu.int8_gemm(torch.zeros(m, 16, dtype=torch.int8, device="cuda"), torch.ones(m, device="cuda"),
+                      torch.zeros(n, 16, dtype=torch.int8, device="cuda"), torch.ones(n, device="cuda"), bias=bias)
+    want = (bias.cpu() + 0.0).to(torch.bfloat16)
+    got = y.cpu()
+    nan = torch.isnan(want)
+    assert bool((torch.isnan(got) == nan).all())
+    assert bool((got.view(torch.int16)[:, ~nan] == want.view(torch.int16)[~nan]).all())
+
+
 def test_gemm_no_columns(gpu):
     say("int8_gemm: k = 0")
     x, w = torch.empty(3, 0, dtype=torch.int8, device=DEV), torch.empty(5, 0, dtype=torch.int8, device=DEV)
