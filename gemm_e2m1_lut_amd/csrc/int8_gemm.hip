@@ -249,6 +249,12 @@ hipError_t launch_stream(const int8_t* x, const float* xs, const int8_t* w, cons
 // reads of the buffer and its requests of step s + 1 are done, passes the step's
 // one barrier (with the previous slice's MFMAs still running), requests step s +
 // NS into the buffer that is now free and reads the first slice of step s + 1.
+// Rows that start inside a 128-byte line (k no multiple of 128) would have every
+// request of a row touch two lines, a third of the time in mid-sized products.
+// By lines (kLines), a request takes the row's line instead, so a step's chunks
+// lie in its own buffer and the next one: the chunk's slot stays as it is, only
+// the buffer depends on how far into a line the row starts, which is the same
+// for all rows of a lane's operands of x, and one of two values for w.
 // A lane's sums of two operands of w are eight neighbouring columns of y, which
 // it scales and stores at once (through LDS instead, 4096 x 4096 x 512 took 17.5
 // us, so 16.3). Stores past the caches (nontemporal) took 58 us where these take
@@ -279,7 +285,7 @@ constexpr int tile_lds_bytes() {   // the ring; w_scale, bias and x_scale of the
 }
 
 // The tile from row n0 of w and row m0 of x on.
-template <int kWN, int kWM, int TN, int TM, int NS, bool kBf16Out>
+template <int kWN, int kWM, int TN, int TM, int NS, bool kLines, bool kBf16Out>
 __device__ __forceinline__ void tile_body(uint8_t* lds, const int8_t* __restrict__ x, const float* __restrict__ xs,
                                           const int8_t* __restrict__ w, const float* __restrict__ ws,
                                           const float* __restrict__ bias, void* __restrict__ y, int m, int n, int k,
@@ -303,11 +309,24 @@ __device__ __forceinline__ void tile_body(uint8_t* lds, const int8_t* __restrict
         const_cast<int8_t*>(x + (int64_t)m0 * k), 0, mt * k, kBufferWord3);
 
     // request q of an operand fills rows 8 q .. + 7; lane l fills slot l % 8 of row l / 8, whose chunk is
-    // l % 8 ^ (row / 2 % 8) for x and l % 8 ^ (2 (row / 8 % 4) + row / 2 % 2) for w. Rows past the matrix read out of
+    // l % 8 ^ (row / 2 % 8) for x and l % 8 ^ (2 (row / 8 % 4) + row / 2 % 2) for w; by lines, it is a chunk of the
+    // step before if this one lies in the row's next line. Rows past the matrix and columns outside [0, k) read out of
     // range: zeros, no memory access.
+    const uint32_t chunks = (uint32_t)k / 16;            // of a row
+    auto past_line = [&](const int8_t* p, uint32_t row) __attribute__((always_inline)) {   // chunks
+        return kLines ? (int)(((uint32_t)((uintptr_t)p / 16) + row * chunks) & 7) : 0;
+    };
     const int colx = 16 * ((lane % 8) ^ (lane >> 4)), colw = 16 * ((lane % 8) ^ (lane >> 4 & 1));
-    auto wcol = [&](int i) __attribute__((always_inline)) { return colw ^ (32 * ((kWLoads * wave + i) & 3)); };
-    auto xcol = [&](int i) __attribute__((always_inline)) { return colx ^ (64 * ((kXLoads * wave + i) & 1)); };
+    const int pastx = past_line(x, lane / 8), pastw = past_line(w, lane / 8);
+    auto in_line = [&](int col, int past) __attribute__((always_inline)) {
+        return kLines && col / 16 + past >= 8 ? col - KS : col;
+    };
+    auto wcol = [&](int i) __attribute__((always_inline)) {
+        return in_line(colw ^ (32 * ((kWLoads * wave + i) & 3)), pastw);
+    };
+    auto xcol = [&](int i) __attribute__((always_inline)) {
+        return in_line(colx ^ (64 * ((kXLoads * wave + i) & 1)), pastx);
+    };
     uint32_t woff[kWLoads], xoff[kXLoads];
 #pragma unroll
     for (int i = 0; i < kWLoads; ++i)
@@ -335,11 +354,11 @@ __device__ __forceinline__ void tile_body(uint8_t* lds, const int8_t* __restrict
         const uint32_t at = base + b * kBufBytes;
 #pragma unroll
         for (int i = 0; i < kWLoads; ++i)   // columns (and whole steps) past K too
-            lds_load16(wres, c0 + wcol(i) < k ? woff[i] + (uint32_t)c0 : kOutOfRange,
+            lds_load16(wres, (uint32_t)(c0 + wcol(i)) < (uint32_t)k ? woff[i] + (uint32_t)c0 : kOutOfRange,
                        __builtin_amdgcn_readfirstlane(at + 1024u * (uint32_t)(kWLoads * wave + i)));
 #pragma unroll
         for (int i = 0; i < kXLoads; ++i)
-            lds_load16(xres, c0 + xcol(i) < k ? xoff[i] + (uint32_t)c0 : kOutOfRange,
+            lds_load16(xres, (uint32_t)(c0 + xcol(i)) < (uint32_t)k ? xoff[i] + (uint32_t)c0 : kOutOfRange,
                        __builtin_amdgcn_readfirstlane(at + NR * KS + 1024u * (uint32_t)(kXLoads * wave + i)));
     };
     // Operand i of w takes rows 32 (i / 2) + 8 (r / 4) + 4 (i % 2) + r % 4 of the wave's, so that a lane's sums of two
@@ -347,14 +366,27 @@ __device__ __forceinline__ void tile_body(uint8_t* lds, const int8_t* __restrict
     static_assert(TN % 2 == 0, "operands of w in pairs");
     const uint8_t* wrow = lds + (wn + 8 * (r >> 2) + (r & 3)) * KS;
     const uint8_t* xrow = lds + NR * KS + (wm + r) * KS;
-    const int wslot = 2 * (r >> 2) + (r >> 1 & 1), xslot = r >> 1;
-    const int wat[2] = {16 * (g ^ wslot), 16 * ((4 + g) ^ wslot)};
-    const int xat[2] = {16 * (g ^ xslot), 16 * ((4 + g) ^ xslot)};
+    // chunk 4 q + g of a row that starts `past` chunks into a line: in the next step's buffer where it is past the line
+    struct Place { int here, last; };   // from the buffer of the step; of the ring's last buffer
+    auto place = [&](int q, int past) __attribute__((always_inline)) {
+        const int at = 16 * ((4 * q + g) ^ (r >> 1)), next = (4 * q + g + past) >> 3;
+        return Place{at + next * kBufBytes, at - next * (NS - 1) * kBufBytes};
+    };
+    Place wat[kLines ? 2 : 1][kSlices], xat[kSlices];
+#pragma unroll
+    for (int q = 0; q < kSlices; ++q) {
+        xat[q] = place(q, past_line(x, r));
+#pragma unroll
+        for (int h = 0; h < (kLines ? 2 : 1); ++h) wat[h][q] = place(q, past_line(w, (r & 3) + 4 * h));
+    }
     auto read_w = [&](int b, int q, int i) __attribute__((always_inline)) {
-        return *reinterpret_cast<const i32x4*>(wrow + wat[q] + (b * kBufBytes + (32 * (i / 2) + 4 * (i % 2)) * KS));
+        const Place& p = wat[kLines ? i % 2 : 0][q];
+        return *reinterpret_cast<const i32x4*>(wrow + (b == NS - 1 ? p.last : p.here) +
+                                               (b * kBufBytes + (32 * (i / 2) + 4 * (i % 2)) * KS));
     };
     auto read_x = [&](int b, int q, int j) __attribute__((always_inline)) {
-        return *reinterpret_cast<const i32x4*>(xrow + xat[q] + (b * kBufBytes + 16 * j * KS));
+        const Place& p = xat[q];
+        return *reinterpret_cast<const i32x4*>(xrow + (b == NS - 1 ? p.last : p.here) + (b * kBufBytes + 16 * j * KS));
     };
 
     i32x4 a[TN], c[2][TM];
@@ -365,9 +397,11 @@ __device__ __forceinline__ void tile_body(uint8_t* lds, const int8_t* __restrict
         for (int j = 0; j < TM; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
 
     constexpr int kPerStep = kWLoads + kXLoads;
+    constexpr int kAhead = kLines ? 1 : 0;   // a step reads the next buffer too
+    static_assert(NS >= 2 + kAhead, "ring");
 #pragma unroll
     for (int st = 0; st < NS; ++st) issue(st, st);
-    step_barrier<kPerStep*(NS - 1)>();
+    step_barrier<kPerStep*(NS - 1 - kAhead)>();
 #pragma unroll
     for (int j = 0; j < TM; ++j) c[0][j] = read_x(0, 0, j);
 #pragma unroll
@@ -383,7 +417,7 @@ __device__ __forceinline__ void tile_body(uint8_t* lds, const int8_t* __restrict
                 const int set = q & 1, nb = q + 1 < kSlices ? b : (b + 1) % NS, nq = (q + 1) % kSlices;
                 __builtin_amdgcn_sched_barrier(0);
                 if (q + 1 == kSlices) {
-                    step_barrier<kPerStep*(NS - 2)>();
+                    step_barrier<kPerStep*(NS - 2 - kAhead)>();
                     issue(s + NS, b);
                 }
 #pragma unroll
@@ -399,7 +433,7 @@ __device__ __forceinline__ void tile_body(uint8_t* lds, const int8_t* __restrict
             }
         }
     }
-    // lane 16 g + r holds, of row wm + 16 j + r of x, columns wn + 32 (i / 2) + 8 g + 4 (i % 2) .. + 3 of y in acc[i][j]
+    // lane 16 g + r holds in acc[i][j], of row wm + 16 j + r of x, columns wn + 32 (i / 2) + 8 g + 4 (i % 2) and on of y
     if (n % 4 == 0 && (reinterpret_cast<uintptr_t>(y) & (kBf16Out ? 7 : 15)) == 0) {
         const bool wide = kBf16Out && n % 8 == 0 && (reinterpret_cast<uintptr_t>(y) & 15) == 0;
         float sx[TM];
@@ -503,7 +537,7 @@ __device__ __forceinline__ uint32_t xcd_number(uint32_t id, uint32_t count) {
     return id / kXcds < per ? id % kXcds * per + id / kXcds : count;
 }
 
-template <int kWN, int kWM, int TN, int TM, int NS, bool kBf16Out>
+template <int kWN, int kWM, int TN, int TM, int NS, bool kLines, bool kBf16Out>
 __global__ __launch_bounds__(kWave * kWN * kWM) void int8_gemm_tile_kernel(
     const int8_t* __restrict__ x, const float* __restrict__ xs, const int8_t* __restrict__ w,
     const float* __restrict__ ws, const float* __restrict__ bias, void* __restrict__ y, int m, int n, int k,
@@ -513,7 +547,7 @@ __global__ __launch_bounds__(kWave * kWN * kWM) void int8_gemm_tile_kernel(
     if (tile >= tiles) return;   // the whole workgroup
     int n0, m0;
     tile_rows(tile, m, n, 16 * TN * kWN, 16 * TM * kWM, n0, m0);
-    tile_body<kWN, kWM, TN, TM, NS, kBf16Out>(lds, x, xs, w, ws, bias, y, m, n, k, n0, m0);
+    tile_body<kWN, kWM, TN, TM, NS, kLines, kBf16Out>(lds, x, xs, w, ws, bias, y, m, n, k, n0, m0);
 }
 
 // 256 x 256 tiles whose last round would leave at least half of the compute units idle: the last tiles, those from
@@ -534,28 +568,28 @@ __global__ __launch_bounds__(512) void int8_gemm_mixed_kernel(
         const uint32_t tile = xcd_number(id, whole);
         if (tile >= whole) return;   // the whole workgroup
         tile_rows(tile, m, n, 256, 256, n0, m0);
-        tile_body<2, 4, 8, 4, 2, kBf16Out>(lds, x, xs, w, ws, bias, y, m, n, k, n0, m0);
+        tile_body<2, 4, 8, 4, 2, false, kBf16Out>(lds, x, xs, w, ws, bias, y, m, n, k, n0, m0);
     } else {
         const uint32_t half = xcd_number(id - ids, 2 * (tiles - whole));
         if (half >= 2 * (tiles - whole)) return;
         tile_rows(whole + half / 2, m, n, 256, 256, n0, m0);
         m0 += 128 * (int)(half % 2);
         if (m0 >= m) return;
-        tile_body<4, 2, 4, 4, 3, kBf16Out>(lds, x, xs, w, ws, bias, y, m, n, k, n0, m0);
+        tile_body<4, 2, 4, 4, 3, false, kBf16Out>(lds, x, xs, w, ws, bias, y, m, n, k, n0, m0);
     }
 }
 
-template <int kWN, int kWM, int TN, int TM, int NS>
+template <int kWN, int kWM, int TN, int TM, int NS, bool kLines>
 hipError_t launch_tile(const int8_t* x, const float* xs, const int8_t* w, const float* ws, const float* bias, void* y,
                        bool out_bf16, int64_t m, int64_t n, int64_t k, hipStream_t stream) {
     constexpr int NR = 16 * TN * kWN, MR = 16 * TM * kWM;
     const int64_t tiles = ((n + NR - 1) / NR) * ((m + MR - 1) / MR);
     const dim3 grid = grid_of((tiles + kXcds - 1) / kXcds * kXcds);
     if (out_bf16)
-        int8_gemm_tile_kernel<kWN, kWM, TN, TM, NS, true>
+        int8_gemm_tile_kernel<kWN, kWM, TN, TM, NS, kLines, true>
             <<<grid, kWave * kWN * kWM, 0, stream>>>(x, xs, w, ws, bias, y, (int)m, (int)n, (int)k, (uint32_t)tiles);
     else
-        int8_gemm_tile_kernel<kWN, kWM, TN, TM, NS, false>
+        int8_gemm_tile_kernel<kWN, kWM, TN, TM, NS, kLines, false>
             <<<grid, kWave * kWN * kWM, 0, stream>>>(x, xs, w, ws, bias, y, (int)m, (int)n, (int)k, (uint32_t)tiles);
     return hipGetLastError();
 }
@@ -571,7 +605,7 @@ hipError_t launch_largest(const int8_t* x, const float* xs, const int8_t* w, con
     const int64_t tiles = ((n + 255) / 256) * ((m + 255) / 256), cus = device_cu_count();
     const int64_t rest = tiles % cus, whole = tiles - rest;
     if (!halves_last_round(tiles, cus))
-        return launch_tile<2, 4, 8, 4, 2>(x, xs, w, ws, bias, y, out_bf16, m, n, k, stream);
+        return launch_tile<2, 4, 8, 4, 2, false>(x, xs, w, ws, bias, y, out_bf16, m, n, k, stream);
     const dim3 grid = grid_of((whole + kXcds - 1) / kXcds * kXcds + (2 * rest + kXcds - 1) / kXcds * kXcds);
     if (out_bf16)
         int8_gemm_mixed_kernel<true>
@@ -599,11 +633,26 @@ const Shape kShapes[] = {
     {16, 16, 2.1f, 0.8f, 0.052f, launch_stream<8, 1, 1>},
     {16, 32, 2.2f, 0.6f, 0.071f, launch_stream<4, 1, 2>},
     {32, 32, 2.3f, 0.7f, 0.118f, launch_stream<4, 2, 2>},
-    {64, 64, 2.3f, 1.1f, 0.202f, launch_tile<2, 4, 2, 1, 4>},
-    {64, 128, 2.3f, 1.5f, 0.311f, launch_tile<2, 4, 2, 2, 3>},
-    {128, 128, 0.4f, 4.0f, 0.468f, launch_tile<4, 4, 2, 2, 3>},
-    {256, 128, 0.4f, 6.5f, 0.772f, launch_tile<4, 4, 4, 2, 3>},
+    {64, 64, 2.3f, 1.1f, 0.202f, launch_tile<2, 4, 2, 1, 4, false>},
+    {64, 128, 2.3f, 1.5f, 0.311f, launch_tile<2, 4, 2, 2, 3, false>},
+    {128, 128, 0.4f, 4.0f, 0.468f, launch_tile<4, 4, 2, 2, 3, false>},
+    {256, 128, 0.4f, 6.5f, 0.772f, launch_tile<4, 4, 4, 2, 3, false>},
     {256, 256, 0.1f, 12.7f, 1.39f, launch_largest},
+};
+
+// The same where rows start inside 128-byte lines (310 calls of such sizes, 0.7 % above the fastest). The tiles up to
+// 256 x 128 then read by lines, with a longer ring; against reading across lines: 130 x 4096 x 4112 9.7 instead of
+// 12.0 us (k = 4096: 8.7), 512 x 4096 x 4112 14.5 instead of 18.2, 2048 x 4096 x 4112 35.9 instead of 39.2. The ring
+// of 256 x 256 tiles has no room for it; still 262 us for 2048 x 28672 x 4112, where 256 x 128 tiles by lines take 322.
+const Shape kShapesInLines[] = {
+    {16, 16, 2.1f, 0.7f, 0.057f, launch_stream<8, 1, 1>},
+    {16, 32, 2.1f, 0.6f, 0.081f, launch_stream<4, 1, 2>},
+    {32, 32, 2.2f, 0.75f, 0.124f, launch_stream<4, 2, 2>},
+    {64, 64, 1.2f, 2.6f, 0.187f, launch_tile<2, 4, 2, 1, 6, true>},
+    {64, 128, 0.9f, 3.2f, 0.286f, launch_tile<2, 4, 2, 2, 5, true>},
+    {128, 128, 0.0f, 4.8f, 0.436f, launch_tile<4, 4, 2, 2, 4, true>},
+    {256, 128, 0.0f, 5.7f, 0.90f, launch_tile<4, 4, 4, 2, 3, true>},
+    {256, 256, 0.0f, 10.5f, 1.56f, launch_largest},
 };
 
 // A last round of halves takes this part of a round of 256 x 256 tiles.
@@ -618,7 +667,9 @@ hipError_t launch_int8_gemm(const int8_t* x, const float* x_scale, const int8_t*
     const float steps = (float)((k + 127) / 128);
     const Shape* best = nullptr;
     float best_us = 0.f;
-    for (const Shape& s : kShapes) {
+    const bool whole_lines =
+        k % 128 == 0 && ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(w)) & 127) == 0;
+    for (const Shape& s : whole_lines ? kShapes : kShapesInLines) {
         const int64_t tiles = ((n + s.rows_w - 1) / s.rows_w) * ((m + s.rows_x - 1) / s.rows_x);
         float rounds = (float)((tiles + cus - 1) / cus);
         if (s.launch == launch_largest && halves_last_round(tiles, cus)) rounds -= 1.f - kHalvesRound;

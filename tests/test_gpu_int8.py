@@ -316,6 +316,9 @@ GEMM_SHAPES = [
     # tiles than compute units, the last round's halved
     (700, 2052, 1040), (515, 2881, 2896), (1020, 4092, 1040), (1020, 4091, 528), (1025, 4100, 1040), (1500, 4097, 1040),
     (2047, 8188, 400), (2047, 8191, 400), (4100, 4097, 1040), (4100, 4100, 1040),
+    # the same tiles over rows of whole 128-byte lines
+    (515, 2881, 1024), (700, 2052, 1152), (1020, 4092, 512), (1020, 4091, 1024), (1025, 4100, 1024), (1500, 4097, 512),
+    (2047, 8188, 512), (4100, 4097, 512),
 ]
 
 
@@ -339,6 +342,27 @@ def test_gemm_output_anywhere(gpu, m, n, dtype, offset):
     """y aligned to its elements only."""
     r = np.random.default_rng(m)
     check_gemm(gpu, random_codes(r, m, 160), random_codes(r, n, 160), dtype, bias=True, offset=offset)
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 50, 256), (40, 200, 512), (300, 2881, 256), (515, 2880, 384), (1020, 4092, 128),
+                                   (1025, 4100, 256)])
+@pytest.mark.parametrize("at_x,at_w", [(0, 16), (48, 0), (112, 64), (64, 112)])
+def test_gemm_operands_inside_lines(gpu, m, n, k, at_x, at_w):
+    """x and w that start inside a 128-byte line, between codes that must not count."""
+    r = np.random.default_rng(m + at_x + at_w)
+
+    def placed(rows, at):
+        buf = torch.full((rows * k + 256,), 127, dtype=torch.int8, device=DEV)
+        assert buf.data_ptr() % 128 == 0
+        codes = random_codes(r, rows, k)
+        t = buf[at:at + rows * k].view(rows, k)
+        t.copy_(torch.from_numpy(codes))
+        return t, codes.astype(np.int64)
+
+    (x, cx), (w, cw) = placed(m, at_x), placed(n, at_w)
+    y = gpu.int8_gemm(x, torch.ones(m, device=DEV), w, torch.ones(n, device=DEV), out_dtype=torch.float32)
+    # sums below 2^14 k <= 2^23 are fp32 numbers
+    assert np.array_equal(y.cpu().numpy().astype(np.int64), (cx.astype(np.float64) @ cw.T.astype(np.float64)))
 
 
 @pytest.mark.parametrize("m", [1, 20, 130, 600])
