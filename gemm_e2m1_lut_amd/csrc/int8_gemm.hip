@@ -100,13 +100,24 @@ dim3 grid_of(int64_t tiles) {
 // of the next under way while one ends, measured the same.)
 
 // Ring stages of a wave. Three or four, with one workgroup on a compute unit instead of two, measured 2 to 10 % slower.
-constexpr int kStages = 2;
+// (By lines a step reads the next stage too, and there are three.)
+template <bool kLines>
+constexpr int kStagesOf = kLines ? 3 : 2;
 
-template <int W, int NT, int MT, bool kBf16Out>
+// Chunks (16 bytes) by which row `row` of a matrix of `chunks` chunks a row at p starts past a 128-byte line.
+__device__ __forceinline__ int past_line(const int8_t* p, uint32_t row, uint32_t chunks) {
+    return (int)(((uint32_t)((uintptr_t)p / 16) + row * chunks) & 7);
+}
+
+// Column `col` (of 128) of a row's next 128, or the one 128 before it, if that is in the line where these start.
+__device__ __forceinline__ int in_line(int col, int past) { return col / 16 + past >= 8 ? col - 128 : col; }
+
+template <int W, int NT, int MT, bool kLines, bool kBf16Out>
 __global__ __launch_bounds__(kWave * W) void int8_gemm_stream_kernel(
     const int8_t* __restrict__ x, const float* __restrict__ xs, const int8_t* __restrict__ w,
     const float* __restrict__ ws, const float* __restrict__ bias, void* __restrict__ y, int m, int n, int k,
     int tiles_n, int tiles_m) {
+    constexpr int kStages = kStagesOf<kLines>;
     constexpr int kRequests = 2 * (NT + MT);            // 1 KB each: eight rows of w or of x
     constexpr int kStage = 1024 * kRequests;
     constexpr int kQuads = NT * MT;                     // 64 quads (four outputs) each
@@ -134,19 +145,26 @@ __global__ __launch_bounds__(kWave * W) void int8_gemm_stream_kernel(
     // l % 8 ^ (row / 2 % 8), so that an operand read (16 rows, one chunk) meets every LDS bank once
     const int col = 16 * ((lane % 8) ^ (lane >> 4));
     const uint32_t off = (uint32_t)(lane / 8) * (uint32_t)k;
+    const uint32_t chunks = (uint32_t)k / 16;           // of a row
+    const int pastw = kLines ? past_line(w, lane / 8, chunks) : 0, pastx = kLines ? past_line(x, lane / 8, chunks) : 0;
     auto issue = [&](int st) __attribute__((always_inline)) {
         const int c0 = 128 * (wave * per + st);
-        const bool live = st < per;
-        const uint32_t even = live && c0 + col < k ? off + (uint32_t)(c0 + col) : kOutOfRange;
-        const uint32_t odd = live && c0 + (col ^ 64) < k ? off + (uint32_t)(c0 + (col ^ 64)) : kOutOfRange;
+        const bool live = st < per + (kLines ? 1 : 0);
+        auto from = [&](int c, int past) __attribute__((always_inline)) {
+            const int at = c0 + (kLines ? in_line(c, past) : c);
+            return live && (uint32_t)at < (uint32_t)k ? off + (uint32_t)at : kOutOfRange;
+        };
+        const uint32_t evenw = from(col, pastw), oddw = from(col ^ 64, pastw);
+        const uint32_t evenx = kLines ? from(col, pastx) : evenw, oddx = kLines ? from(col ^ 64, pastx) : oddw;
         const uint32_t into = base + (st % kStages) * kStage;
 #pragma unroll
         for (int j = 0; j < kRequests; ++j) {
-            const int jj = j < 2 * NT ? j : j - 2 * NT;
-            const uint32_t o = j & 1 ? odd : even;
+            const bool of_w = j < 2 * NT;
+            const int jj = of_w ? j : j - 2 * NT;
+            const uint32_t o = of_w ? (j & 1 ? oddw : evenw) : (j & 1 ? oddx : evenx);
             // (selected once more: "out of range" plus a row offset would wrap)
             const uint32_t v = jj == 0 || o == kOutOfRange ? o : o + (uint32_t)(8 * jj) * (uint32_t)k;
-            lds_load16(j < 2 * NT ? wres : xres, v, __builtin_amdgcn_readfirstlane(into + 1024u * (uint32_t)j));
+            lds_load16(of_w ? wres : xres, v, __builtin_amdgcn_readfirstlane(into + 1024u * (uint32_t)j));
         }
     };
 
@@ -166,6 +184,8 @@ __global__ __launch_bounds__(kWave * W) void int8_gemm_stream_kernel(
     }
 
     const int slot[2] = {r * 128 + 16 * (g ^ (r >> 1)), r * 128 + 16 * ((4 + g) ^ (r >> 1))};
+    // whether chunk 4 h + g of the lane's row of w or x lies in the next stage
+    const int fromw = kLines ? g + past_line(w, r, chunks) : 0, fromx = kLines ? g + past_line(x, r, chunks) : 0;
     i32x4 acc[NT][MT];
 #pragma unroll
     for (int i = 0; i < NT; ++i)
@@ -173,15 +193,17 @@ __global__ __launch_bounds__(kWave * W) void int8_gemm_stream_kernel(
         for (int j = 0; j < MT; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
     for (int s = 0; s < per; ++s) {
         issue(s + kStages - 1);                   // into the slot read in the last turn of this loop
-        wait_vm<kRequests*(kStages - 1)>();       // this step's rows are in LDS
-        const uint8_t* p = ring + (s % kStages) * kStage;
+        wait_vm<kRequests>();                     // this step's rows (by lines, the next one's) are in LDS
+        const int here = (s % kStages) * kStage, next = ((s + 1) % kStages) * kStage;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
+            const uint8_t* pw = ring + (kLines && fromw + 4 * h >= 8 ? next : here) + slot[h];
+            const uint8_t* px = ring + (kLines && fromx + 4 * h >= 8 ? next : here) + slot[h];
             i32x4 a[NT], b[MT];
 #pragma unroll
-            for (int i = 0; i < NT; ++i) a[i] = *reinterpret_cast<const i32x4*>(p + 2048 * i + slot[h]);
+            for (int i = 0; i < NT; ++i) a[i] = *reinterpret_cast<const i32x4*>(pw + 2048 * i);
 #pragma unroll
-            for (int j = 0; j < MT; ++j) b[j] = *reinterpret_cast<const i32x4*>(p + 2048 * (NT + j) + slot[h]);
+            for (int j = 0; j < MT; ++j) b[j] = *reinterpret_cast<const i32x4*>(px + 2048 * (NT + j));
 #pragma unroll
             for (int i = 0; i < NT; ++i)
 #pragma unroll
@@ -222,16 +244,16 @@ __global__ __launch_bounds__(kWave * W) void int8_gemm_stream_kernel(
     store4<kBf16Out>(y, (int64_t)mm * n + nn, v, min(4, n - nn));
 }
 
-template <int W, int NT, int MT>
+template <int W, int NT, int MT, bool kLines>
 hipError_t launch_stream(const int8_t* x, const float* xs, const int8_t* w, const float* ws, const float* bias,
                          void* y, bool out_bf16, int64_t m, int64_t n, int64_t k, hipStream_t stream) {
     const int64_t tiles_n = (n + 16 * NT - 1) / (16 * NT), tiles_m = (m + 16 * MT - 1) / (16 * MT);
     const dim3 grid = grid_of(tiles_n * tiles_m);
     if (out_bf16)
-        int8_gemm_stream_kernel<W, NT, MT, true><<<grid, kWave * W, 0, stream>>>(
+        int8_gemm_stream_kernel<W, NT, MT, kLines, true><<<grid, kWave * W, 0, stream>>>(
             x, xs, w, ws, bias, y, (int)m, (int)n, (int)k, (int)tiles_n, (int)tiles_m);
     else
-        int8_gemm_stream_kernel<W, NT, MT, false><<<grid, kWave * W, 0, stream>>>(
+        int8_gemm_stream_kernel<W, NT, MT, kLines, false><<<grid, kWave * W, 0, stream>>>(
             x, xs, w, ws, bias, y, (int)m, (int)n, (int)k, (int)tiles_n, (int)tiles_m);
     return hipGetLastError();
 }
@@ -313,19 +335,18 @@ __device__ __forceinline__ void tile_body(uint8_t* lds, const int8_t* __restrict
     // step before if this one lies in the row's next line. Rows past the matrix and columns outside [0, k) read out of
     // range: zeros, no memory access.
     const uint32_t chunks = (uint32_t)k / 16;            // of a row
-    auto past_line = [&](const int8_t* p, uint32_t row) __attribute__((always_inline)) {   // chunks
-        return kLines ? (int)(((uint32_t)((uintptr_t)p / 16) + row * chunks) & 7) : 0;
+    auto past = [&](const int8_t* p, uint32_t row) __attribute__((always_inline)) {
+        return kLines ? past_line(p, row, chunks) : 0;
     };
     const int colx = 16 * ((lane % 8) ^ (lane >> 4)), colw = 16 * ((lane % 8) ^ (lane >> 4 & 1));
-    const int pastx = past_line(x, lane / 8), pastw = past_line(w, lane / 8);
-    auto in_line = [&](int col, int past) __attribute__((always_inline)) {
-        return kLines && col / 16 + past >= 8 ? col - KS : col;
-    };
+    const int pastx = past(x, lane / 8), pastw = past(w, lane / 8);
     auto wcol = [&](int i) __attribute__((always_inline)) {
-        return in_line(colw ^ (32 * ((kWLoads * wave + i) & 3)), pastw);
+        const int col = colw ^ (32 * ((kWLoads * wave + i) & 3));
+        return kLines ? in_line(col, pastw) : col;
     };
     auto xcol = [&](int i) __attribute__((always_inline)) {
-        return in_line(colx ^ (64 * ((kXLoads * wave + i) & 1)), pastx);
+        const int col = colx ^ (64 * ((kXLoads * wave + i) & 1));
+        return kLines ? in_line(col, pastx) : col;
     };
     uint32_t woff[kWLoads], xoff[kXLoads];
 #pragma unroll
@@ -366,18 +387,18 @@ __device__ __forceinline__ void tile_body(uint8_t* lds, const int8_t* __restrict
     static_assert(TN % 2 == 0, "operands of w in pairs");
     const uint8_t* wrow = lds + (wn + 8 * (r >> 2) + (r & 3)) * KS;
     const uint8_t* xrow = lds + NR * KS + (wm + r) * KS;
-    // chunk 4 q + g of a row that starts `past` chunks into a line: in the next step's buffer where it is past the line
+    // chunk 4 q + g of a row that starts `chunks_past` into a line: in the next step's buffer where it is past the line
     struct Place { int here, last; };   // from the buffer of the step; of the ring's last buffer
-    auto place = [&](int q, int past) __attribute__((always_inline)) {
-        const int at = 16 * ((4 * q + g) ^ (r >> 1)), next = (4 * q + g + past) >> 3;
+    auto place = [&](int q, int chunks_past) __attribute__((always_inline)) {
+        const int at = 16 * ((4 * q + g) ^ (r >> 1)), next = (4 * q + g + chunks_past) >> 3;
         return Place{at + next * kBufBytes, at - next * (NS - 1) * kBufBytes};
     };
     Place wat[kLines ? 2 : 1][kSlices], xat[kSlices];
 #pragma unroll
     for (int q = 0; q < kSlices; ++q) {
-        xat[q] = place(q, past_line(x, r));
+        xat[q] = place(q, past(x, r));
 #pragma unroll
-        for (int h = 0; h < (kLines ? 2 : 1); ++h) wat[h][q] = place(q, past_line(w, (r & 3) + 4 * h));
+        for (int h = 0; h < (kLines ? 2 : 1); ++h) wat[h][q] = place(q, past(w, (r & 3) + 4 * h));
     }
     auto read_w = [&](int b, int q, int i) __attribute__((always_inline)) {
         const Place& p = wat[kLines ? i % 2 : 0][q];
@@ -433,7 +454,7 @@ __device__ __forceinline__ void tile_body(uint8_t* lds, const int8_t* __restrict
             }
         }
     }
-    // lane 16 g + r holds in acc[i][j], of row wm + 16 j + r of x, columns wn + 32 (i / 2) + 8 g + 4 (i % 2) and on of y
+    // lane 16 g + r holds in acc[i][j], of row wm + 16 j + r of x, columns wn + 32 (i / 2) + 8 g + 4 (i % 2) on of y
     if (n % 4 == 0 && (reinterpret_cast<uintptr_t>(y) & (kBf16Out ? 7 : 15)) == 0) {
         const bool wide = kBf16Out && n % 8 == 0 && (reinterpret_cast<uintptr_t>(y) & 15) == 0;
         float sx[TM];
@@ -630,9 +651,9 @@ struct Shape {
 };
 
 const Shape kShapes[] = {
-    {16, 16, 2.1f, 0.8f, 0.052f, launch_stream<8, 1, 1>},
-    {16, 32, 2.2f, 0.6f, 0.071f, launch_stream<4, 1, 2>},
-    {32, 32, 2.3f, 0.7f, 0.118f, launch_stream<4, 2, 2>},
+    {16, 16, 2.1f, 0.8f, 0.052f, launch_stream<8, 1, 1, false>},
+    {16, 32, 2.2f, 0.6f, 0.071f, launch_stream<4, 1, 2, false>},
+    {32, 32, 2.3f, 0.7f, 0.118f, launch_stream<4, 2, 2, false>},
     {64, 64, 2.3f, 1.1f, 0.202f, launch_tile<2, 4, 2, 1, 4, false>},
     {64, 128, 2.3f, 1.5f, 0.311f, launch_tile<2, 4, 2, 2, 3, false>},
     {128, 128, 0.4f, 4.0f, 0.468f, launch_tile<4, 4, 2, 2, 3, false>},
@@ -640,19 +661,21 @@ const Shape kShapes[] = {
     {256, 256, 0.1f, 12.7f, 1.39f, launch_largest},
 };
 
-// The same where rows start inside 128-byte lines (310 calls of such sizes, 0.7 % above the fastest). The tiles up to
-// 256 x 128 then read by lines, with a longer ring; against reading across lines: 130 x 4096 x 4112 9.7 instead of
-// 12.0 us (k = 4096: 8.7), 512 x 4096 x 4112 14.5 instead of 18.2, 2048 x 4096 x 4112 35.9 instead of 39.2. The ring
-// of 256 x 256 tiles has no room for it; still 262 us for 2048 x 28672 x 4112, where 256 x 128 tiles by lines take 322.
+// The same where rows start inside 128-byte lines (370 calls of such sizes, 0.8 % above the fastest). All but the
+// first and the last shape then read by lines, with a longer ring; against reading across lines: 32 x 4096 x 14352
+// 13.4 instead of 17.1 us (k = 14336: 12.0), 130 x 4096 x 4112 9.7 instead of 12.0 (k = 4096: 8.7), 512 x 4096 x 4112
+// 14.5 instead of 18.2, 2048 x 4096 x 4112 35.9 instead of 39.2. 16 x 16 stream tiles, whose workgroups no longer
+// share a compute unit with a longer ring, take 12.4 us across lines and 15.7 by lines for 1 x 14336 x 4112. The ring
+// of 256 x 256 tiles has no room; across lines they take 262 us for 2048 x 28672 x 4112, 256 x 128 ones by lines 322.
 const Shape kShapesInLines[] = {
-    {16, 16, 2.1f, 0.7f, 0.057f, launch_stream<8, 1, 1>},
-    {16, 32, 2.1f, 0.6f, 0.081f, launch_stream<4, 1, 2>},
-    {32, 32, 2.2f, 0.75f, 0.124f, launch_stream<4, 2, 2>},
-    {64, 64, 1.2f, 2.6f, 0.187f, launch_tile<2, 4, 2, 1, 6, true>},
-    {64, 128, 0.9f, 3.2f, 0.286f, launch_tile<2, 4, 2, 2, 5, true>},
-    {128, 128, 0.0f, 4.8f, 0.436f, launch_tile<4, 4, 2, 2, 4, true>},
-    {256, 128, 0.0f, 5.7f, 0.90f, launch_tile<4, 4, 4, 2, 3, true>},
-    {256, 256, 0.0f, 10.5f, 1.56f, launch_largest},
+    {16, 16, 1.9f, 0.72f, 0.065f, launch_stream<8, 1, 1, false>},
+    {16, 32, 2.4f, 0.7f, 0.078f, launch_stream<4, 1, 2, true>},
+    {32, 32, 1.4f, 1.9f, 0.126f, launch_stream<4, 2, 2, true>},
+    {64, 64, 1.2f, 2.4f, 0.208f, launch_tile<2, 4, 2, 1, 6, true>},
+    {64, 128, 1.0f, 3.0f, 0.294f, launch_tile<2, 4, 2, 2, 5, true>},
+    {128, 128, 0.2f, 4.3f, 0.438f, launch_tile<4, 4, 2, 2, 4, true>},
+    {256, 128, 0.0f, 5.6f, 0.93f, launch_tile<4, 4, 4, 2, 3, true>},
+    {256, 256, 0.0f, 11.0f, 1.48f, launch_largest},
 };
 
 // A last round of halves takes this part of a round of 256 x 256 tiles.
