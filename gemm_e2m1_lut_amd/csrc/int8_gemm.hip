@@ -3,8 +3,9 @@
 //
 // Mathematics: y[m][n] = (sum_k x[m][k] w[n][k]) x_scale[m] w_scale[n] + bias[n].
 // The sum is exact: int8 products in int32 accumulators (|sum| <= 2^14 k, below
-// 2^31 for k <= 131056). It is rounded to fp32 once, then multiplied by the two
-// scales and added to the bias in fp32, and rounded to the output type once.
+// 2^31 for k <= 131056). It is rounded to fp32 once, then multiplied by x_scale
+// in fp32, by w_scale with the bias added in one fma, and rounded to the output
+// type.
 //
 // gfx950 design. Few rows of x: the bytes of w bound the product, and the stream
 // form reads them at 5.0 to 5.7 TB/s (4096 x 14336: 10.3 us for one row of x,
@@ -34,6 +35,11 @@ typedef __bf16 bf16x2v __attribute__((ext_vector_type(2)));
 // bf16 patterns of two floats, nearest even, in the conversion instruction
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2v{lo, hi}), bf16x2v));
+}
+
+// One output. The same in every form, so that a row of y has the same bits whatever the other rows and their number.
+__device__ __forceinline__ float output(int32_t sum, float sx, float sw, float bias) {
+    return fmaf((float)sum * sx, sw, bias);
 }
 
 // v's first `count` (at most four) values to y from element idx on.
@@ -237,10 +243,7 @@ __global__ __launch_bounds__(kWave * W) void int8_gemm_stream_kernel(
     if (mm >= m || nn >= n) return;
     f32x4 v;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        v[e] = (float)sum[e] * sx * sw[e];
-        if (bias != nullptr) v[e] += sb[e];
-    }
+    for (int e = 0; e < 4; ++e) v[e] = output(sum[e], sx, sw[e], bias != nullptr ? sb[e] : 0.f);
     store4<kBf16Out>(y, (int64_t)mm * n + nn, v, min(4, n - nn));
 }
 
@@ -474,7 +477,7 @@ __device__ __forceinline__ void tile_body(uint8_t* lds, const int8_t* __restrict
                 const int mm = m0 + wm + 16 * j + r;
                 f32x4 v[2];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e / 4][e % 4] = (float)acc[i + e / 4][j][e % 4] * sx[j] * sw[e] + bb[e];
+                for (int e = 0; e < 8; ++e) v[e / 4][e % 4] = output(acc[i + e / 4][j][e % 4], sx[j], sw[e], bb[e]);
                 if (mm < m && nn < n) {
                     const int64_t at = (int64_t)mm * n + nn;
                     if (wide) {
@@ -525,7 +528,7 @@ __device__ __forceinline__ void tile_body(uint8_t* lds, const int8_t* __restrict
 #pragma unroll
             for (int e = 0; e < kSides; ++e) {
                 const int c = lane % kSide + kSide * e;
-                const float v = area[br * 16 * TN + 4 * ((c / 4) ^ mix(br)) + c % 4] * sw[e] + bb[e];
+                const float v = fmaf(area[br * 16 * TN + 4 * ((c / 4) ^ mix(br)) + c % 4], sw[e], bb[e]);   // output()
                 const int64_t at = (int64_t)mm * n + (n0 + wn + c);
                 if (mm < m && n0 + wn + c < n) {
                     if constexpr (kBf16Out) reinterpret_cast<uint16_t*>(y)[at] = (uint16_t)pack_bf16(v, 0.f);

@@ -280,10 +280,11 @@ int silu_mul_int8_quantize(const void* gate_up, int dtype, int8_t* q, float* sca
 /*
  * int8_gemm -- y = (x . w^T) with int8 operands, an fp32 scale per row of x
  * (token) and per row of w (output channel), and an optional bias.
- * Operation: y[i][j] = fl32(fl32(fl32(sum) * x_scale[i]) * w_scale[j]) (+
- * bias[j] in fp32), sum = sum over k of x[i][k] w[j][k], exact in int32, the
- * result rounded to the output type to nearest even. Every int8 value is
- * accepted, -128 included.
+ * Operation: y[i][j] = fl32(fl32(fl32(sum) * x_scale[i]) * w_scale[j] +
+ * bias[j]), the last product and the bias in one fma, sum = sum over k of
+ * x[i][k] w[j][k], exact in int32, the result rounded to the output type to
+ * nearest even: the same bits for a row whatever the other rows and their
+ * number. Every int8 value is accepted, -128 included.
  *   x        int8 [m, k]  (16-byte aligned)
  *   x_scale  fp32 [m]
  *   w        int8 [n, k]  (16-byte aligned)

@@ -384,6 +384,32 @@ def test_gemm_each_column_counts_once(gpu, m, n):
     check_gemm(gpu, x, w, "f32")
 
 
+@pytest.mark.parametrize("n,k", [(300, 1040), (301, 1024), (2881, 400), (4096, 512)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("bias", [False, True])
+def test_gemm_rows_do_not_depend_on_the_batch(gpu, n, k, dtype, bias):
+    """Every form gives the formula's bits: fl32(sum) x_scale, then one fma with w_scale and the bias."""
+    r = np.random.default_rng(n)
+    x, w = random_codes(r, 1300, k), random_codes(r, n, k)
+    xs, ws = r.uniform(-1, 1, 1300).astype(np.float32), r.uniform(-1, 1, n).astype(np.float32)
+    b = (r.standard_normal(n) * 100).astype(np.float32) if bias else None
+    dev = lambda a: torch.from_numpy(a).to(DEV)   # noqa: E731
+    dx, dxs, dw, dws, db = dev(x), dev(xs), dev(w), dev(ws), None if b is None else dev(b)
+    whole = gpu.int8_gemm(dx, dxs, dw, dws, bias=db, out_dtype=DT[dtype])
+    for lo, hi in ((0, 1), (3, 20), (7, 40), (100, 200), (17, 500), (250, 1299)):
+        part = gpu.int8_gemm(dx[lo:hi], dxs[lo:hi].clone(), dw, dws, bias=db, out_dtype=DT[dtype])
+        assert torch.equal(part.view(torch.int16 if dtype == "bf16" else torch.int32),
+                           whole[lo:hi].view(torch.int16 if dtype == "bf16" else torch.int32)), (lo, hi)
+    if dtype == "f32":
+        # the fma in 64 bits: its product is exact there, and its sum off by 2^-53 of the larger term before the
+        # rounding to 32 bits, which so differs only where that sum lies next to a halfway value
+        sums = (x[:64].astype(np.float64) @ w.T.astype(np.float64)).astype(np.float32)
+        want = (sums * xs[:64, None]).astype(np.float64) * ws + (0.0 if b is None else b)
+        got = whole[:64].cpu().numpy()
+        near = np.abs(want.astype(np.float32) - got)
+        assert np.all(near <= np.spacing(np.abs(got))) and np.mean(near != 0) < 1e-5
+
+
 @pytest.mark.parametrize("m", [1, 20, 130])
 @pytest.mark.parametrize("low", [0x0000, 0x7FFF, 0x8000, 0x8001])
 def test_gemm_rounds_to_the_nearest_bf16(gpu, m, low):
