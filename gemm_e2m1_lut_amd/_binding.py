@@ -299,39 +299,39 @@ _FLOAT_CODE = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
 INT8_MAX_K = 131056
 
 
-def _need_on(t, name: str, dtype: torch.dtype, shape: tuple, device: torch.device) -> int:
-    """_need, and on `device`; the tensor's address."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device
+def _need_on(t, name: str, dtype: torch.dtype, shape: tuple, device: int) -> int:
+    """_need, and on GPU `device`; the tensor's address."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == device
             and t.is_contiguous()):
         _need(t, name, (dtype,), shape)
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
     return t.data_ptr()
 
 
 def _float_rows(x, name: str) -> tuple:
-    """(rows, columns, dtype code, device) of a [rows, k] fp32 or bf16 tensor."""
+    """(rows, columns, dtype code, GPU) of a [rows, k] fp32 or bf16 tensor."""
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise ValueError(f"{name} must be a [rows, k] tensor")
     code = _FLOAT_CODE.get(x.dtype)
     if code is None or not x.is_cuda or not x.is_contiguous():
         _need(x, name, tuple(_FLOAT_CODE))
     rows, k = x.shape
-    return rows, k, code, x.device
+    return rows, k, code, x.get_device()
 
 
-def _handle_on(stream, device: torch.device) -> int:
-    """The handle of the stream a call on `device` runs on."""
+def _handle_on(stream, device: int) -> int:
+    """The handle of the stream a call on GPU `device` runs on."""
     if stream is None:
         # what torch.cuda.current_stream(device).cuda_stream gives, in 0.1 us instead of 1.9
-        return torch._C._cuda_getCurrentRawStream(device.index)
+        return torch._C._cuda_getCurrentRawStream(device)
     if not hasattr(stream, "cuda_stream"):
         return int(stream)
-    if stream.device != device:
-        raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
+    if stream.device.index != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on cuda:{device}")
     return stream.cuda_stream
 
 
-def _new(shape: tuple, dtype: torch.dtype, device: torch.device, stream) -> torch.Tensor:
+def _new(shape: tuple, dtype: torch.dtype, device: int, stream) -> torch.Tensor:
     """An output; for a stream of the caller's it is allocated for that stream, so that its memory is not still in
     use by work queued on another one."""
     if stream is None:
@@ -343,9 +343,9 @@ def _new(shape: tuple, dtype: torch.dtype, device: torch.device, stream) -> torc
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _call_on(device: torch.device, name: str, *args) -> None:
+def _call_on(device: int, name: str, *args) -> None:
     fn = getattr(_lib or load_library(), name)
-    if torch.cuda.current_device() == device.index:
+    if torch._C._cuda_getDevice() == device:   # torch.cuda.current_device(), without its check for a first call
         status = fn(*args)
     else:   # the launch goes to the tensors' device, whichever is current
         with torch.cuda.device(device):
@@ -354,7 +354,7 @@ def _call_on(device: torch.device, name: str, *args) -> None:
         _check(name, status)
 
 
-def _codes_out(out, rows: int, k: int, device: torch.device, stream):
+def _codes_out(out, rows: int, k: int, device: int, stream):
     if out is None:
         out = (_new((rows, k), torch.int8, device, stream), _new((rows,), torch.float32, device, stream))
     q, scale = out
@@ -418,9 +418,9 @@ def int8_gemm(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale: 
             raise ValueError(f"{name} must be a 2-dimensional tensor")
     m, k = x.shape
     n = w.shape[0]
-    device = w.device
     if not w.is_cuda:
-        raise ValueError(f"w must be on a GPU, got {device}")
+        raise ValueError(f"w must be on a GPU, got {w.device}")
+    device = w.get_device()
     xp = _need_on(x, "x", torch.int8, (m, k), device)
     wp = _need_on(w, "w", torch.int8, (n, k), device)
     xsp = _need_on(x_scale, "x_scale", torch.float32, (m,), device)
