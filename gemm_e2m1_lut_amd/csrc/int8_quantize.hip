@@ -156,22 +156,23 @@ struct Unit<float> {
 // w in (0.5, 1], it is u g / (1 + e^-a) for g >= 0 and u w 2^t g / (1 + e^-a)
 // for g < 0. The power of two joins u last, so neither a very negative gate nor
 // a large `up` overflows on the way. The exponent's argument takes two words of
-// log2 e: with a bf16 gate the product with the first (16 bits) is exact, with
-// an fp32 gate its rounding error is carried along. a is capped at 1000 (e^-1000
-// times any fp32 is 0 in fp32); the factor g keeps NaN and infinity.
+// log2 e (16 bits and the rest for a bf16 gate, 24 for an fp32 one), each in an
+// fma: the first one's product joins t unrounded, whose own rounding (as the
+// argument of ceil) only moves the border between two values of t. a is capped
+// at 1000 (e^-1000 times any fp32 is 0 in fp32); the factor g keeps NaN and
+// infinity.
 template <bool kBf16>
 __device__ __forceinline__ float silu_mul(float g, float u) {
     const float a = fminf(fabsf(g), 1000.f);
-    float hi, lo;
+    float t, e;   // the exponent of 2 is t + e
     if constexpr (kBf16) {
-        hi = a * -0x1.7154p+0f;
-        lo = a * -0x1.d94ae0p-18f;
+        t = ceilf(a * -0x1.7154p+0f);
+        e = fmaf(a, -0x1.d94ae0p-18f, fmaf(a, -0x1.7154p+0f, -t));
     } else {
-        hi = a * -0x1.715476p+0f;
-        lo = fmaf(a, -0x1.4ae0cp-26f, fmaf(a, -0x1.715476p+0f, -hi));
+        t = ceilf(a * -0x1.715476p+0f);
+        e = fmaf(a, -0x1.4ae0cp-26f, fmaf(a, -0x1.715476p+0f, -t));
     }
-    const float t = ceilf(hi);
-    const float w = __builtin_amdgcn_exp2f((hi - t) + lo);
+    const float w = __builtin_amdgcn_exp2f(e);
     const int ti = (int)t;
     const float r = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_ldexpf(w, ti));
     const float n = g < 0.f ? __builtin_amdgcn_ldexpf(u * w, ti) : u;

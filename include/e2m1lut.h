@@ -266,8 +266,9 @@ int rmsnorm_int8_quantize(const void* x, const void* residual, const void* weigh
  * Operation, per row: P = gate / (1 + exp(-gate)) * up, not rounded;
  * Pmax = max |P|; q = the integer nearest to 127 P / Pmax, P evaluated in
  * 64 bits wherever that decides a code; scale = fl32(Pmax / 127).
- * Non-finite rows as in int8_quantize, a |P| of 2^127 or more among them. A
- * row whose |P| are all below 2^-140 may count as a row of zeros.
+ * Non-finite rows as in int8_quantize; a |P| past the fp32 range counts as
+ * infinite (one within 2^-19 of 2^128, relatively, either way). A row whose
+ * |P| are all below 2^-140 may count as a row of zeros.
  *   gate_up  [rows, 2 inter], fp32 or bf16 (dtype), columns [0, inter) gate and
  *            [inter, 2 inter) up, as one product over W13 leaves them (16-byte aligned)
  *   q        int8 [rows, inter], overwritten (16-byte aligned)

@@ -276,6 +276,30 @@ def test_act_moderate_gates(gpu, dtype, k):
     check_act(gpu, np.concatenate([g, u], axis=1), dtype)
 
 
+def spread_products(r, g: np.ndarray, size: float) -> np.ndarray:
+    """up for gates g whose products silu(g) up are spread evenly over -size .. size, so that a row meets every code."""
+    return r.uniform(-1, 1, g.shape) * size * (1.0 + np.exp(-g)) / g
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lo,hi,size", [(-64, -44, 1.0), (-90, -86, 1e-3), (-110, -44, 1e-12), (-44, -1, 1.0),
+                                        (44, 300, 1e3)])
+def test_act_spread_products(gpu, dtype, lo, hi, size):
+    """Gates far from zero in rows whose products reach every code: 1.3 million codes and 320 row maxima a case."""
+    r = np.random.default_rng(int(hi - lo))
+    g = r.uniform(lo, hi, (320, 4096))
+    check_act(gpu, np.concatenate([g, spread_products(r, g, size)], axis=1), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_act_spread_products_in_mixed_units(gpu, dtype):
+    """One gate beyond 44 in every unit of eight, the others' moderate: the evaluation for wide gates on those too."""
+    r = np.random.default_rng(8)
+    g = r.uniform(-44, 44, (320, 4096))
+    g[:, ::8] = r.uniform(-60, -44.5, g[:, ::8].shape)
+    check_act(gpu, np.concatenate([g, spread_products(r, g, 1.0)], axis=1), dtype)
+
+
 # ------------------------------------------------------------------- gemm --
 
 def random_codes(r, rows: int, k: int) -> np.ndarray:
