@@ -152,24 +152,24 @@ struct Unit<float> {
 // -------------------------------------------------------------------- act --
 
 // silu(g) u in fp32, within 2^-20 of the exact value relatively wherever that
-// is a normal fp32 number: with a = |g|, e^-a = w 2^t, t = ceil(-a log2 e) and
-// w in (0.5, 1], it is u g / (1 + e^-a) for g >= 0 and u w 2^t g / (1 + e^-a)
+// is 2^-110 or more: with a = |g|, e^-a = w 2^t, t = ceil(1/2 - a log2 e)
+// and w in (0.35, 0.71], it is u g / (1 + e^-a) for g >= 0 and u w 2^t g / (1 + e^-a)
 // for g < 0. The power of two joins u last, so neither a very negative gate nor
 // a large `up` overflows on the way. The exponent's argument takes two words of
 // log2 e (16 bits and the rest for a bf16 gate, 24 for an fp32 one), each in an
 // fma: the first one's product joins t unrounded, whose own rounding (as the
-// argument of ceil) only moves the border between two values of t. a is capped
-// at 1000 (e^-1000 times any fp32 is 0 in fp32); the factor g keeps NaN and
-// infinity.
+// argument of ceil) only moves the border between two values of t. (That border
+// is kept off w = 1, past which u w could overflow.) a is capped at 1000
+// (e^-1000 times any fp32 is 0 in fp32); the factor g keeps NaN and infinity.
 template <bool kBf16>
 __device__ __forceinline__ float silu_mul(float g, float u) {
     const float a = fminf(fabsf(g), 1000.f);
     float t, e;   // the exponent of 2 is t + e
     if constexpr (kBf16) {
-        t = ceilf(a * -0x1.7154p+0f);
+        t = ceilf(fmaf(a, -0x1.7154p+0f, 0.5f));
         e = fmaf(a, -0x1.d94ae0p-18f, fmaf(a, -0x1.7154p+0f, -t));
     } else {
-        t = ceilf(a * -0x1.715476p+0f);
+        t = ceilf(fmaf(a, -0x1.715476p+0f, 0.5f));
         e = fmaf(a, -0x1.4ae0cp-26f, fmaf(a, -0x1.715476p+0f, -t));
     }
     const float w = __builtin_amdgcn_exp2f(e);

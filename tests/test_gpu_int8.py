@@ -300,6 +300,18 @@ def test_act_spread_products_in_mixed_units(gpu, dtype):
     check_act(gpu, np.concatenate([g, spread_products(r, g, 1.0)], axis=1), dtype)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_act_largest_up(gpu, dtype):
+    """`up` at its type's largest value beside very negative gates, those whose -g log2 e lies next to a whole number
+    (above it or below) among them: products far inside the fp32 range. Every gate with the largest `up`, a row each."""
+    n = np.arange(64, 150, dtype=np.float64)
+    at = (n / np.log2(np.e)).astype(np.float32)
+    g = -np.concatenate([at + d * np.spacing(at) for d in range(-3, 4)]).astype(np.float64)
+    rows = np.tile(g[:, None], (1, 16))
+    u = np.full(rows.shape, float(torch.finfo(DT[dtype]).max)) * np.where(np.arange(16) % 3, 1.0, 2.0**-8)
+    check_act(gpu, np.concatenate([rows, u * np.random.default_rng(1).choice([-1.0, 1.0], u.shape)], axis=1), dtype)
+
+
 # ------------------------------------------------------------------- gemm --
 
 def random_codes(r, rows: int, k: int) -> np.ndarray:
