@@ -312,6 +312,29 @@ def test_act_largest_up(gpu, dtype):
     check_act(gpu, np.concatenate([rows, u * np.random.default_rng(1).choice([-1.0, 1.0], u.shape)], axis=1), dtype)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("first", [3.0, 50.0, -50.0])
+def test_act_products_near_the_fp32_limit(gpu, dtype, first):
+    """Products of 2^127 to 2^128 are finite numbers whatever the other gates of their unit of eight are; a larger one
+    counts as infinite."""
+    r = np.random.default_rng(5)
+    g = r.uniform(1, 2, (6, 64))
+    g[:, ::8] = first
+    u = r.uniform(-1, 1, (6, 64)) * 1e30
+    for row, (gate, up) in enumerate([(4.0, 6e37), (2.0, 1.9e38), (1.5, -2.5e38), (1.25, 3.3e38), (40.0, 8e36)]):
+        g[row, 13], u[row, 13] = gate, up
+        u[row, 20:] *= 1e6
+    check_act(gpu, np.concatenate([g, u], axis=1), dtype)
+    for gate, up in ((4.0, 1e38), (2.0, -2e38), (40.0, 9e36)):   # 1.15, 1.04, 1.06 times 2^128
+        g[0, 13], u[0, 13] = gate, up
+        x, xv = on_gpu(np.concatenate([g, u], axis=1), dtype)
+        q, s = gpu.silu_mul_int8_quantize(x)
+        wq, ws = ref.silu_mul(xv)
+        wq[0], ws[0] = 0, np.nan
+        same_codes(q, wq)
+        same_scale(s, ws, 0)
+
+
 # ------------------------------------------------------------------- gemm --
 
 def random_codes(r, rows: int, k: int) -> np.ndarray:
