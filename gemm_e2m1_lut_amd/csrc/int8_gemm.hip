@@ -684,17 +684,11 @@ const Shape kShapesInLines[] = {
 // A last round of halves takes this part of a round of 256 x 256 tiles.
 constexpr float kHalvesRound = 0.6f;
 
-}  // namespace
-
-hipError_t launch_int8_gemm(const int8_t* x, const float* x_scale, const int8_t* w, const float* w_scale,
-                            const float* bias, void* y, bool out_bf16, int64_t m, int64_t n, int64_t k,
-                            hipStream_t stream) {
-    const int64_t cus = device_cu_count();
+// The entry of kShapes (whole_lines) or kShapesInLines that a call takes on a device of `cus` compute units.
+const Shape& shape_of(int64_t m, int64_t n, int64_t k, bool whole_lines, int64_t cus) {
     const float steps = (float)((k + 127) / 128);
     const Shape* best = nullptr;
     float best_us = 0.f;
-    const bool whole_lines =
-        k % 128 == 0 && ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(w)) & 127) == 0;
     for (const Shape& s : whole_lines ? kShapes : kShapesInLines) {
         const int64_t tiles = ((n + s.rows_w - 1) / s.rows_w) * ((m + s.rows_x - 1) / s.rows_x);
         float rounds = (float)((tiles + cus - 1) / cus);
@@ -705,7 +699,26 @@ hipError_t launch_int8_gemm(const int8_t* x, const float* x_scale, const int8_t*
             best_us = us;
         }
     }
-    return best->launch(x, x_scale, w, w_scale, bias, y, out_bf16, m, n, k, stream);
+    return *best;
+}
+
+}  // namespace
+
+hipError_t launch_int8_gemm(const int8_t* x, const float* x_scale, const int8_t* w, const float* w_scale,
+                            const float* bias, void* y, bool out_bf16, int64_t m, int64_t n, int64_t k,
+                            hipStream_t stream) {
+    const bool whole_lines =
+        k % 128 == 0 && ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(w)) & 127) == 0;
+    return shape_of(m, n, k, whole_lines, device_cu_count())
+        .launch(x, x_scale, w, w_scale, bias, y, out_bf16, m, n, k, stream);
 }
 
 }  // namespace e2m1
+
+int e2m1_int8_gemm_variant(int64_t m, int64_t n, int64_t k, int whole_lines, int cus) {
+    using namespace e2m1;
+    const Shape& s = shape_of(m, n, k, whole_lines != 0, cus);
+    const int at = (int)(&s - (whole_lines ? kShapes : kShapesInLines));
+    const bool halved = s.launch == launch_largest && halves_last_round(((n + 255) / 256) * ((m + 255) / 256), cus);
+    return at + (halved ? 1 : 0);
+}

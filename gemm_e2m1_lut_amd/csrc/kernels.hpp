@@ -84,3 +84,8 @@ hipError_t launch_moe(const uint16_t* x, const uint8_t* w13, const uint8_t* w13s
                       hipStream_t stream);
 
 }  // namespace e2m1
+
+// Which form int8_gemm takes for a product on a device of `cus` compute units: the place of its shape in the table for
+// rows of whole 128-byte lines or in the other one, one more for 256 x 256 tiles whose last round is halved. Host only;
+// exported for the tests, which have to reach every form.
+extern "C" int e2m1_int8_gemm_variant(int64_t m, int64_t n, int64_t k, int whole_lines, int cus);

@@ -145,3 +145,19 @@ def test_binding_refuses():
         g.int8_gemm(i, s, i, s)
     with pytest.raises(ValueError, match="2-dimensional"):
         g.int8_gemm(i[0], s, i, s)
+
+
+def test_gpu_tests_reach_every_form_of_the_product(lib):
+    """The form that the library takes on 256 compute units for each product of test_gpu_int8_forms.py."""
+    import test_gpu_int8_forms as t
+    variant = lib.e2m1_int8_gemm_variant
+    variant.argtypes, variant.restype = [ctypes.c_int64] * 3 + [ctypes.c_int] * 2, ctypes.c_int
+    reached = {True: set(), False: set()}
+    for form, m, n, k, *at in t.WHOLE_LINES + t.INSIDE_LINES:
+        whole = k % 128 == 0 and not any(at)
+        assert variant(m, n, k, whole, 256) == form, (m, n, k, at)
+        reached[whole].add(form)
+        assert n % 4 == 0
+    assert reached[True] == reached[False] == set(range(t.LARGEST_HALVED + 1))
+    for form, m, n, k in t.LONGEST:
+        assert variant(m, n, k, k % 128 == 0, 256) == form, (m, n, k)
