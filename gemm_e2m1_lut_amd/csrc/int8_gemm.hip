@@ -7,18 +7,22 @@
 // in fp32, by w_scale with the bias added in one fma, and rounded to the output
 // type.
 //
-// gfx950 design. Few rows of x: the bytes of w bound the product, and the stream
-// form reads them at 5.0 to 5.7 TB/s (4096 x 14336: 10.3 us for one row of x,
-// 10.6 for 16; a plain read of the same bytes takes 8.8). Many rows: the matrix
-// cores bound it, and under full load their energy does: with the operands of
-// real matrices the chip lowers its clock (1.3 GHz was measured, 2.4 with
-// constant operands). 16x16x64 tiles take less of it than 32x32x32
-// ones (matrix cores alone, normal codes: 4.09 against 3.42 POP/s; 8192^3: 441
-// against 494 us), so they are used throughout: 8192^3 takes 430 us, 2048 x 28672
-// x 4096 218. Both forms feed the matrix
-// cores from LDS rings that direct-to-LDS loads fill in 128-byte row segments
-// (64-byte ones read at half the L2 rate: 66 against 130 GB/s a compute unit).
-// What bounds the tiles in between is LDS traffic and a step's latency.
+// gfx950 design. Few rows of x: the bytes of w bound the product, which are read
+// at 5.3 to 5.6 TB/s (us in a graph: 4096 x 14336 10.6 for one row of x, 11.1 for
+// 16; a plain read of the same bytes takes 8.8). The stream form takes it where
+// its tiles of 16 or 32 rows of w are about one round over the compute units, 64
+// x 64 tiles of the tile form where w has more rows (14336 x 4096, one row of x:
+// 10.8, with 32 x 32 stream tiles 11.1, with 16 x 16 ones 11.7). Many rows: the
+// matrix cores' work bounds it from below. A step of a 256 x 256 tile (128
+// columns) takes 3200 cycles, 2050 of which its matrix instructions fill, at 1.6
+// to 2.0 GHz: with the operands of real matrices the power limit lowers the clock
+// (operands of zero: 2.4 GHz, 3550 cycles). 16x16x64 tiles take less energy
+// than 32x32x32 ones (matrix cores alone, normal codes: 4.09 against 3.42 POP/s;
+// 8192^3: 441 against 494 us), so they are used throughout: 8192^3 takes 430 to
+// 450 us, 2048 x 28672 x 4096 217 to 226. Both forms feed the matrix cores from
+// LDS rings that direct-to-LDS loads fill in 128-byte row segments (64-byte ones
+// read at half the L2 rate: 66 against 130 GB/s a compute unit). What bounds the
+// tiles in between is LDS traffic and a step's latency.
 #include "device.hpp"
 #include "kernels.hpp"
 
@@ -97,10 +101,10 @@ dim3 grid_of(int64_t tiles) {
 // waves split K, a run of 128-column steps each (runs spread a workgroup's
 // requests over the row, and so over the memory channels: with the steps dealt
 // out one by one, every workgroup is at the same columns of rows that lie 4096
-// bytes apart, and 14336 x 4096 takes 13.2 us instead of 11.8). Each wave has
-// an LDS ring of its own (kStages steps of its rows of w and of x, filled by
-// direct-to-LDS requests of 8 rows x 128 bytes), so that no wave waits for
-// another before the end. Lane 16 g + r takes columns 16 g .. + 15 of row r of
+// bytes apart, and 14336 x 4096 took 13.2 us in this form instead of 11.8).
+// Each wave has an LDS ring of its own (kStages steps of its rows of w and of
+// x, filled by direct-to-LDS requests of 8 rows x 128 bytes), so that no wave
+// waits for another before the end. Lane 16 g + r takes columns 16 g .. + 15 of row r of
 // a 64-column half step; 16x16x64 matrix-core tiles, A = w, B = x. The waves'
 // sums meet in LDS. (Workgroups that go on to further tiles, with the requests
 // of the next under way while one ends, measured the same.)
@@ -287,10 +291,11 @@ hipError_t launch_stream(const int8_t* x, const float* xs, const int8_t* w, cons
 // Waves: as many as the registers and pairs of operands allow, though small ones
 // read an operand from LDS more often; a step's latency (barrier, LDS reads,
 // matrix instructions) is hidden by the other waves alone. 130 x 4096 x 4096 in
-// 64 x 64 tiles: 13.0 us with two waves, 10.7 with four, 9.2 with eight; one
-// round of 128 x 128 tiles of 4096 columns 35.6, 22.4 and, with sixteen, 15.7.
-// A workgroup alone passes 41 LDS bytes a cycle for them (64 x 64: 16 KB in 375
-// cycles), the stream form 57, the direct-to-LDS path at most 64. Ring buffers:
+// 64 x 64 tiles: 13.0 us with two waves, 10.7 with four, 9.2 with eight (8.4 to
+// 8.9 with the later steps); one round of 128 x 128 tiles of 4096 columns 35.6,
+// 22.4 and, with sixteen, 15.7. A workgroup alone on its compute unit passes 38
+// LDS bytes a cycle for them (64 x 64: 16 KB in 430 cycles at 2.2 GHz); the
+// direct-to-LDS path at most 64. Ring buffers:
 // as few as let a second workgroup onto the compute unit (64 x 64 with eight
 // instead of four: 512 x 4096 x 4096 18.2 instead of 15.8 us).
 
@@ -665,11 +670,12 @@ const Shape kShapes[] = {
 };
 
 // The same where rows start inside 128-byte lines (370 calls of such sizes, 0.8 % above the fastest). All but the
-// first and the last shape then read by lines, with a longer ring; against reading across lines: 32 x 4096 x 14352
-// 13.4 instead of 17.1 us (k = 14336: 12.0), 130 x 4096 x 4112 9.7 instead of 12.0 (k = 4096: 8.7), 512 x 4096 x 4112
-// 14.5 instead of 18.2, 2048 x 4096 x 4112 35.9 instead of 39.2. 16 x 16 stream tiles, whose workgroups no longer
-// share a compute unit with a longer ring, take 12.4 us across lines and 15.7 by lines for 1 x 14336 x 4112. The ring
-// of 256 x 256 tiles has no room; across lines they take 262 us for 2048 x 28672 x 4112, 256 x 128 ones by lines 322.
+// first and the last shape then read by lines, with a longer ring; against reading across lines, in a graph: 32 x 4096
+// x 14352 13.4 instead of 17.1 us (k = 14336: 12.0), 130 x 4096 x 4112 9.7 instead of 12.0 (k = 4096: 8.8), 512 x 4096
+// x 4112 14.5 instead of 18.2, 2048 x 4096 x 4112 35.9 instead of 39.2. 16 x 16 stream tiles, whose workgroups no
+// longer share a compute unit with a longer ring, take 12.4 us across lines and 15.7 by lines for 1 x 14336 x 4112.
+// The ring of 256 x 256 tiles has no room; across lines they take 262 us for 2048 x 28672 x 4112, 256 x 128 ones by
+// lines 322.
 const Shape kShapesInLines[] = {
     {16, 16, 1.9f, 0.72f, 0.065f, launch_stream<8, 1, 1, false>},
     {16, 32, 2.4f, 0.7f, 0.078f, launch_stream<4, 1, 2, true>},

@@ -22,12 +22,13 @@
 // most 32 bits). Outside 2^-100 <= pmax <= 2^100 the row is first multiplied by
 // 2^64 or 2^-64, so that neither 127 / pmax nor a product leaves the fp32
 // range; elements that this flushes are below half a code.
-// silu(gate) up is not an fp32 number. Its fp32 evaluation is within 8.4 * 2^-24
-// of it (relatively; the sum of the roundings of exp2, of 1 + e^-a, of the
-// reciprocal, one ulp each for the hardware's, and of four products), so the
-// largest magnitude is taken in fp64 over the elements within 2^-18 of the
-// largest fp32 value, and codes whose v (then within 127 * 11.4 * 2^-24 < 2^-13.5)
-// is within kNearAct of a half-integer are decided in fp64 (one element in 5000).
+// silu(gate) up is not an fp32 number. Its fp32 evaluation is within 9.4 * 2^-24
+// of it (relatively; the sum of the roundings of the exponent, of exp2, of 1 +
+// e^-a, of the reciprocal, one ulp each for the hardware's, and of three
+// products), so the largest magnitude is taken in fp64 over the elements within
+// 2^-18 of the largest fp32 value, and codes whose v (then within 127 * 12.4 *
+// 2^-24 < 1.54 * 2^-14) is within kNearAct of a half-integer are decided in fp64
+// (one element in 5000).
 //
 // The largest magnitude is an integer maximum of the magnitude patterns: a NaN
 // has the largest pattern, so a row that holds a NaN or an infinity (or whose
@@ -480,10 +481,14 @@ hipError_t dispatch(const void* xv, const void* resv, const void* wv, float eps,
     const int64_t units = k / 8;
 #define E2M1_ROWS(TPR, UNITS, LONG) \
     launch_rows<T, kOp, TPR, UNITS, LONG>(x, r, w, eps, h, q, scale, rows, k, stream)
-    // Few elements: as many threads a row as it has units, for the latency. Many: two units or more a thread, for
-    // the bytes in flight. (bf16, us, the one against the other: norm with residual, k 4096, 512 rows 5.4 / 5.5, 2000
-    // rows 12.6 / 12.3; plain, 14336 x 4096, 43.1 / 34.6; k 8192, 512 rows 5.5 / 5.4, 2000 rows 15.7 / 12.8; act,
-    // k 14336, 512 rows 11.4 / 12.0, 2000 rows 34.7 / 32.7; k 1024, 2000 rows 4.0 / 4.1, 20000 rows 16.3 / 14.8.)
+    // Few elements: as many threads a row as it has units, for the latency. Many: two units or more a thread, for the
+    // bytes in flight. us in a graph, the one against the other, bf16:
+    //   plain               1 x 4096 2.7 / 2.9, 128 x 1024 2.8 / 3.7, 1024 x 4096 5.1 / 5.0, 8192 x 4096 25.4 / 21.5
+    //   norm with residual  1 x 4096 3.2 / 3.6, 128 x 4096 3.8 / 4.3, 2000 x 4096 13.0 / 12.7, 8192 x 8192 90.4 / 82.7
+    //   act                 1 x 14336 4.9 / 5.3, 16 x 14336 5.6 / 6.1, 1024 x 8192 12.4 / 11.6, 8192 x 4096 37.5 / 32.8
+    // fp32, whose units have twice the bytes: the same for few (plain 128 x 1024 2.7 / 2.9, act 16 x 14336 5.9 / 6.5),
+    // and for many not enough on either side for a rule of its own (8192 x 4096: plain 30.6 / 31.1, norm 78.4 / 79.3,
+    // act 53.1 / 57.6; 2000 x 8192: act 31.2 / 29.2).
     const bool many = rows * k >= (int64_t)6 << 20;
     if (units <= 64) {
         E2M1_ROWS(64, 1, false);
