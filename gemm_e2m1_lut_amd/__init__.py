@@ -11,7 +11,8 @@ ternary_wl_gemv, nvfp4_embedding_gather, mxfp4_moe_gemm (+
 mxfp4_moe_workspace_size, and mxfp4_moe_gemm_noalloc for callers that cannot
 allocate), nm_spmm (N:M structured-sparse weights), the
 encoders mxfp4_quantize, nvfp4_quantize, and the 8-bit layer: int8_gemm with
-int8_quantize, rmsnorm_int8_quantize and silu_mul_int8_quantize for its operands.
+int8_quantize, rmsnorm_int8_quantize and silu_mul_int8_quantize for its operands, and an attention layer's 4-bit
+cache: mxfp4_cache_write, norm_rope_mxfp4_cache_write, mxfp4_cache_read, mxfp4_attention (+ workspace size).
 """
 from ._binding import (  # noqa: F401
     ABI_VERSION,
@@ -31,11 +32,16 @@ from ._binding import (  # noqa: F401
     int8_quantize,
     library_path,
     load_library,
+    mxfp4_attention,
+    mxfp4_attention_workspace_size,
+    mxfp4_cache_read,
+    mxfp4_cache_write,
     mxfp4_moe_gemm,
     mxfp4_moe_gemm_noalloc,
     MOE_NOALLOC_WORKSPACE_BYTES,
     mxfp4_moe_workspace_size,
     mxfp4_quantize,
+    norm_rope_mxfp4_cache_write,
     nvfp4_embedding_gather,
     nvfp4_quantize,
     nm_spmm,

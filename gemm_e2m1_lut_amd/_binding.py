@@ -64,6 +64,13 @@ def load_library() -> ctypes.CDLL:
         "rmsnorm_int8_quantize": (ctypes.c_int, [vp, vp, vp, i32, ctypes.c_float, vp, vp, vp, i64, i64, vp]),
         "silu_mul_int8_quantize": (ctypes.c_int, [vp, i32, vp, vp, i64, i64, vp]),
         "int8_gemm": (ctypes.c_int, [vp, vp, vp, vp, vp, vp, i32, i64, i64, i64, vp]),
+        "mxfp4_cache_write": (ctypes.c_int, [vp, vp, i32, i64, i64, vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, vp, vp]),
+        "norm_rope_mxfp4_cache_write": (ctypes.c_int, [vp, i32, i64, vp, vp, ctypes.c_float, vp, i64, i64, i32, vp, vp,
+                                                       vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, i64, vp, vp]),
+        "mxfp4_cache_read": (ctypes.c_int, [vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, vp, vp]),
+        "mxfp4_attention_workspace_size": (sz, [i64, i64, i64, i64, i64]),
+        "mxfp4_attention": (ctypes.c_int, [vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, ctypes.c_float, i32, i64, vp, vp, sz,
+                                           i64, i64, i64, i64, i64, i64, i64, i64, vp, vp]),
         "ternary_gemv": (ctypes.c_int, [vp, vp, vp, vp, i64, i64, vp]),
         "ternary_gemm_workspace_size": (sz, [i64, i64, i64]),
         "ternary_gemm": (ctypes.c_int, [vp, vp, vp, vp, vp, sz, i64, i64, i64, vp]),
@@ -436,6 +443,189 @@ def int8_gemm(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale: 
         out = _new((m, n), out_dtype, device, stream)
     yp = _need_on(out, "out", out_dtype, (m, n), device)
     _call_on(device, "int8_gemm", xp, xsp, wp, wsp, bp, yp, code, m, n, k, handle)
+    return out
+
+
+# -------------------------------------------------------- attention cache --
+
+def _cache_of(cache) -> tuple:
+    """(addresses, pages, kv heads, page size, head dim, GPU) of (k_codes, k_scales, v_codes, v_scales)."""
+    if not isinstance(cache, (tuple, list)) or len(cache) != 4:
+        raise ValueError("cache must hold four tensors (k_codes, k_scales, v_codes, v_scales)")
+    k_codes = cache[0]
+    if not isinstance(k_codes, torch.Tensor) or k_codes.dim() != 4:
+        raise ValueError("cache[0] must be a [pages, kv_heads, page_size, head_dim / 2] tensor")
+    if not k_codes.is_cuda:
+        raise ValueError(f"cache[0] must be on a GPU, got {k_codes.device}")
+    device = k_codes.get_device()
+    pages, heads, page, half = k_codes.shape
+    codes, scales = (pages, heads, page, half), (pages, heads, page, half // 16)
+    ptrs = (_need_on(k_codes, "cache[0]", torch.uint8, codes, device),
+            _need_on(cache[1], "cache[1]", torch.uint8, scales, device),
+            _need_on(cache[2], "cache[2]", torch.uint8, codes, device),
+            _need_on(cache[3], "cache[3]", torch.uint8, scales, device))
+    return ptrs, pages, heads, page, 2 * half, device
+
+
+def _token_rows(t, name: str, dtypes, shape: tuple, device: int) -> int:
+    """Checks a tensor of `shape` whose tokens (the first extent) may be further apart than their rows; that distance."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
+    if t.shape != shape or t.get_device() != device:
+        raise ValueError(f"{name} is {tuple(t.shape)} on {t.device}, expected {shape} on cuda:{device}")
+    row = 1
+    for n in shape[1:]:
+        row *= n
+    if t.is_contiguous():
+        return row
+    if len(shape) == 3 and t.stride()[1:] == (shape[2], 1) or len(shape) == 2 and t.stride(1) == 1:
+        if shape[0] < 2:
+            return row
+        if t.stride(0) >= row:
+            return t.stride(0)
+    raise ValueError(f"{name}: a token's values must be contiguous and the tokens apart, got strides {t.stride()}")
+
+
+def _err_ptr(err_flag, device: int):
+    return None if err_flag is None else _need_on(err_flag, "err_flag", torch.int32, (1,), device)
+
+
+_FLOATS = (torch.float32, torch.bfloat16)
+
+
+def mxfp4_cache_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cache, err_flag: torch.Tensor | None = None,
+                      stream=None):
+    """Keys and values, bf16 or fp32 [tokens, kv_heads, head_dim] (slices along the tokens are fine), quantized into
+    `cache` at int64 slots [tokens] (negative: left out). Returns the cache.
+
+    cache: (k_codes, k_scales, v_codes, v_scales), uint8 [pages, kv_heads, page_size, head_dim / 2] and [..,
+    head_dim / 32]."""
+    ptrs, pages, heads, page, dim, device = _cache_of(cache)
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("k must be a [tokens, kv_heads, head_dim] tensor")
+    tokens = k.shape[0]
+    ks = _token_rows(k, "k", _FLOATS, (tokens, heads, dim), device)
+    vs = _token_rows(v, "v", (k.dtype,), (tokens, heads, dim), device)
+    sp = _need_on(slots, "slots", torch.int64, (tokens,), device)
+    _call_on(device, "mxfp4_cache_write", k.data_ptr(), v.data_ptr(), _FLOAT_CODE[k.dtype], ks, vs, sp, *ptrs, tokens,
+             heads, dim, pages, page, _err_ptr(err_flag, device), _handle_on(stream, device))
+    return cache
+
+
+def norm_rope_mxfp4_cache_write(qkv: torch.Tensor, cos_sin: torch.Tensor | None, positions: torch.Tensor | None,
+                                slots: torch.Tensor, cache, q_weight: torch.Tensor | None = None,
+                                k_weight: torch.Tensor | None = None, eps: float = 1e-6, interleaved: bool = False,
+                                out: torch.Tensor | None = None, err_flag: torch.Tensor | None = None,
+                                stream=None) -> torch.Tensor:
+    """Rows of a fused product, bf16 or fp32 [tokens, (heads + 2 kv_heads) * head_dim], q | k | v: each query and key
+    head normed (where its weight [head_dim] is given) and rotated, keys and values quantized into `cache` at `slots`.
+    Returns the queries, bf16 [tokens, heads, head_dim].
+
+    cos_sin: fp32 [max_pos, rot_dim], cosines then sines; positions int64 [tokens]; both None: no rotation."""
+    ptrs, pages, kv_heads, page, dim, device = _cache_of(cache)
+    if not isinstance(qkv, torch.Tensor) or qkv.dim() != 2:
+        raise ValueError("qkv must be a [tokens, (heads + 2 kv_heads) * head_dim] tensor")
+    tokens, width = qkv.shape
+    heads = width // dim - 2 * kv_heads if dim else -1
+    if heads < 0 or width != (heads + 2 * kv_heads) * dim:
+        raise ValueError(f"qkv has {width} columns, expected those of some query heads and {kv_heads} key and value "
+                         f"heads of {dim}")
+    stride = _token_rows(qkv, "qkv", _FLOATS, (tokens, width), device)
+    sp = _need_on(slots, "slots", torch.int64, (tokens,), device)
+    wq = None if q_weight is None else _need_on(q_weight, "q_weight", qkv.dtype, (dim,), device)
+    wk = None if k_weight is None else _need_on(k_weight, "k_weight", qkv.dtype, (dim,), device)
+    if (cos_sin is None) != (positions is None):
+        raise ValueError("cos_sin and positions go together")
+    cp = pp = None
+    max_pos = rot = 0
+    if cos_sin is not None:
+        if not isinstance(cos_sin, torch.Tensor) or cos_sin.dim() != 2:
+            raise ValueError("cos_sin must be a [max_pos, rot_dim] tensor")
+        max_pos, rot = cos_sin.shape
+        cp = _need_on(cos_sin, "cos_sin", torch.float32, (max_pos, rot), device)
+        pp = _need_on(positions, "positions", torch.int64, (tokens,), device)
+    handle = _handle_on(stream, device)
+    if out is None:
+        out = _new((tokens, heads, dim), torch.bfloat16, device, stream)
+    op = _need_on(out, "out", torch.bfloat16, (tokens, heads, dim), device)
+    _call_on(device, "norm_rope_mxfp4_cache_write", qkv.data_ptr(), _FLOAT_CODE[qkv.dtype], stride, wq, wk, eps, cp,
+             max_pos, rot, int(interleaved), pp, sp, op, *ptrs, tokens, heads, kv_heads, dim, pages, page,
+             _err_ptr(err_flag, device), handle)
+    return out
+
+
+def mxfp4_cache_read(cache, slots: torch.Tensor, out: tuple[torch.Tensor, torch.Tensor] | None = None,
+                     err_flag: torch.Tensor | None = None, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """The cache's tokens at int64 slots [tokens] -> (k, v), bf16 [tokens, kv_heads, head_dim]; zeros for a negative
+    slot."""
+    ptrs, pages, heads, page, dim, device = _cache_of(cache)
+    if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
+        raise ValueError("slots must be a [tokens] tensor")
+    tokens = slots.shape[0]
+    sp = _need_on(slots, "slots", torch.int64, (tokens,), device)
+    handle = _handle_on(stream, device)
+    if out is None:
+        out = tuple(_new((tokens, heads, dim), torch.bfloat16, device, stream) for _ in range(2))
+    k, v = out
+    kp = _need_on(k, "out[0]", torch.bfloat16, (tokens, heads, dim), device)
+    vp = _need_on(v, "out[1]", torch.bfloat16, (tokens, heads, dim), device)
+    _call_on(device, "mxfp4_cache_read", *ptrs, sp, kp, vp, tokens, heads, dim, pages, page, _err_ptr(err_flag, device),
+             handle)
+    return out
+
+
+def mxfp4_attention_workspace_size(tokens: int, seqs: int, heads: int, kv_heads: int, head_dim: int) -> int:
+    """Bytes mxfp4_attention needs on the current device."""
+    size = (_lib or load_library()).mxfp4_attention_workspace_size(tokens, seqs, heads, kv_heads, head_dim)
+    if size == _NO_SIZE:
+        raise ValueError("invalid attention extents")
+    return size
+
+
+_NO_SIZE = ctypes.c_size_t(-1).value
+
+
+def mxfp4_attention(q: torch.Tensor, cache, page_table: torch.Tensor, kv_lens: torch.Tensor, q_offsets: torch.Tensor,
+                    scale: float | None = None, causal: bool = True, window: int = 0,
+                    sinks: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                    workspace: torch.Tensor | None = None, err_flag: torch.Tensor | None = None,
+                    stream=None) -> torch.Tensor:
+    """Attention of packed query rows q, bf16 [tokens, heads, head_dim], over the paged cache -> bf16 of that shape.
+
+    Sequence s: query rows q_offsets[s] .. q_offsets[s + 1] - 1 (int32 [seqs + 1]), the last of its kv_lens[s] (int32
+    [seqs]) cached tokens, which are on the pages page_table[s] (int32 [seqs, width]). scale: head_dim ** -0.5 when not
+    given; window: keys a query sees, its own included (0: all before it); sinks: fp32 [heads], a logit that takes part
+    in the softmax and has no value. `workspace` (uint8, mxfp4_attention_workspace_size bytes) is allocated when not
+    given."""
+    ptrs, pages, kv_heads, page, dim, device = _cache_of(cache)
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a [tokens, heads, head_dim] tensor")
+    tokens, heads = q.shape[:2]
+    stride = _token_rows(q, "q", (torch.bfloat16,), (tokens, heads, dim), device)
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise ValueError("page_table must be a [seqs, width] tensor")
+    seqs, width = page_table.shape
+    tp = _need_on(page_table, "page_table", torch.int32, (seqs, width), device)
+    lp = _need_on(kv_lens, "kv_lens", torch.int32, (seqs,), device)
+    fp = _need_on(q_offsets, "q_offsets", torch.int32, (seqs + 1,), device)
+    np_ = None if sinks is None else _need_on(sinks, "sinks", torch.float32, (heads,), device)
+    handle = _handle_on(stream, device)
+    if out is None:
+        out = _new((tokens, heads, dim), torch.bfloat16, device, stream)
+    op = _need_on(out, "out", torch.bfloat16, (tokens, heads, dim), device)
+    if workspace is None:
+        with torch.cuda.device(device):
+            need = mxfp4_attention_workspace_size(tokens, seqs, heads, kv_heads, dim)
+        workspace = _new((need,), torch.uint8, device, stream)
+    elif not (isinstance(workspace, torch.Tensor) and workspace.dtype is torch.uint8 and workspace.get_device() == device
+              and workspace.is_contiguous()):
+        _need(workspace, "workspace", _U8)
+        raise ValueError(f"workspace is on {workspace.device}, expected cuda:{device}")
+    _call_on(device, "mxfp4_attention", q.data_ptr(), stride, *ptrs, tp, lp, fp, np_,
+             dim ** -0.5 if scale is None else scale, int(causal), window, op, workspace.data_ptr(), workspace.numel(),
+             tokens, seqs, heads, kv_heads, dim, pages, page, width, _err_ptr(err_flag, device), handle)
     return out
 
 

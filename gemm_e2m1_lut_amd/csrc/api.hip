@@ -272,6 +272,141 @@ int int8_gemm(const int8_t* x, const float* x_scale, const int8_t* w, const floa
                                                 as_stream(stream)));
 }
 
+// Extents of a paged cache: 0, or why not.
+static int cache_shape(int64_t kv_heads, int64_t head_dim, int64_t pages, int64_t page_size) {
+    if (kv_heads < 1 || kv_heads > E2M1_CACHE_MAX_HEADS || (head_dim != 64 && head_dim != 128) || pages < 0 ||
+        pages > INT_MAX || page_size < 16 || page_size > E2M1_CACHE_MAX_PAGE || (page_size & (page_size - 1)) != 0)
+        return E2M1_ERR_SHAPE;
+    return E2M1_OK;
+}
+
+static int cache_pointers(const void* k_codes, const void* k_scales, const void* v_codes, const void* v_scales,
+                          int64_t pages) {
+    if (pages > 0 && (!k_codes || !k_scales || !v_codes || !v_scales)) return E2M1_ERR_NULL;
+    if (!aligned(k_codes, 16) || !aligned(k_scales, 16) || !aligned(v_codes, 16) || !aligned(v_scales, 16))
+        return E2M1_ERR_ALIGN;
+    return E2M1_OK;
+}
+
+static e2m1::CacheView cache_view(const uint8_t* k_codes, const uint8_t* k_scales, const uint8_t* v_codes,
+                                  const uint8_t* v_scales, int64_t kv_heads, int64_t head_dim, int64_t pages,
+                                  int64_t page_size) {
+    e2m1::CacheView c;
+    c.k_codes = const_cast<uint8_t*>(k_codes);
+    c.k_scales = const_cast<uint8_t*>(k_scales);
+    c.v_codes = const_cast<uint8_t*>(v_codes);
+    c.v_scales = const_cast<uint8_t*>(v_scales);
+    c.slots = pages * page_size;
+    c.heads = (int)kv_heads;
+    c.head_dim = (int)head_dim;
+    c.page_bits = __builtin_ctzll((unsigned long long)page_size);
+    return c;
+}
+
+// A row stride in elements: no less than the row, whole 16-byte units, the last row's end within 2^62 bytes.
+static bool stride_ok(int64_t stride, int64_t row, int64_t tokens, int dtype) {
+    return stride >= row && stride % (dtype == E2M1_DTYPE_BF16 ? 8 : 4) == 0 && mul_ok(stride, tokens) &&
+           stride * tokens <= ((int64_t)1 << 60);
+}
+
+int mxfp4_cache_write(const void* k, const void* v, int dtype, int64_t k_stride, int64_t v_stride, const int64_t* slots,
+                      uint8_t* k_codes, uint8_t* k_scales, uint8_t* v_codes, uint8_t* v_scales, int64_t tokens,
+                      int64_t kv_heads, int64_t head_dim, int64_t pages, int64_t page_size, int32_t* err_flag,
+                      void* stream) {
+    if (dtype != E2M1_DTYPE_F32 && dtype != E2M1_DTYPE_BF16) return E2M1_ERR_DTYPE;
+    if (int bad = cache_shape(kv_heads, head_dim, pages, page_size)) return bad;
+    if (tokens < 0 || tokens > E2M1_CACHE_MAX_TOKENS) return E2M1_ERR_SHAPE;
+    if (tokens == 0) return E2M1_OK;
+    if (!stride_ok(k_stride, kv_heads * head_dim, tokens, dtype) ||
+        !stride_ok(v_stride, kv_heads * head_dim, tokens, dtype))
+        return E2M1_ERR_SHAPE;
+    if (!k || !v || !slots) return E2M1_ERR_NULL;
+    if (int bad = cache_pointers(k_codes, k_scales, v_codes, v_scales, pages)) return bad;
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 8) || !aligned(err_flag, 4)) return E2M1_ERR_ALIGN;
+    const e2m1::CacheView c = cache_view(k_codes, k_scales, v_codes, v_scales, kv_heads, head_dim, pages, page_size);
+    return launch_status(e2m1::launch_cache_write(k, v, dtype == E2M1_DTYPE_BF16, k_stride, v_stride, slots, c, tokens,
+                                                  err_flag, as_stream(stream)));
+}
+
+int norm_rope_mxfp4_cache_write(const void* qkv, int dtype, int64_t qkv_stride, const void* q_weight,
+                                const void* k_weight, float eps, const float* cos_sin, int64_t max_pos,
+                                int64_t rot_dim, int interleaved, const int64_t* positions, const int64_t* slots,
+                                uint16_t* q_out, uint8_t* k_codes, uint8_t* k_scales, uint8_t* v_codes,
+                                uint8_t* v_scales, int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim,
+                                int64_t pages, int64_t page_size, int32_t* err_flag, void* stream) {
+    if (dtype != E2M1_DTYPE_F32 && dtype != E2M1_DTYPE_BF16) return E2M1_ERR_DTYPE;
+    if (int bad = cache_shape(kv_heads, head_dim, pages, page_size)) return bad;
+    if (tokens < 0 || tokens > E2M1_CACHE_MAX_TOKENS || heads < 0 || heads > E2M1_CACHE_MAX_HEADS || max_pos < 0 ||
+        max_pos > INT_MAX || rot_dim < 0 || rot_dim > head_dim || rot_dim % 16 != 0 || !(eps >= 0.0f) || eps > FLT_MAX)
+        return E2M1_ERR_SHAPE;
+    if (tokens == 0) return E2M1_OK;
+    if (!stride_ok(qkv_stride, (heads + 2 * kv_heads) * head_dim, tokens, dtype)) return E2M1_ERR_SHAPE;
+    if (!qkv || !slots || (heads > 0 && !q_out) || (rot_dim > 0 && (!positions || (max_pos > 0 && !cos_sin))))
+        return E2M1_ERR_NULL;
+    if (int bad = cache_pointers(k_codes, k_scales, v_codes, v_scales, pages)) return bad;
+    if (!aligned(qkv, 16) || !aligned(q_weight, 16) || !aligned(k_weight, 16) || !aligned(cos_sin, 16) ||
+        !aligned(positions, 8) || !aligned(slots, 8) || !aligned(q_out, 16) || !aligned(err_flag, 4))
+        return E2M1_ERR_ALIGN;
+    const e2m1::CacheView c = cache_view(k_codes, k_scales, v_codes, v_scales, kv_heads, head_dim, pages, page_size);
+    const e2m1::NormRope a = {qkv,   qkv_stride, q_weight, k_weight, eps, cos_sin, max_pos, (int)rot_dim, interleaved != 0,
+                              positions, slots, q_out, (int)heads};
+    return launch_status(
+        e2m1::launch_norm_rope_write(a, dtype == E2M1_DTYPE_BF16, c, tokens, err_flag, as_stream(stream)));
+}
+
+int mxfp4_cache_read(const uint8_t* k_codes, const uint8_t* k_scales, const uint8_t* v_codes, const uint8_t* v_scales,
+                     const int64_t* slots, uint16_t* k_out, uint16_t* v_out, int64_t tokens, int64_t kv_heads,
+                     int64_t head_dim, int64_t pages, int64_t page_size, int32_t* err_flag, void* stream) {
+    if (int bad = cache_shape(kv_heads, head_dim, pages, page_size)) return bad;
+    if (tokens < 0 || tokens > E2M1_CACHE_MAX_TOKENS) return E2M1_ERR_SHAPE;
+    if (tokens == 0) return E2M1_OK;
+    if (!slots || !k_out || !v_out) return E2M1_ERR_NULL;
+    if (int bad = cache_pointers(k_codes, k_scales, v_codes, v_scales, pages)) return bad;
+    if (!aligned(slots, 8) || !aligned(k_out, 16) || !aligned(v_out, 16) || !aligned(err_flag, 4)) return E2M1_ERR_ALIGN;
+    const e2m1::CacheView c = cache_view(k_codes, k_scales, v_codes, v_scales, kv_heads, head_dim, pages, page_size);
+    return launch_status(e2m1::launch_cache_read(c, slots, k_out, v_out, tokens, err_flag, as_stream(stream)));
+}
+
+static bool attention_shape_ok(int64_t tokens, int64_t seqs, int64_t heads, int64_t kv_heads, int64_t head_dim) {
+    return tokens >= 0 && tokens <= E2M1_CACHE_MAX_TOKENS && seqs >= 0 && seqs <= E2M1_CACHE_MAX_TOKENS && kv_heads >= 1 &&
+           heads >= kv_heads && heads <= E2M1_CACHE_MAX_HEADS && heads % kv_heads == 0 &&
+           (head_dim == 64 || head_dim == 128);
+}
+
+size_t mxfp4_attention_workspace_size(int64_t tokens, int64_t seqs, int64_t heads, int64_t kv_heads, int64_t head_dim) {
+    if (!attention_shape_ok(tokens, seqs, heads, kv_heads, head_dim)) return SIZE_MAX;
+    return tokens == 0 || seqs == 0 ? 0 : e2m1::attention_workspace_bytes(tokens, seqs, heads, kv_heads, head_dim);
+}
+
+int mxfp4_attention(const uint16_t* q, int64_t q_stride, const uint8_t* k_codes, const uint8_t* k_scales,
+                    const uint8_t* v_codes, const uint8_t* v_scales, const int32_t* page_table, const int32_t* kv_lens,
+                    const int32_t* q_offsets, const float* sinks, float scale, int causal, int64_t window,
+                    uint16_t* out, void* workspace, size_t workspace_bytes, int64_t tokens, int64_t seqs, int64_t heads,
+                    int64_t kv_heads, int64_t head_dim, int64_t pages, int64_t page_size, int64_t table_width,
+                    int32_t* err_flag, void* stream) {
+    if (!attention_shape_ok(tokens, seqs, heads, kv_heads, head_dim) || table_width < 0 || window < 0 ||
+        (window > 0 && !causal) || !(scale >= 0.0f) || scale > FLT_MAX)
+        return E2M1_ERR_SHAPE;
+    if (int bad = cache_shape(kv_heads, head_dim, pages, page_size)) return bad;
+    if (table_width > INT_MAX / page_size || !mul_ok(table_width, seqs)) return E2M1_ERR_SHAPE;
+    if (tokens == 0 || seqs == 0) return E2M1_OK;
+    if (!stride_ok(q_stride, heads * head_dim, tokens, E2M1_DTYPE_BF16)) return E2M1_ERR_SHAPE;
+    if (!q || !kv_lens || !q_offsets || !out || (table_width > 0 && !page_table)) return E2M1_ERR_NULL;
+    if (int bad = cache_pointers(k_codes, k_scales, v_codes, v_scales, pages)) return bad;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(page_table, 4) || !aligned(kv_lens, 4) ||
+        !aligned(q_offsets, 4) || !aligned(sinks, 4) || !aligned(err_flag, 4))
+        return E2M1_ERR_ALIGN;
+    const size_t need = e2m1::attention_workspace_bytes(tokens, seqs, heads, kv_heads, head_dim);
+    if (need > 0) {
+        if (!workspace || workspace_bytes < need) return E2M1_ERR_WORKSPACE;
+        if (!aligned(workspace, 256)) return E2M1_ERR_ALIGN;
+    }
+    const e2m1::CacheView c = cache_view(k_codes, k_scales, v_codes, v_scales, kv_heads, head_dim, pages, page_size);
+    const e2m1::Attention a = {q,   q_stride, page_table, kv_lens, q_offsets, sinks, scale, causal != 0, window,
+                               out, tokens,   seqs,       (int)heads, table_width, err_flag};
+    return launch_status(e2m1::launch_attention(a, c, workspace, as_stream(stream)));
+}
+
 int ternary_gemv(const uint32_t* packed, const float* row_scale, const float* x, float* y,
                  int64_t n, int64_t k, void* stream) {
     if (n < 0 || k < 0 || k % 16 != 0 || n > INT_MAX || k / 16 > INT_MAX / 64 || !mul_ok(n, k))

@@ -57,6 +57,55 @@ hipError_t launch_int8_gemm(const int8_t* x, const float* x_scale, const int8_t*
                             const float* bias, void* y, bool out_bf16, int64_t m, int64_t n, int64_t k,
                             hipStream_t stream);
 
+// A paged MXFP4 cache of keys and values: codes [pages, heads, page, head_dim / 2], scales [.., head_dim / 32].
+struct CacheView {
+    uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
+    int64_t slots;       // pages * page size
+    int heads, head_dim; // head_dim 64 or 128
+    int page_bits;       // log2 of the page size
+};
+
+// Rows k [tokens, heads, head_dim] and v (row strides in elements) -> the cache's slots; err_flag may be null.
+hipError_t launch_cache_write(const void* k, const void* v, bool bf16, int64_t k_stride, int64_t v_stride,
+                              const int64_t* slots, const CacheView& c, int64_t tokens, int32_t* err_flag,
+                              hipStream_t stream);
+
+struct NormRope {
+    const void* qkv;
+    int64_t stride;
+    const void *q_weight, *k_weight;   // each may be null: that norm is left out
+    float eps;
+    const float* cos_sin;              // [max_pos, rot]
+    int64_t max_pos;
+    int rot;                           // a multiple of 16, 0: no rotation
+    bool interleaved;
+    const int64_t *positions, *slots;
+    uint16_t* q_out;
+    int heads;
+};
+hipError_t launch_norm_rope_write(const NormRope& a, bool bf16, const CacheView& c, int64_t tokens, int32_t* err_flag,
+                                  hipStream_t stream);
+
+hipError_t launch_cache_read(const CacheView& c, const int64_t* slots, uint16_t* k_out, uint16_t* v_out, int64_t tokens,
+                             int32_t* err_flag, hipStream_t stream);
+
+struct Attention {
+    const uint16_t* q;
+    int64_t q_stride;
+    const int32_t *page_table, *kv_lens, *q_offsets;
+    const float* sinks;   // may be null
+    float scale;
+    bool causal;
+    int64_t window;       // 0: none
+    uint16_t* out;
+    int64_t tokens, seqs;
+    int heads;
+    int64_t table_width;
+    int32_t* err_flag;
+};
+size_t attention_workspace_bytes(int64_t tokens, int64_t seqs, int64_t heads, int64_t kv_heads, int64_t head_dim);
+hipError_t launch_attention(const Attention& a, const CacheView& c, void* workspace, hipStream_t stream);
+
 hipError_t launch_ternary(const uint32_t* packed, const float* row_scale, const float* x, float* y,
                           int64_t n, int64_t k, hipStream_t stream);
 

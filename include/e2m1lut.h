@@ -62,7 +62,7 @@ extern "C" {
 #define E2M1_ERR_WORKSPACE (-5) /* workspace missing or smaller than required */
 #define E2M1_ERR_LAUNCH (-6)    /* the HIP runtime reported an error at launch (e.g. no gfx950 code for the device) */
 
-/* Dtype codes of outputs (dequant_gemv and its like) and of the int8 quantizers' inputs. */
+/* Dtype codes of outputs (dequant_gemv and its like) and of the int8 quantizers' and cache writers' inputs. */
 #define E2M1_DTYPE_F32 0
 #define E2M1_DTYPE_BF16 1
 
@@ -301,6 +301,134 @@ int silu_mul_int8_quantize(const void* gate_up, int dtype, int8_t* q, float* sca
 #define E2M1_INT8_MAX_OUTPUTS ((int64_t)1 << 39)
 int int8_gemm(const int8_t* x, const float* x_scale, const int8_t* w, const float* w_scale, const float* bias,
               void* y, int y_dtype, int64_t m, int64_t n, int64_t k, void* stream);
+
+/*
+ * The paged MXFP4 cache of an attention layer: four caller-owned arrays,
+ *   k_codes, v_codes    uint8 [pages, kv_heads, page_size, head_dim/2]   (16-byte aligned)
+ *   k_scales, v_scales  uint8 [pages, kv_heads, page_size, head_dim/32]  (16-byte aligned)
+ * in the format of mxfp4_quantize (a block is 32 channels of one token's head),
+ * with scale bytes 0..252, and 255 for a block that is not finite; 253 and 254
+ * are not valid. slot = page * page_size + place in the page.
+ * Every call on it requires 1 <= kv_heads <= E2M1_CACHE_MAX_HEADS, head_dim 64
+ * or 128, page_size a power of two from 16 to E2M1_CACHE_MAX_PAGE, 0 <= pages
+ * < 2^31, 0 <= tokens <= E2M1_CACHE_MAX_TOKENS. err_flag is int32 [1] on the
+ * device, or NULL; 1 is stored there where a call says so, and nothing else
+ * (never cleared by the library). Slots, positions, lengths and page numbers
+ * are checked on the device: none of their values makes a call read or write
+ * outside its arrays.
+ */
+#define E2M1_CACHE_MAX_HEADS 4096
+#define E2M1_CACHE_MAX_PAGE 65536
+#define E2M1_CACHE_MAX_TOKENS ((int64_t)1 << 26)
+
+/*
+ * mxfp4_cache_write -- rows of keys and values into the cache.
+ * Operation: per token and head, the codes and scales of mxfp4_quantize (from
+ * bf16 or fp32 values) at the token's slot. A block that holds a NaN or an
+ * infinity gets scale byte 255 and codes 0. A token with a negative slot
+ * (padding) is left out; one with a slot past the cache too, and err_flag is
+ * set. Non-negative slots have to differ from each other: of tokens that share
+ * one, bytes of either may be left.
+ *   k, v     [tokens, kv_heads, head_dim], fp32 (dtype = E2M1_DTYPE_F32) or bf16
+ *            (E2M1_DTYPE_BF16), 16-byte aligned; a token's heads are dense, tokens are
+ *            k_stride and v_stride elements apart (at least kv_heads * head_dim,
+ *            whole multiples of 16 bytes), as in a slice of a fused product
+ *   slots    int64 [tokens]
+ */
+int mxfp4_cache_write(const void* k, const void* v, int dtype, int64_t k_stride, int64_t v_stride, const int64_t* slots,
+                      uint8_t* k_codes, uint8_t* k_scales, uint8_t* v_codes, uint8_t* v_scales, int64_t tokens,
+                      int64_t kv_heads, int64_t head_dim, int64_t pages, int64_t page_size, int32_t* err_flag,
+                      void* stream);
+
+/*
+ * norm_rope_mxfp4_cache_write -- the rows of a fused q | k | v product: norm of
+ * each query and key head, rotation by position, queries to q_out in bf16, keys
+ * and values into the cache.
+ * Operation, per token and query or key head x (fp32 throughout, rounded once
+ * at the end): x <- x w / sqrt(mean(x^2) + eps) over the head's channels (left
+ * out where that weight is NULL; a head of zeros stays zeros); the first rot_dim
+ * channels are rotated: pairs (i, i + rot_dim/2), or (2i, 2i+1) with
+ * interleaved, become (a cos - b sin, b cos + a sin) with cos and sin i of the
+ * token's position. Queries are rounded to bf16 (nearest even), keys and values
+ * coded as in mxfp4_cache_write, slots as there. A token whose position is
+ * outside [0, max_pos) gets zeros in q_out and is not written to the cache, and
+ * err_flag is set unless its slot is negative.
+ *   qkv        [tokens, (heads + 2 kv_heads) head_dim], fp32 or bf16 (dtype), 16-byte aligned,
+ *              tokens qkv_stride elements apart (as k_stride above)
+ *   q_weight, k_weight  [head_dim] of the same type (16-byte aligned), or NULL
+ *   cos_sin    fp32 [max_pos, rot_dim] (16-byte aligned): rot_dim/2 cosines, then rot_dim/2 sines
+ *   positions  int64 [tokens]; not read, and may be NULL, where rot_dim is 0
+ *   slots      int64 [tokens]
+ *   q_out      bf16 [tokens, heads, head_dim], overwritten (16-byte aligned)
+ * Requires 0 <= heads <= E2M1_CACHE_MAX_HEADS, rot_dim % 16 == 0, 0 <= rot_dim <=
+ * head_dim, 0 <= max_pos < 2^31, eps finite and >= 0.
+ */
+int norm_rope_mxfp4_cache_write(const void* qkv, int dtype, int64_t qkv_stride, const void* q_weight,
+                                const void* k_weight, float eps, const float* cos_sin, int64_t max_pos,
+                                int64_t rot_dim, int interleaved, const int64_t* positions, const int64_t* slots,
+                                uint16_t* q_out, uint8_t* k_codes, uint8_t* k_scales, uint8_t* v_codes,
+                                uint8_t* v_scales, int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim,
+                                int64_t pages, int64_t page_size, int32_t* err_flag, void* stream);
+
+/*
+ * mxfp4_cache_read -- tokens of the cache by slot, decoded to bf16.
+ * Operation: dequant_decode's values (exact; both zero codes give +0.0), NaN
+ * (0x7FC0) for a block with scale byte 255. A negative slot gives a row of
+ * zeros, a slot past the cache too, and err_flag is set. Slots may repeat.
+ *   slots         int64 [tokens]
+ *   k_out, v_out  bf16 [tokens, kv_heads, head_dim], overwritten (16-byte aligned)
+ */
+int mxfp4_cache_read(const uint8_t* k_codes, const uint8_t* k_scales, const uint8_t* v_codes, const uint8_t* v_scales,
+                     const int64_t* slots, uint16_t* k_out, uint16_t* v_out, int64_t tokens, int64_t kv_heads,
+                     int64_t head_dim, int64_t pages, int64_t page_size, int32_t* err_flag, void* stream);
+
+/*
+ * mxfp4_attention_workspace_size -- bytes of device workspace mxfp4_attention
+ * needs for these extents on the current device (0 where it runs without one,
+ * (size_t)-1 for extents it rejects).
+ */
+size_t mxfp4_attention_workspace_size(int64_t tokens, int64_t seqs, int64_t heads, int64_t kv_heads, int64_t head_dim);
+
+/*
+ * mxfp4_attention -- attention of packed query rows over the paged cache, for
+ * any mix of single tokens, drafts, chunks of a prompt and whole prompts.
+ * Operation: sequence s has the query rows q_offsets[s] .. q_offsets[s+1] - 1
+ * and kv_lens[s] cached tokens, token j in place j % page_size of page
+ * page_table[s][j / page_size]. The last query is at position kv_lens[s] - 1,
+ * the others before it in order; a query at p sees the tokens j <= p, with a
+ * window those with p - window < j too, and every token where causal is 0.
+ * Head h reads kv head h / (heads / kv_heads):
+ *   out = sum_j exp(s_j) v_j / (sum_j exp(s_j) + exp(sinks[h])), s_j = scale q . k_j
+ * over the tokens it sees (no sink term where sinks is NULL), zeros where it
+ * sees none. Scores, maxima and sums are fp32; the weights exp(s_j - max) are rounded to
+ * bf16 before they meet the values, out is rounded to bf16 once. A query that sees
+ * a token with a scale byte 255 in its key or value of that head is NaN in that head;
+ * what is in tokens that it does not see changes nothing.
+ *   q           bf16 [tokens, heads, head_dim] (16-byte aligned), a token's heads dense, tokens q_stride
+ *               elements apart (at least heads * head_dim, a multiple of 8)
+ *   page_table  int32 [seqs, table_width]; entries past a sequence's tokens are not read
+ *   kv_lens     int32 [seqs]
+ *   q_offsets   int32 [seqs + 1], not descending, within 0 .. tokens
+ *   sinks       fp32 [heads], or NULL
+ *   out         bf16 [tokens, heads, head_dim], overwritten (16-byte aligned); rows of q
+ *               that belong to no sequence are left as they were
+ *   workspace   device buffer of at least mxfp4_attention_workspace_size() bytes,
+ *               256-byte aligned, contents need no initialisation (may be NULL
+ *               where that size is 0); the call writes it, so calls that overlap
+ *               in time need workspaces of their own
+ * A token on a page outside [0, pages) is not seen, tokens past table_width
+ * pages neither, and err_flag is set for both. A negative length counts as 0.
+ * Requires heads a multiple of kv_heads, at most E2M1_CACHE_MAX_HEADS, 0 <= seqs
+ * <= E2M1_CACHE_MAX_TOKENS, table_width * page_size < 2^31, scale finite and >=
+ * 0, window >= 0 (0: none) and 0 without causal.
+ * Errors: E2M1_ERR_WORKSPACE as in ternary_gemm.
+ */
+int mxfp4_attention(const uint16_t* q, int64_t q_stride, const uint8_t* k_codes, const uint8_t* k_scales,
+                    const uint8_t* v_codes, const uint8_t* v_scales, const int32_t* page_table, const int32_t* kv_lens,
+                    const int32_t* q_offsets, const float* sinks, float scale, int causal, int64_t window,
+                    uint16_t* out, void* workspace, size_t workspace_bytes, int64_t tokens, int64_t seqs, int64_t heads,
+                    int64_t kv_heads, int64_t head_dim, int64_t pages, int64_t page_size, int64_t table_width,
+                    int32_t* err_flag, void* stream);
 
 /*
  * ternary_gemv -- y[i] = row_scale[i] * sum_k t(i,k) * x[k], t in {-1, 0, +1}.
