@@ -370,7 +370,7 @@ int mxfp4_cache_read(const uint8_t* k_codes, const uint8_t* k_scales, const uint
 static bool attention_shape_ok(int64_t tokens, int64_t seqs, int64_t heads, int64_t kv_heads, int64_t head_dim) {
     return tokens >= 0 && tokens <= E2M1_CACHE_MAX_TOKENS && seqs >= 0 && seqs <= E2M1_CACHE_MAX_TOKENS && kv_heads >= 1 &&
            heads >= kv_heads && heads <= E2M1_CACHE_MAX_HEADS && heads % kv_heads == 0 &&
-           (head_dim == 64 || head_dim == 128);
+           (head_dim == 64 || head_dim == 128) && tokens * heads <= E2M1_ATTENTION_MAX_ROWS;
 }
 
 size_t mxfp4_attention_workspace_size(int64_t tokens, int64_t seqs, int64_t heads, int64_t kv_heads, int64_t head_dim) {
@@ -385,7 +385,7 @@ int mxfp4_attention(const uint16_t* q, int64_t q_stride, const uint8_t* k_codes,
                     int64_t kv_heads, int64_t head_dim, int64_t pages, int64_t page_size, int64_t table_width,
                     int32_t* err_flag, void* stream) {
     if (!attention_shape_ok(tokens, seqs, heads, kv_heads, head_dim) || table_width < 0 || window < 0 ||
-        (window > 0 && !causal) || !(scale >= 0.0f) || scale > FLT_MAX)
+        (window > 0 && !causal) || !(scale >= 0.0f) || scale > 0x1p126f)
         return E2M1_ERR_SHAPE;
     if (int bad = cache_shape(kv_heads, head_dim, pages, page_size)) return bad;
     if (table_width > INT_MAX / page_size || !mul_ok(table_width, seqs)) return E2M1_ERR_SHAPE;
@@ -402,7 +402,7 @@ int mxfp4_attention(const uint16_t* q, int64_t q_stride, const uint8_t* k_codes,
         if (!aligned(workspace, 256)) return E2M1_ERR_ALIGN;
     }
     const e2m1::CacheView c = cache_view(k_codes, k_scales, v_codes, v_scales, kv_heads, head_dim, pages, page_size);
-    const e2m1::Attention a = {q,   q_stride, page_table, kv_lens, q_offsets, sinks, scale, causal != 0, window,
+    const e2m1::Attention a = {q,   q_stride, page_table, kv_lens, q_offsets, sinks, scale, causal != 0, window < INT_MAX ? window : 0,
                                out, tokens,   seqs,       (int)heads, table_width, err_flag};
     return launch_status(e2m1::launch_attention(a, c, workspace, as_stream(stream)));
 }

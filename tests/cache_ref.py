@@ -79,8 +79,10 @@ def attention(q, keys, values, scale: float, causal: bool, window: int, sinks=No
 
     The bound counts: the weights' rounding to bf16 (half a step of each, relative, times |v|), the result's own, and the
     scores' errors, which enter the weights and the sum (twice). A score's: a query is taken as sums of parts that
-    leave at most 2^-16 of its block's largest magnitude, products add in fp32 (d terms and the accumulator's roundings),
-    then one product and the exponential's argument, and the exponential itself (2 steps)."""
+    leave at most 2^-16 of its block's largest magnitude (or 2^-131), products add in fp32 (d terms and the accumulator's roundings),
+    then one product and the exponential's argument, and the exponential itself (2 steps).
+    A weight below the smallest normal number counts as zero. The maximum in use is never above the row's, so the
+    largest weight, and the sum with it, is at least 1, and what is lost of the result is at most 2^-126 |v| a token."""
     n, heads, d = q.shape
     length, kv = keys.shape[:2]
     out = np.zeros((n, heads, d))
@@ -99,8 +101,8 @@ def attention(q, keys, values, scale: float, causal: bool, window: int, sinks=No
         x = np.asarray(q[:, h], np.float64)
         s = scale * (x @ k.T)
         size = scale * (np.abs(x) @ np.abs(k).T)
-        blocks = np.abs(x).reshape(n, d // 32, 32).max(-1)
-        parts = scale * 2.0**-16 * (blocks @ np.abs(k).reshape(length, d // 32, 32).sum(-1).T)
+        blocks = np.maximum(2.0**-16 * np.abs(x).reshape(n, d // 32, 32).max(-1), 2.0**-131)
+        parts = scale * (blocks @ np.abs(k).reshape(length, d // 32, 32).sum(-1).T)
         delta = np.where(seen, parts + (d + 8) * U_F32 * size + 4 * U_F32 * np.abs(s), 0.0).max(1, initial=0.0)
         delta = np.expm1(2 * delta + 8 * U_F32)
         s = np.where(seen, s, -np.inf)
@@ -115,6 +117,7 @@ def attention(q, keys, values, scale: float, causal: bool, window: int, sinks=No
         mag = (p @ np.abs(v)) / total[:, None]
         # sums of `length` terms in fp32, in any order
         bound[:, h] = mag * (U_BF16 * (1 + delta[:, None]) + 2 * delta[:, None] + (length + 8) * U_F32)
+        bound[:, h] += 2.0**-126 * (seen.astype(np.float64) @ np.abs(v))
         bound[:, h] += U_BF16 * (np.abs(o) + bound[:, h]) + 2.0**-134
         o[(seen & bad[None, :]).any(1)] = np.nan
         out[:, h] = o

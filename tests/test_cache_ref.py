@@ -162,7 +162,7 @@ def test_attention_refusals(lib):
     assert attend(lib, seqs=0, table=NULL) == E_OK
     for bad in (dict(heads=30), dict(heads=4), dict(kv=0), dict(heads=8192, kv=8), dict(seqs=-1), dict(width=-1),
                 dict(window=-1), dict(window=5, causal=0), dict(scale=-0.1), dict(scale=float("nan")),
-                dict(scale=float("inf")), dict(width=2**27), dict(stride=4095), dict(stride=4088), dict(stride=4100)):
+                dict(scale=float("inf")), dict(scale=2.0**127), dict(tokens=2**26, stride=2**13), dict(width=2**27), dict(stride=4095), dict(stride=4088), dict(stride=4100)):
         assert attend(lib, **bad) == E_SHAPE, bad
     for name in ("q", "table", "lens", "offsets", "out"):
         assert attend(lib, **{name: NULL}) == E_NULL, name
