@@ -450,21 +450,23 @@ def int8_gemm(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale: 
 
 def _cache_of(cache) -> tuple:
     """(addresses, pages, kv heads, page size, head dim, GPU) of (k_codes, k_scales, v_codes, v_scales)."""
-    if not isinstance(cache, (tuple, list)) or len(cache) != 4:
-        raise ValueError("cache must hold four tensors (k_codes, k_scales, v_codes, v_scales)")
-    k_codes = cache[0]
-    if not isinstance(k_codes, torch.Tensor) or k_codes.dim() != 4:
-        raise ValueError("cache[0] must be a [pages, kv_heads, page_size, head_dim / 2] tensor")
-    if not k_codes.is_cuda:
-        raise ValueError(f"cache[0] must be on a GPU, got {k_codes.device}")
-    device = k_codes.get_device()
-    pages, heads, page, half = k_codes.shape
-    codes, scales = (pages, heads, page, half), (pages, heads, page, half // 16)
-    ptrs = (_need_on(k_codes, "cache[0]", torch.uint8, codes, device),
-            _need_on(cache[1], "cache[1]", torch.uint8, scales, device),
-            _need_on(cache[2], "cache[2]", torch.uint8, codes, device),
-            _need_on(cache[3], "cache[3]", torch.uint8, scales, device))
-    return ptrs, pages, heads, page, 2 * half, device
+    try:
+        k, ks, v, vs = cache
+        pages, heads, page, half = shape = k.shape
+    except (TypeError, ValueError, AttributeError):
+        raise ValueError("cache must hold four tensors (k_codes, k_scales, v_codes, v_scales), codes [pages, kv_heads, "
+                         "page_size, head_dim / 2]") from None
+    scales = (pages, heads, page, half // 16)
+    device = k.get_device()
+    u8 = torch.uint8
+    if not (device >= 0 and k.dtype is u8 and ks.dtype is u8 and v.dtype is u8 and vs.dtype is u8 and v.shape == shape
+            and ks.shape == scales and vs.shape == scales and k.is_contiguous() and ks.is_contiguous()
+            and v.is_contiguous() and vs.is_contiguous() and ks.get_device() == device and v.get_device() == device
+            and vs.get_device() == device):
+        for i, want in ((0, shape), (1, scales), (2, shape), (3, scales)):
+            _need(cache[i], f"cache[{i}]", _U8, want)
+        raise ValueError("the cache's tensors are on different GPUs")
+    return (k.data_ptr(), ks.data_ptr(), v.data_ptr(), vs.data_ptr()), pages, heads, page, 2 * half, device
 
 
 def _token_rows(t, name: str, dtypes, shape: tuple, device: int) -> int:

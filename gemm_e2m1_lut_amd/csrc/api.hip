@@ -388,7 +388,7 @@ int mxfp4_attention(const uint16_t* q, int64_t q_stride, const uint8_t* k_codes,
         (window > 0 && !causal) || !(scale >= 0.0f) || scale > 0x1p126f)
         return E2M1_ERR_SHAPE;
     if (int bad = cache_shape(kv_heads, head_dim, pages, page_size)) return bad;
-    if (table_width > INT_MAX / page_size || !mul_ok(table_width, seqs)) return E2M1_ERR_SHAPE;
+    if (table_width > E2M1_ATTENTION_MAX_LENGTH / page_size || !mul_ok(table_width, seqs)) return E2M1_ERR_SHAPE;
     if (tokens == 0 || seqs == 0) return E2M1_OK;
     if (!stride_ok(q_stride, heads * head_dim, tokens, E2M1_DTYPE_BF16)) return E2M1_ERR_SHAPE;
     if (!q || !kv_lens || !q_offsets || !out || (table_width > 0 && !page_table)) return E2M1_ERR_NULL;

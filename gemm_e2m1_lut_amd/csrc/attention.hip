@@ -13,25 +13,27 @@
 // they read) against steps of 32 tokens.
 //   * Scores: v_mfma_scale_f32_16x16x128_f8f6f4 takes the cache's own bytes: 16
 //     tokens' E2M1 codes as the A operand, one 16-byte load a lane, their E8M0
-//     bytes as its scales, so keys are never decoded. Queries are the B operand,
-//     as a sum of three E2M3 (6-bit) parts with block scales 2^e, 2^(e-4),
-//     2^(e-10): a bf16 number has 8 significant bits, three parts keep every
-//     element to 2^-16 of its block's largest (the second part alone leaves
-//     2^-10). 4- and 6-bit operands run at twice the rate of 8-bit ones, so the three
-//     products take 3/4 of the time of bf16 keys, and no key is unpacked. (Two E4M3 parts
-//     would do too, at the rate of four E2M3 ones.) Heads of 64 channels fill half of the
+//     bytes as its scales, so keys are never decoded. Queries, times scale
+//     log2(e), are the B operand, as a sum of three E2M3 (6-bit) parts with block
+//     scales 2^e, 2^(e-4), 2^(e-9), which leave 2^-13 of a block's largest
+//     magnitude (two parts: 2^-9). 4- and 6-bit operands run at twice the rate of
+//     8-bit ones, so the three products take 3/4 of the time of bf16 keys, and no
+//     key is unpacked. The accumulator starts at minus the maximum in use: the
+//     result is the exponent of the weight. Heads of 64 channels fill half of the
 //     instruction's 128: the other half takes the second part of the same keys.
 //   * The scores come out transposed (a lane has 4 tokens of one query row), which
 //     is what the values' product takes as its B operand: the weights never
 //     leave their lane. Its A operand is the values transposed, 8 tokens of a
 //     channel a lane: a lane loads the codes of 8 channels of its 8 tokens,
 //     v_cvt_scalef32_pk_bf16_fp4 decodes pairs of channels with the token's scale
-//     and v_perm_b32 pairs the tokens. One operation an element, for all NQ tiles.
-//   * A maximum is replaced only when a score passes it by 2^8 (a vote per step):
+//     and v_perm_b32 pairs the tokens: one operation an element, for all NQ tiles.
+//     The weights' sum is one more such product, with ones.
+//   * The maximum is replaced only when a score passes it by 2^8 (a vote per step):
 //     weights are then at most 2^8, the sums fp32, and the usual step has no
 //     exchange between lanes and no rescaling.
-// Weights are rounded to bf16 for the matrix cores (half a step is 2^-8 of a weight, and the
-// errors of a row's weights are independent: the result's own rounding is larger).
+// Weights are rounded to bf16 for the matrix cores: half a step is 2^-8 of a
+// weight, in the sum as in the product, and the errors of a row's weights are
+// independent: the result's own rounding is larger.
 // No LDS and no barrier in the loop: the bytes of a step are few (4352 for 32
 // tokens of 128 channels), and waves that share tokens find them in the L1.
 #include "device.hpp"
@@ -43,7 +45,9 @@ namespace {
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr int kWaves = 4;          // of a workgroup
 constexpr int kStep = 32;          // tokens a wave takes at a time
-constexpr int kUnit = kWaves * kStep;
+// Steps whose bytes a wave holds or waits for.
+template <int NQ>
+constexpr int kAhead = NQ == 1 ? 3 : 2;
 constexpr float kSlack = 8.0f;     // how far a score may pass the maximum in use, in powers of two
 constexpr int kFarRight = 0x7FFFFFFF;
 
@@ -58,82 +62,139 @@ __device__ __forceinline__ float exp2_raw(float x) { return __builtin_amdgcn_exp
 
 // What a sequence asks for.
 struct Span {
-    int64_t first;   // its first query row
-    int n;           // queries
-    int len;         // cached tokens
+    int first;   // its first query row
+    int n;       // queries
+    int len;     // cached tokens
 };
 
-__device__ __forceinline__ Span span_of(const Attention& a, int page_bits, int64_t s) {
-    const int64_t o0 = a.q_offsets[s], o1 = a.q_offsets[s + 1];
+__device__ __forceinline__ Span span_of(const Attention& a, int page_bits, int s) {
+    const int o0 = a.q_offsets[s], o1 = a.q_offsets[s + 1];
+    const int len = a.kv_lens[s];
+    const int tokens = (int)a.tokens, most = (int)(a.table_width << page_bits);
     Span r;
-    r.first = min(max(o0, (int64_t)0), a.tokens);
-    r.n = (int)(min(max(o1, r.first), a.tokens) - r.first);
-    const int64_t most = a.table_width << page_bits;
-    const int64_t len = a.kv_lens[s];
-    r.len = (int)min(max(len, (int64_t)0), most);
+    r.first = min(max(o0, 0), tokens);
+    r.n = min(max(o1, r.first), tokens) - r.first;
+    r.len = min(max(len, 0), most);
     if (len > most && r.n > 0 && a.err_flag) *a.err_flag = 1;
     return r;
 }
 
-// The first token that some query of [i0, ..) sees.
-__device__ __forceinline__ int first_seen(const Attention& a, const Span& s, int i0) {
-    return a.window > 0 ? (int)max((int64_t)0, (int64_t)s.len - s.n + i0 - a.window + 1) : 0;
+// The first token that query i of a sequence sees.
+__device__ __forceinline__ int first_seen(const Attention& a, const Span& s, int i) {
+    const int pos = s.len - s.n + i, window = (int)a.window;
+    return window > 0 && window <= pos ? pos - window + 1 : 0;
 }
 
-// Units of kUnit tokens of every tile of a sequence.
-__device__ __forceinline__ int units_of(const Attention& a, const Span& s) {
+__device__ __forceinline__ uint32_t tiles_of(const Span& s, int group, int rows) {
+    return (uint32_t)(s.n * group + rows - 1) / (uint32_t)rows;
+}
+
+// Units of 2^unit_bits tokens of every tile of a sequence.
+__device__ __forceinline__ uint32_t units_of(const Attention& a, const Span& s, int unit_bits) {
     const int lo = first_seen(a, s, 0) & ~(kStep - 1);
-    return max(1, (s.len - lo + kUnit - 1) / kUnit);
+    return max(1u, ((uint32_t)(s.len - lo) + (1u << unit_bits) - 1) >> unit_bits);
 }
 
-__device__ __forceinline__ int64_t scan64(int64_t v, int lane) {
-#pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) {
-        const int64_t o = __shfl_up((long long)v, d, kWave);
-        if (lane >= d) v += o;
-    }
+template <int kCtrl, int kRowMask>
+__device__ __forceinline__ uint32_t shifted(uint32_t v) {   // 0 where there is no lane to take from
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kCtrl, kRowMask, 0xF, false);
+}
+
+// Sums over the lanes up to each one's own.
+__device__ __forceinline__ uint32_t scan(uint32_t v) {
+    v += shifted<0x111, 0xF>(v);   // row_shr:1, 2, 4, 8
+    v += shifted<0x112, 0xF>(v);
+    v += shifted<0x114, 0xF>(v);
+    v += shifted<0x118, 0xF>(v);
+    v += shifted<0x142, 0xA>(v);   // row_bcast:15 to rows 1 and 3
+    v += shifted<0x143, 0xC>(v);   // row_bcast:31 to rows 2 and 3
     return v;
 }
 
-__device__ __forceinline__ int64_t uniform64(int64_t v, int lane) {
-    const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)v, lane);
-    const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), lane);
-    return (int64_t)((uint64_t)hi << 32 | lo);
-}
+__device__ __forceinline__ int from_lane(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
 
-// Sequences laid end to end by weight: each lane sums a run of them, a scan over the wave gives the runs' places.
-template <typename F>
-struct Layout {
-    F weight;
-    int64_t seqs, per, before, total;
-    int lane;
+// Sequences laid end to end by weight, a run of them a lane; a scan over the wave gives the runs' places. Up to 64 sequences
+// are read once and kept.
+struct Plan {
+    const Attention& a;
+    int page_bits, lane, per;
+    Span mine;                 // of the lane's sequence, where each lane has one
+    uint32_t before, total;
+    bool ok;                   // no offset is below the one before it: then no query row belongs to two sequences
 
-    __device__ __forceinline__ Layout(F f, int64_t n, int lane_) : weight(f), seqs(n), lane(lane_) {
-        per = (n + kWave - 1) / kWave;
-        int64_t sum = 0;
-        for (int64_t s = lane * per; s < min((lane + 1) * per, n); ++s) sum += weight(s);
-        const int64_t end = scan64(sum, lane);
-        before = end - sum;
-        total = uniform64(end, kWave - 1);
-        after = end;
+    // The lane's sequences [lane per, ..).
+    __device__ __forceinline__ int begin() const { return lane * per; }
+    __device__ __forceinline__ int end() const { return (int)min((int64_t)(lane + 1) * per, a.seqs); }
+
+    template <typename F>
+    __device__ __forceinline__ Plan(const Attention& a_, int page_bits_, int lane_, F weight)
+        : a(a_), page_bits(page_bits_), lane(lane_) {
+        per = (int)((a.seqs + kWave - 1) / kWave);
+        mine = {0, 0, 0};
+        uint32_t sum = 0;
+        bool bad = false;
+        if (per == 1) {
+            if (lane < a.seqs) {
+                mine = span_of(a, page_bits, lane);
+                bad = a.q_offsets[lane + 1] < a.q_offsets[lane];
+            }
+            sum = weight(mine);
+        } else {
+            for (int s = begin(); s < end(); ++s) {
+                sum += weight(span_of(a, page_bits, s));
+                bad |= a.q_offsets[s + 1] < a.q_offsets[s];
+            }
+        }
+        ok = !__any(bad);
+        if (bad && a.err_flag) *a.err_flag = 1;
+        const uint32_t after = scan(sum);
+        before = after - sum;
+        total = (uint32_t)from_lane((int)after, kWave - 1);
     }
-    int64_t after;
+
+    // Another weight's sum over the sequences before `seq`, and over all.
+    template <typename F>
+    __device__ __forceinline__ uint32_t sum_before(int seq, F weight, uint32_t& all) const {
+        uint32_t sum = 0, part = 0;
+        if (per == 1) {
+            sum = weight(mine);
+        } else {
+            for (int s = begin(); s < end(); ++s) {
+                const uint32_t w = weight(span_of(a, page_bits, s));
+                sum += w;
+                if (s < seq) part += w;
+            }
+        }
+        const int owner = (int)((uint32_t)seq / (uint32_t)per);
+        const uint32_t after = scan(sum);
+        all = (uint32_t)from_lane((int)after, kWave - 1);
+        return (uint32_t)from_lane((int)(after - sum + part), owner);
+    }
+
+    // A sequence, the same for every lane.
+    __device__ __forceinline__ Span span(int seq) const {
+        if (per == 1) return {from_lane(mine.first, seq), from_lane(mine.n, seq), from_lane(mine.len, seq)};
+        const Span s = span_of(a, page_bits, seq);
+        return {uniform(s.first), uniform(s.n), uniform(s.len)};
+    }
 
     // The sequence that holds place `at` < total, and where it begins.
-    __device__ __forceinline__ void find(int64_t at, int64_t& seq, int64_t& begin) const {
-        const uint64_t mine = __ballot(at >= before && at < after);
-        const int owner = __builtin_ctzll(mine);
-        int64_t s = lane * per, b = before;
-        if (lane == owner) {
+    template <typename F>
+    __device__ __forceinline__ int find(uint32_t at, uint32_t& begins, F weight) const {
+        // the last lane whose run begins at or before it: empty runs before it begin at the same place
+        const int owner = 63 - __builtin_clzll(__ballot(before <= at && begin() < end()));
+        int s = begin();
+        uint32_t b = before;
+        if (per > 1 && lane == owner) {
             for (;;) {
-                const int64_t w = weight(s);
+                const uint32_t w = weight(span_of(a, page_bits, s));
                 if (at < b + w) break;
                 b += w;
                 ++s;
             }
         }
-        seq = uniform64(s, owner);
-        begin = uniform64(b, owner);
+        begins = (uint32_t)from_lane((int)b, owner);
+        return from_lane(s, owner);
     }
 };
 
@@ -159,15 +220,20 @@ struct Rows {
     int lo_max, hi_min;   // the tokens that every row sees
 };
 
+// Sums of row lane % 16: 32 of its D channels, the weights' (four times the same number), the maximum in use and how far
+// above it a score may be: nothing at all before there is one.
 template <int D, int NQ>
 struct Sums {
     f32x4 o[NQ][D / 16];
-    float m[NQ], l[NQ];   // l: of the lane's own tokens
+    f32x4 l[NQ];
+    float m[NQ], slack[NQ];
+    __device__ __forceinline__ float top(int i) const { return slack[i] < 0.0f ? -INFINITY : m[i]; }
     __device__ __forceinline__ void clear() {
 #pragma unroll
         for (int i = 0; i < NQ; ++i) {
-            m[i] = -INFINITY;
-            l[i] = 0.0f;
+            m[i] = 0.0f;
+            slack[i] = -INFINITY;
+            l[i] = f32x4{0, 0, 0, 0};
 #pragma unroll
             for (int j = 0; j < D / 16; ++j) o[i][j] = f32x4{0, 0, 0, 0};
         }
@@ -192,25 +258,29 @@ struct Lane {
     }
 };
 
-// First row (of the cache's [pages, heads, page]) of the 16 tokens from tb on; ok: they exist and some row sees them.
-template <int NQ>
-__device__ __forceinline__ int64_t half_row(const Attention& a, const CacheView& c, const int32_t* table, int head, int tb,
-                                            int lo_all, int hi_all, bool& ok) {
-    const bool in = tb < hi_all && tb + 16 > lo_all;
-    const int at = in ? tb : 0;
-    int pg = hi_all > lo_all ? uniform(table[at >> c.page_bits]) : 0;
-    const bool there = pg >= 0 && ((int64_t)pg << c.page_bits) < c.slots;
-    if (in && !there && a.err_flag) *a.err_flag = 1;
-    ok = in && there;
-    return ok ? ((((int64_t)pg * c.heads + head) << c.page_bits) + (at & ((1 << c.page_bits) - 1))) : 0;
+// Where a wave's next 32 steps are: lane 2 i + t holds the page of half t of step at + i stride, -1 where no row sees a token
+// of it or the page is not there.
+__device__ __forceinline__ int pages_ahead(const Attention& a, const CacheView& c, const int32_t* table, int at, int stride,
+                                           int lo_all, int hi_all, int lane) {
+    const int64_t tb = (int64_t)(at + (lane / 2) * stride) * kStep + (lane % 2) * 16;
+    if (tb >= hi_all || tb + 16 <= lo_all) return -1;
+    const int pg = table[tb >> c.page_bits];
+    if (pg >= 0 && ((int64_t)pg << c.page_bits) < c.slots) return pg;
+    if (a.err_flag) *a.err_flag = 1;
+    return -1;
 }
 
-template <int D, int NQ>
-__device__ __forceinline__ void load_step(Stage<D>& s, const Attention& a, const CacheView& c, const int32_t* table,
-                                          int head, int base, const Rows<NQ>& rows, const Lane<D>& ln) {
+// The bytes of a step, the `i`-th that `pages` holds; where there is none, those of the cache's first tokens.
+template <int D>
+__device__ __forceinline__ void load_step(Stage<D>& s, const CacheView& c, int pages, int i, int head, int base,
+                                          const Lane<D>& ln) {
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-        const int64_t row = half_row<NQ>(a, c, table, head, base + 16 * t, rows.lo_all, rows.hi_all, s.ok[t]);
+        const int pg = __builtin_amdgcn_readlane(pages, 2 * i + t);
+        s.ok[t] = pg >= 0;
+        const int64_t row = s.ok[t] ? ((((int64_t)pg * c.heads + head) << c.page_bits) +
+                                       ((base + 16 * t) & ((1 << c.page_bits) - 1)))
+                                    : 0;
         const uint8_t* kc = c.k_codes + row * (D / 2);
         const uint8_t* kx = c.k_scales + row * (D / 32);
         const uint8_t* vc = c.v_codes + row * (D / 2);
@@ -254,18 +324,45 @@ __device__ __forceinline__ uint32_t pack_weights(float a, float b) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
 }
 
+// Values with scale byte 255 in a step that not all rows see whole: NaN for the rows that see the token, in its block's
+// channels (which a lane group has to itself), and zeros for the product with the others' weights.
 template <int D, int NQ>
-__device__ __forceinline__ void take_step(Stage<D>& s, const Rows<NQ>& rows, Sums<D, NQ>& sums, float scale, int base,
+__device__ void values_not_finite(Stage<D>& s, const Rows<NQ>& rows, Sums<D, NQ>& sums, int base, const Lane<D>& ln) {
+    const int block = ln.g * (D / 4) / 32, own = ln.n * (D / 16) / 32;
+    bool sees[NQ] = {};
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const uint32_t w = scale_bytes<D>(s.vs[t], r);
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const uint32_t there = (uint32_t)from_lane((int)w, 16 * g);   // of token j
+                const int j = base + 16 * t + 4 * g + r;
+#pragma unroll
+                for (int i = 0; i < NQ; ++i)
+                    sees[i] |= ((there >> (8 * block)) & 255u) == 255u && j >= rows.lo[i] && j < rows.hi[i];
+            }
+            clear_token<D>(s, t, r, ((w >> (8 * own)) & 255u) == 255u);
+        }
+#pragma unroll
+    for (int i = 0; i < NQ; ++i)
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) sums.o[i][j] += sees[i] ? __uint_as_float(0x7FC00000u) : 0.0f;
+}
+
+template <int D, int NQ>
+__device__ __forceinline__ void take_step(Stage<D>& s, const Rows<NQ>& rows, Sums<D, NQ>& sums, int base,
                                           const Lane<D>& ln) {
     constexpr int NJ = D / 16;
-    // scores of 2 x 16 tokens
+    // scores of 2 x 16 tokens, less the maximum in use
     f32x4 x[NQ][2];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
         const i32x8 k = {(int)s.k[t].x, (int)s.k[t].y, (int)s.k[t].z, (int)s.k[t].w, 0, 0, 0, 0};
 #pragma unroll
         for (int i = 0; i < NQ; ++i) {
-            f32x4 z = {0, 0, 0, 0};
+            f32x4 z = {-sums.m[i], -sums.m[i], -sums.m[i], -sums.m[i]};
             z = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(k, rows.q[i][0], z, 4, 2, 0, s.ks[t], 0, rows.qs[i]);
             z = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(k, rows.q[i][1], z, 4, 2, 0, s.ks[t], 1, rows.qs[i]);
             if constexpr (D == 128)
@@ -273,83 +370,65 @@ __device__ __forceinline__ void take_step(Stage<D>& s, const Rows<NQ>& rows, Sum
             x[i][t] = z;
         }
     }
-    const int j0 = base + 4 * ln.g;
-    const bool edge = base < rows.lo_max || base + kStep > rows.hi_min || !(s.ok[0] && s.ok[1]);
-    if (edge) {   // tokens that no row sees: values that stay finite whatever is there
+    if (base < rows.lo_max || base + kStep > rows.hi_min || !(s.ok[0] && s.ok[1])) {   // not every row sees every token
+        const int j0 = base + 4 * ln.g;
+        bool high = false;
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int j = j0 + 16 * t + r;
+                // values that no row sees stay finite whatever is there
                 clear_token<D>(s, t, r, !(s.ok[t] && j >= rows.lo_all && j < rows.hi_all));
-            }
-    }
-    // A value's scale byte past 252: its token turns NaN in the scores, its values are left out. Bytes from 192 on are rare
-    // enough to be looked at one by one.
-    uint32_t high = 0;
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) high |= s.vs[t][i] & (s.vs[t][i] << 1);
-    if (__builtin_expect(__any((high & 0x80808080u) != 0), 0)) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const uint32_t w = scale_bytes<D>(s.vs[t], r);
-                bool bad = false;
-#pragma unroll
-                for (int b = 0; b < D / 32; ++b) bad |= ((w >> (8 * b)) & 255u) > 252u;
-#pragma unroll
-                for (int i = 0; i < NQ; ++i) x[i][t][r] = bad ? __uint_as_float(0x7FC00000u) : x[i][t][r];
-                clear_token<D>(s, t, r, bad);
-            }
-    }
-    if (edge) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int j = j0 + 16 * t + r;
 #pragma unroll
                 for (int i = 0; i < NQ; ++i)
                     x[i][t][r] = s.ok[t] && j >= rows.lo[i] && j < rows.hi[i] ? x[i][t][r] : -INFINITY;
+                const uint32_t w = scale_bytes<D>(s.vs[t], r);
+                high |= (w & (w << 1) & 0x80808080u) != 0;   // bytes from 192 on: rare enough to be looked at one by one
             }
+        if (__any(high)) values_not_finite<D, NQ>(s, rows, sums, base, ln);
     }
-    // maxima
+    // the maximum is left alone until a score is 2^8 above it
     bool past = false;
     float top[NQ];
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
-        top[i] = fmaxf(fmaxf(fmaxf(x[i][0][0], x[i][0][1]), fmaxf(x[i][0][2], x[i][0][3])),
-                       fmaxf(fmaxf(x[i][1][0], x[i][1][1]), fmaxf(x[i][1][2], x[i][1][3]))) * scale;
-        past |= top[i] > sums.m[i] + kSlack;
+        float v = fmaxf(fmaxf(x[i][0][0], x[i][0][1]), x[i][0][2]);
+        v = fmaxf(fmaxf(v, x[i][0][3]), x[i][1][0]);
+        v = fmaxf(fmaxf(v, x[i][1][1]), x[i][1][2]);
+        top[i] = fmaxf(v, x[i][1][3]);
+        past |= top[i] > sums.slack[i];
     }
     if (__any(past)) {
 #pragma unroll
         for (int i = 0; i < NQ; ++i) {
             float v = fmaxf(top[i], __shfl_xor(top[i], 16, kWave));
             v = fmaxf(v, __shfl_xor(v, 32, kWave));
-            const float mn = fmaxf(sums.m[i], v);
-            const float f = mn == -INFINITY ? 1.0f : exp2_raw(sums.m[i] - mn);
-            sums.m[i] = mn;
+            const bool none = sums.slack[i] < 0.0f;
+            const float by = v == -INFINITY ? 0.0f : none ? v : fmaxf(v, 0.0f);
+            const float f = none ? 1.0f : exp2_raw(-by);
+            if (v != -INFINITY) sums.slack[i] = kSlack;
+            sums.m[i] += by;
             sums.l[i] *= f;
 #pragma unroll
             for (int j = 0; j < NJ; ++j) sums.o[i][j] *= f;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) x[i][t] -= by;
         }
     }
-    // weights
+    // weights, and their sum by a product with ones
+    const uint32_t one = 0x3F803F80u;
+    const u32x4 ones = {one, one, one, one};
     bf16x8 p[NQ];
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
-        const float m = sums.m[i] == -INFINITY ? 0.0f : sums.m[i];
         float w[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = exp2_raw(__builtin_fmaf(x[i][e / 4][e % 4], scale, -m));
-        sums.l[i] += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
+        for (int e = 0; e < 8; ++e) w[e] = exp2_raw(x[i][e / 4][e % 4]);
         const u32x4 pk = {pack_weights(w[0], w[1]), pack_weights(w[2], w[3]), pack_weights(w[4], w[5]),
                           pack_weights(w[6], w[7])};
         p[i] = __builtin_bit_cast(bf16x8, pk);
+        sums.l[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, ones), p[i], sums.l[i], 0, 0, 0);
     }
     // values: a byte (two channels) of all eight tokens at a time
     float sc[8];
@@ -388,51 +467,62 @@ __device__ __forceinline__ void take_step(Stage<D>& s, const Rows<NQ>& rows, Sum
 
 // ---------------------------------------------------------------- queries --
 
-// x - y of bf16 pairs, exact where the difference fits bf16.
-__device__ __forceinline__ bf16x32 difference(const bf16x32& x, const bf16x32& y) {
-    typedef uint32_t u32x16 __attribute__((ext_vector_type(16)));
-    const u32x16 a = __builtin_bit_cast(u32x16, x), b = __builtin_bit_cast(u32x16, y);
-    u32x16 d;
+typedef uint32_t u32x16 __attribute__((ext_vector_type(16)));
+
+// x <- x - part, the values of a part of them.
+__device__ __forceinline__ void take_off(float (&x)[32], const bf16x32& part) {
+    const u32x16 w = __builtin_bit_cast(u32x16, part);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-        const float lo = __uint_as_float(a[i] << 16) - __uint_as_float(b[i] << 16);
-        const float hi = __uint_as_float(a[i] & 0xFFFF0000u) - __uint_as_float(b[i] & 0xFFFF0000u);
-        d[i] = __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
+        x[2 * i] -= __uint_as_float(w[i] << 16);
+        x[2 * i + 1] -= __uint_as_float(w[i] & 0xFFFF0000u);
     }
-    return __builtin_bit_cast(bf16x32, d);
+}
+
+__device__ __forceinline__ bf16x32 as_bf16(const float (&x)[32]) {
+    u32x16 w;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = pack_weights(x[2 * i], x[2 * i + 1]);
+    return __builtin_bit_cast(bf16x32, w);
 }
 
 __device__ __forceinline__ i32x8 widen(const u32x6& v) {
     return i32x8{(int)v[0], (int)v[1], (int)v[2], (int)v[3], (int)v[4], (int)v[5], 0, 0};
 }
 
-// The three parts of a lane's 32 channels. Their largest magnitude lies in [4, 8) of the first part's unit 2^e, so the
-// first part leaves at most 1/2, the second, in units of 2^(e-4), at most 2^-8, the third, in 2^(e-10), 2^-14. Each
-// remainder has at most the 8 significant bits it started with. A block that holds a NaN or an infinity gets the scale NaN.
+// The three parts of a lane's 32 channels times `scale`. Their largest magnitude lies in [3.75, 7.5] of the first part's
+// unit 2^e (7.5 is E2M3's largest), so the first part leaves at most 1/4 (half of its largest step), the second, in units of
+// 2^(e-4), at most 2^-7, the third, in 2^(e-9), 2^-12: 2^-13 of the largest. Remainders are fp32; they go through bf16 on
+// their way to a part, which may choose the part next to the nearest and so only moves what the next one has to take.
+// A block that holds a NaN or an infinity gets the scale NaN.
 template <int D>
-__device__ __forceinline__ void split_query(const u32x4 (&w)[4], int g, i32x8 (&q)[3], uint32_t& scales) {
-    typedef uint32_t u32x16 __attribute__((ext_vector_type(16)));
-    u32x16 a;
-    u16x2 top = {0, 0};
+__device__ __forceinline__ void split_query(const u32x4 (&w)[4], float scale, int g, i32x8 (&q)[3], uint32_t& scales) {
+    float x[32];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-        a[i] = w[i / 4][i % 4];
-        top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, a[i] & 0x7FFF7FFFu));
+        const uint32_t v = w[i / 4][i % 4];
+        x[2 * i] = __uint_as_float(v << 16) * scale;
+        x[2 * i + 1] = __uint_as_float(v & 0xFFFF0000u) * scale;
     }
-    const uint32_t field = max((uint32_t)top.x, (uint32_t)top.y) >> 7;
-    const uint32_t e = max(field, 12u) - 2u;
-    const bf16x32 x = __builtin_bit_cast(bf16x32, a);
-    const float s0 = __uint_as_float(e << 23), s1 = __uint_as_float((e - 4u) << 23), s2 = __uint_as_float((e - 10u) << 23);
-    const u32x6 p0 = __builtin_amdgcn_cvt_scalef32_pk32_fp6_bf16(x, s0);
-    const bf16x32 r0 = difference(x, __builtin_amdgcn_cvt_scalef32_pk32_bf16_fp6(p0, s0));
-    const u32x6 p1 = __builtin_amdgcn_cvt_scalef32_pk32_fp6_bf16(r0, s1);
-    const bf16x32 r1 = difference(r0, __builtin_amdgcn_cvt_scalef32_pk32_bf16_fp6(p1, s1));
-    const u32x6 p2 = __builtin_amdgcn_cvt_scalef32_pk32_fp6_bf16(r1, s2);
+    const bf16x32 b0 = as_bf16(x);
+    u16x2 top = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, __builtin_bit_cast(u32x16, b0)[i] & 0x7FFF7FFFu));
+    const uint32_t most = max((uint32_t)top.x, (uint32_t)top.y);
+    const uint32_t field = (most + 0xFu) >> 7;   // past 1.875 2^n: of 2^(n+1)
+    const uint32_t e = max(field, 11u) - 2u;
+    const float s0 = __uint_as_float(e << 23), s1 = __uint_as_float((e - 4u) << 23), s2 = __uint_as_float((e - 9u) << 23);
+    const u32x6 p0 = __builtin_amdgcn_cvt_scalef32_pk32_fp6_bf16(b0, s0);
+    take_off(x, __builtin_amdgcn_cvt_scalef32_pk32_bf16_fp6(p0, s0));
+    const u32x6 p1 = __builtin_amdgcn_cvt_scalef32_pk32_fp6_bf16(as_bf16(x), s1);
+    take_off(x, __builtin_amdgcn_cvt_scalef32_pk32_bf16_fp6(p1, s1));
+    const u32x6 p2 = __builtin_amdgcn_cvt_scalef32_pk32_fp6_bf16(as_bf16(x), s2);
     if constexpr (D == 128) {
         q[0] = widen(p0);
         q[1] = widen(p1);
         q[2] = widen(p2);
-        scales = e | (e - 4u) << 8 | (e - 10u) << 16;
+        scales = e | (e - 4u) << 8 | (e - 9u) << 16;
     } else {   // the upper half of the lanes has the same channels: the second part, and nothing
         const bool up = g >= 2;
         u32x6 first, second;
@@ -444,17 +534,17 @@ __device__ __forceinline__ void split_query(const u32x4 (&w)[4], int g, i32x8 (&
         q[0] = widen(first);
         q[1] = widen(second);
         q[2] = q[1];   // not used
-        scales = (up ? e - 4u : e) | (e - 10u) << 8;
+        scales = (up ? e - 4u : e) | (e - 9u) << 8;
     }
-    if (field == 255u) scales = 0xFFFFFFFFu;
+    if (most >= 0x7F80u) scales = 0xFFFFFFFFu;
 }
 
 // The rows [row0, row0 + 16 NQ) of a sequence's (query, head of the group) pairs; rows past the last one see what it sees.
 template <int D, int NQ>
-__device__ __forceinline__ void set_ranges(Rows<NQ>& rows, const Attention& a, const Span& s, int group, int64_t row0,
+__device__ __forceinline__ void set_ranges(Rows<NQ>& rows, const Attention& a, const Span& s, int group, int row0,
                                            const Lane<D>& ln) {
-    const int64_t last = (int64_t)s.n * group - 1;
-    const int i_first = (int)(row0 / group), i_last = (int)(min(row0 + 16 * NQ - 1, last) / group);
+    const int last = s.n * group - 1;
+    const int i_first = row0 / group, i_last = min(row0 + 16 * NQ - 1, last) / group;
     const int p0 = s.len - s.n;   // position of query 0
     if (a.causal) {
         rows.lo_all = first_seen(a, s, i_first);
@@ -467,63 +557,67 @@ __device__ __forceinline__ void set_ranges(Rows<NQ>& rows, const Attention& a, c
     }
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
-        const int q = (int)(min(row0 + 16 * i + ln.n, last) / group);
+        const int q = (int)((uint32_t)min(row0 + 16 * i + ln.n, last) / (uint32_t)group);
         rows.lo[i] = a.causal ? first_seen(a, s, q) : 0;
         rows.hi[i] = a.causal ? max(0, p0 + q + 1) : s.len;
     }
 }
 
-template <int D, int NQ>
-__device__ __forceinline__ void load_queries(Rows<NQ>& rows, const Attention& a, const Span& s, int kv_head, int group,
-                                             int64_t row0, const Lane<D>& ln) {
-    const int64_t last = (int64_t)s.n * group - 1;
-    const int block = D == 128 ? ln.g : ln.g & 1;
-    u32x4 w[NQ][4];
-#pragma unroll
-    for (int i = 0; i < NQ; ++i) {
-        const int64_t row = min(row0 + 16 * i + ln.n, last);
-        const int64_t q = row / group;
-        const uint16_t* p = a.q + (s.first + q) * a.q_stride + ((int64_t)kv_head * group + (row - q * group)) * D + block * 32;
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            w[i][b] = *reinterpret_cast<const u32x4*>(p + 8 * b);
-            if (a.scale == 0.0f) w[i][b] = u32x4{0, 0, 0, 0};
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < NQ; ++i) split_query<D>(w[i], ln.g, rows.q[i], rows.qs[i]);
-}
-
-// Steps first, first + stride, .. below `last` of a wave's rows: the next step's bytes are on their way while one is worked on.
+// Steps first, first + stride, .. below `last` of a wave's rows. The bytes of the steps to come are on their way while
+// one is worked on.
 template <int D, int NQ>
 __device__ __forceinline__ void run_steps(const Attention& a, const CacheView& c, const int32_t* table, const Span& s,
-                                          int kv_head, int group, int64_t row0, int first, int last, int stride,
+                                          int kv_head, int group, int row0, int first, int last, int stride,
                                           Sums<D, NQ>& sums, const Lane<D>& ln) {
     Rows<NQ> rows;
     set_ranges<D, NQ>(rows, a, s, group, row0, ln);
     sums.clear();
     if (c.slots == 0) return;   // no page is there
-    // 0 has to leave a masked score's -infinity alone: the queries become zeros instead
-    const float scale = a.scale > 0.0f ? a.scale * kLog2e : 1.0f;
     // steps with a token that some row sees
-    first = max(first, 0);
     int at = first;
     const int low = rows.lo_all / kStep;
-    if (at < low) at += (low - at + stride - 1) / stride * stride;
-    const int end = min(last, (rows.hi_all + kStep - 1) / kStep);
+    if (at < low) at += (int)((uint32_t)(low - at + stride - 1) / (uint32_t)stride) * stride;
+    const int end = min(last, (int)(((uint32_t)rows.hi_all + kStep - 1) / kStep));
     if (at >= end) return;
-    Stage<D> st[2];
-    load_step<D, NQ>(st[0], a, c, table, kv_head, at * kStep, rows, ln);
-    load_queries<D, NQ>(rows, a, s, kv_head, group, row0, ln);
+    // the queries' bytes first: their parts are made while the first tokens are on their way
+    u32x4 w[NQ][4];
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+        const int row = min(row0 + 16 * i + ln.n, s.n * group - 1);
+        const int q = (int)((uint32_t)row / (uint32_t)group);
+        const int block = D == 128 ? ln.g : ln.g & 1;
+        const uint16_t* p =
+            a.q + (int64_t)(s.first + q) * a.q_stride + (int64_t)(kv_head * group + (row - q * group)) * D + block * 32;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) w[i][b] = *reinterpret_cast<const u32x4*>(p + 8 * b);
+    }
+    const int lane = threadIdx.x % kWave;
+    int pages = pages_ahead(a, c, table, at, stride, rows.lo_all, rows.hi_all, lane);
+    int later = pages_ahead(a, c, table, at + 32 * stride, stride, rows.lo_all, rows.hi_all, lane);
+    int i = 0;       // place in `pages` of the step to load next
+    int ahead = at;  // and the step
+    Stage<D> st[kAhead<NQ>];
+    auto load = [&](Stage<D>& stage) {
+        load_step<D>(stage, c, pages, i, kv_head, ahead * kStep, ln);
+        ahead += stride;
+        if (++i == 32) {
+            i = 0;
+            pages = later;
+            later = pages_ahead(a, c, table, ahead + 32 * stride, stride, rows.lo_all, rows.hi_all, lane);
+        }
+    };
+#pragma unroll
+    for (int b = 0; b + 1 < kAhead<NQ>; ++b) load(st[b]);
+#pragma unroll
+    for (int b = 0; b < NQ; ++b) split_query<D>(w[b], a.scale * kLog2e, ln.g, rows.q[b], rows.qs[b]);
     for (;;) {
-        if (at + stride < end) load_step<D, NQ>(st[1], a, c, table, kv_head, (at + stride) * kStep, rows, ln);
-        take_step<D, NQ>(st[0], rows, sums, scale, at * kStep, ln);
-        at += stride;
-        if (at >= end) break;
-        if (at + stride < end) load_step<D, NQ>(st[0], a, c, table, kv_head, (at + stride) * kStep, rows, ln);
-        take_step<D, NQ>(st[1], rows, sums, scale, at * kStep, ln);
-        at += stride;
-        if (at >= end) break;
+#pragma unroll
+        for (int b = 0; b < kAhead<NQ>; ++b) {
+            load(st[(b + kAhead<NQ> - 1) % kAhead<NQ>]);   // past the end too: then it is the cache's first tokens, or a neighbour's
+            take_step<D, NQ>(st[b], rows, sums, at * kStep, ln);
+            at += stride;
+            if (at >= end) return;
+        }
     }
 }
 
@@ -552,22 +646,26 @@ __device__ __forceinline__ void store_out(uint16_t* p, const float (&v)[NJ]) {
     else *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
 }
 
-// A worker's place in the workspace: two partial results (of the segment it begins in and of the one it ends in), each
-// 16 NQ rows of D sums, maximum and total; then a record for the joining kernel.
+// Where a segment (a tile of a sequence) was cut: its parts are the second one of worker `from` and the first ones of the
+// workers up to `to`.
 struct Record {
-    int64_t row0, first;    // rows of the sequence, its first query
-    int from, rows, head;   // from: the worker whose second part is the first one; -1: nothing to join
-    int pad;
+    int row0, first;    // the tile's first row, the sequence's first query
+    int from, to;       // from == to: nothing to join
+    int rows, head;
+    int pad[2];
 };
 
+// A worker has room for two parts (of the segment it begins in and of the one it ends in): 16 NQ rows of D sums, then
+// maximum and total of each.
 template <int D, int NQ>
 constexpr size_t part_floats() { return (size_t)16 * NQ * (D + 2); }
 
-// Split form: workers take equal shares of all units (kUnit tokens of a tile), in a row; the waves of one take every
+// Split form: workers take equal shares of all units (2^unit_bits tokens of a tile), in a row; the waves of one take every
 // fourth step of its share and join in LDS.
 template <int D, int NQ>
-__global__ __launch_bounds__(kWaves * kWave) void attention_split_kernel(Attention a, CacheView c, float* parts,
-                                                                         Record* records, int workers) {
+__global__ __launch_bounds__(kWaves * kWave, 2) void attention_split_kernel(Attention a, CacheView c, float* parts,
+                                                                            Record* records, int workers,
+                                                                            int unit_bits, int record_count, bool by_segment) {
     constexpr int NJ = D / 16;
     constexpr int kRows = 16 * NQ;
     __shared__ float lo_o[kWaves][4 * NJ][kWave];
@@ -579,69 +677,63 @@ __global__ __launch_bounds__(kWaves * kWave) void attention_split_kernel(Attenti
     const int group = a.heads / c.heads;
     const Lane<D> ln(lane);
 
-    auto weight = [&](int64_t s) -> int64_t {
-        const Span sp = span_of(a, c.page_bits, s);
-        const int64_t tiles = ((int64_t)sp.n * group + kRows - 1) / kRows;
-        return tiles * c.heads * units_of(a, sp);
-    };
-    const Layout<decltype(weight)> plan(weight, a.seqs, lane);
-    const int64_t share = plan.total / workers, more = plan.total - share * workers;
-    int64_t u = id * share + min((int64_t)id, more);
-    const int64_t u_end = u + share + (id < more ? 1 : 0);
-    if (u >= u_end) {
-        if (threadIdx.x == 0) records[id].from = -1;
+    auto segments = [&](const Span& s) { return tiles_of(s, group, kRows) * c.heads; };
+    auto weight = [&](const Span& s) { return segments(s) * units_of(a, s, unit_bits); };
+    const Plan plan(a, c.page_bits, lane, weight);
+    if (!plan.ok) {
+        if (threadIdx.x == 0 && id < record_count) records[id].from = records[id].to = 0;
         return;
     }
-    const int64_t u_begin = u;
-    int64_t seq, begin;
-    plan.find(u, seq, begin);
-    Span s = span_of(a, c.page_bits, seq);
-    s.first = uniform64(s.first, 0);
-    s.n = uniform(s.n);
-    s.len = uniform(s.len);
-    int units = units_of(a, s);
-    int64_t tiles = ((int64_t)s.n * group + kRows - 1) / kRows;
-    int from = -1;
-    Record rec = {0, 0, -1, 0, 0, 0};
+    const uint32_t share = plan.total / (uint32_t)workers, more = plan.total - share * workers;
+    uint32_t u = id * share + min((uint32_t)id, more);
+    const uint32_t u_end = u + share + ((uint32_t)id < more ? 1 : 0);
+    const bool idle = u >= u_end;
+    uint32_t begin = 0, segs_before = 0;
+    int seq = idle ? 0 : plan.find(u, begin, weight);
+    if (by_segment) {   // a record for every segment there could be: worker i also writes the i-th where there is none
+        uint32_t all;
+        segs_before = plan.sum_before(seq, segments, all);
+        if (threadIdx.x == 0 && id < record_count && (uint32_t)id >= all) records[id].from = records[id].to = 0;
+    } else if (idle) {
+        if (threadIdx.x == 0) records[id].from = records[id].to = 0;
+    }
+    if (idle) return;
+    Span s = plan.span(seq);
+    uint32_t units = units_of(a, s, unit_bits), segs = segments(s);
+    Record cut = {};
     while (u < u_end) {
-        while (u >= begin + tiles * c.heads * units) {   // on to the next sequence that has queries
-            begin += tiles * c.heads * units;
-            ++seq;
-            s = span_of(a, c.page_bits, seq);
-            s.first = uniform64(s.first, 0);
-            s.n = uniform(s.n);
-            s.len = uniform(s.len);
-            units = units_of(a, s);
-            tiles = ((int64_t)s.n * group + kRows - 1) / kRows;
+        while (u >= begin + segs * units) {   // on to the next sequence that has queries
+            begin += segs * units;
+            segs_before += segs;
+            s = plan.span(++seq);
+            units = units_of(a, s, unit_bits);
+            segs = segments(s);
         }
-        const int64_t segment = (u - begin) / units;
-        const int64_t seg_begin = begin + segment * units;
+        const uint32_t segment = (u - begin) / units;
+        const uint32_t seg_begin = begin + segment * units;
         const int u0 = (int)(u - seg_begin);
-        const int u1 = (int)min((int64_t)units, u_end - seg_begin);
+        const int u1 = (int)min(units, u_end - seg_begin);
+        const uint32_t tiles = segs / (uint32_t)c.heads;
         const int head = (int)(segment / tiles);
-        const int64_t row0 = (segment - head * tiles) * kRows;
-        const int origin = (first_seen(a, s, 0) & ~(kStep - 1)) / kStep;
+        const int row0 = (int)(segment - head * tiles) * kRows;
+        const int origin = first_seen(a, s, 0) / kStep, steps = unit_bits - 5;
         Sums<D, NQ> sums;
-        run_steps<D, NQ>(a, c, a.page_table + seq * a.table_width, s, head, group, row0, origin + u0 * kWaves + wave,
-                         origin + u1 * kWaves, kWaves, sums, ln);
-        const bool whole = u0 == 0 && u1 == units;
-        const bool goes_on = u0 > 0;   // the segment's start is another worker's
-        float* part = parts + (2 * (size_t)id + (goes_on ? 0 : 1)) * part_floats<D, NQ>();
-        const int64_t rows_left = (int64_t)s.n * group - row0;
+        run_steps<D, NQ>(a, c, a.page_table + seq * a.table_width, s, head, group, row0, origin + (u0 << steps) + wave,
+                         origin + (u1 << steps), kWaves, sums, ln);
+        const bool whole = u0 == 0 && u1 == (int)units;
+        float* part = parts + (2 * (size_t)id + (u0 > 0 ? 0 : 1)) * part_floats<D, NQ>();
+        const int rows_left = s.n * group - row0;
 #pragma unroll
         for (int i = 0; i < NQ; ++i) {
             if (16 * i >= rows_left) break;
-            float l = sums.l[i];
-            l += __shfl_xor(l, 16, kWave);
-            l += __shfl_xor(l, 32, kWave);
             __syncthreads();
 #pragma unroll
             for (int j = 0; j < NJ; ++j)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) lo_o[wave][r * NJ + j][lane] = sums.o[i][j][r];
             if (lane < 16) {
-                lo_ml[wave][lane][0] = sums.m[i];
-                lo_ml[wave][lane][1] = l;
+                lo_ml[wave][lane][0] = sums.top(i);
+                lo_ml[wave][lane][1] = sums.l[i][0];
             }
             __syncthreads();
             float m = lo_ml[0][ln.n][0];
@@ -660,12 +752,12 @@ __global__ __launch_bounds__(kWaves * kWave) void attention_split_kernel(Attenti
             const int d = NJ * (4 * ln.g + wave);   // this lane's channels of row `at`
             if (at < rows_left) {
                 if (whole) {
-                    const int64_t row = row0 + at, q = row / group;
-                    const int h = head * group + (int)(row - q * group);
+                    const int row = row0 + at, q = (int)((uint32_t)row / (uint32_t)group);
+                    const int h = head * group + (row - q * group);
                     const float f = last_factor(m, total, a.sinks, h);
 #pragma unroll
                     for (int j = 0; j < NJ; ++j) o[j] *= f;
-                    store_out<NJ>(a.out + ((s.first + q) * a.heads + h) * D + d, o);
+                    store_out<NJ>(a.out + ((int64_t)(s.first + q) * a.heads + h) * D + d, o);
                 } else {
 #pragma unroll
                     for (int j = 0; j < NJ; j += 4)
@@ -677,28 +769,31 @@ __global__ __launch_bounds__(kWaves * kWave) void attention_split_kernel(Attenti
                 }
             }
         }
-        if (goes_on && u1 == units) {   // its last part: this worker's record names the join
-            const int64_t edge = more * (share + 1);
-            from = (int)(seg_begin < edge ? seg_begin / (share + 1) : more + (seg_begin - edge) / share);
-            rec = {row0, s.first, from, (int)min((int64_t)kRows, rows_left), head, 0};
+        if (u1 == (int)units) {   // the segment ends here
+            Record r = {row0, s.first, 0, 0, min(kRows, rows_left), head, {0, 0}};
+            if (u0 > 0) {
+                const uint32_t edge = more * (share + 1);
+                r.from = (int)(seg_begin < edge ? seg_begin / (share + 1) : more + (seg_begin - edge) / share);
+                r.to = id;
+                cut = r;
+            }
+            if (by_segment && threadIdx.x == 0) records[segs_before + segment] = r;
         }
         u = seg_begin + u1;
     }
-    (void)u_begin;
-    if (threadIdx.x == 0) records[id] = rec;
+    if (!by_segment && threadIdx.x == 0) records[id] = cut;
 }
 
-// Joins the parts of the segment that worker blockIdx.x ended: the second part of worker `from`, the first ones of the
-// workers after it. A wave a row.
+// Joins the parts of a segment, a wave a row: two parts at a time, half a wave each, sixteen of them on their way.
 template <int D, int NQ>
 __global__ __launch_bounds__(kWaves * kWave) void attention_join_kernel(Attention a, CacheView c, const float* parts,
                                                                         const Record* records) {
     constexpr int kRows = 16 * NQ;
-    constexpr int kEach = D / kWave;
+    constexpr int kEach = D / 32;
     const Record r = records[blockIdx.x];
-    if (r.from < 0) return;
-    const int lane = threadIdx.x % kWave;
-    const int count = (int)blockIdx.x - r.from + 1;
+    if (r.from == r.to) return;
+    const int lane = threadIdx.x % kWave, half = lane / 32, place = lane % 32;
+    const int count = r.to - r.from + 1;
     const int group = a.heads / c.heads;
     for (int at = blockIdx.y * kWaves + threadIdx.x / kWave; at < r.rows; at += gridDim.y * kWaves) {
         auto part_of = [&](int i) { return parts + (2 * (size_t)(r.from + i) + (i == 0 ? 1 : 0)) * part_floats<D, NQ>(); };
@@ -707,69 +802,70 @@ __global__ __launch_bounds__(kWaves * kWave) void attention_join_kernel(Attentio
         for (int x = 32; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor(m, x, kWave));
         const float m0 = finite_or_zero(m);
         float total = 0.0f, o[kEach] = {};
-        for (int i0 = 0; i0 < count; i0 += kWave) {
-            float f = 0.0f;
-            if (i0 + lane < count) {
-                const float* ml = part_of(i0 + lane) + (size_t)kRows * D + 2 * at;
-                f = exp2_raw(ml[0] - m0);
-                total += f * ml[1];
-            }
-            const int here = min(kWave, count - i0);
-#pragma unroll 8
-            for (int i = 0; i < here; ++i) {
-                const float* p = part_of(i0 + i) + (size_t)at * D + lane * kEach;
-                const float w = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(f), i));
+        for (int i0 = 0; i0 < count; i0 += 16) {
+            float v[8][kEach], ml[8][2];
 #pragma unroll
-                for (int e = 0; e < kEach; ++e) o[e] += w * p[e];
+            for (int b = 0; b < 8; ++b) {
+                const float* p = part_of(min(i0 + 2 * b + half, count - 1));
+#pragma unroll
+                for (int e = 0; e < kEach; ++e) v[b][e] = p[(size_t)at * D + place * kEach + e];
+                ml[b][0] = p[(size_t)kRows * D + 2 * at];
+                ml[b][1] = p[(size_t)kRows * D + 2 * at + 1];
+            }
+#pragma unroll
+            for (int b = 0; b < 8; ++b) {
+                if (i0 + 2 * b + half < count) {
+                    const float f = exp2_raw(ml[b][0] - m0);
+                    total += f * ml[b][1];
+#pragma unroll
+                    for (int e = 0; e < kEach; ++e) o[e] += f * v[b][e];
+                }
             }
         }
-        total = group_sum<kWave>(total);
-        const int64_t row = r.row0 + at, q = row / group;
-        const int h = r.head * group + (int)(row - q * group);
+        total += __shfl_xor(total, 32, kWave);
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) o[e] += __shfl_xor(o[e], 32, kWave);
+        const int row = r.row0 + at, q = (int)((uint32_t)row / (uint32_t)group);
+        const int h = r.head * group + (row - q * group);
         const float f = last_factor(m, total, a.sinks, h);
-        uint16_t* out = a.out + ((r.first + q) * a.heads + h) * D + lane * kEach;
-        if constexpr (kEach == 2) *reinterpret_cast<uint32_t*>(out) = pack_bf16x2(o[0] * f, o[1] * f);
-        else *out = (uint16_t)f32_to_bf16_rne(o[0] * f);
+        if (half == 0) {
+            uint16_t* out = a.out + ((int64_t)(r.first + q) * a.heads + h) * D + place * kEach;
+            if constexpr (kEach == 4)
+                *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(o[0] * f, o[1] * f), pack_bf16x2(o[2] * f, o[3] * f));
+            else *reinterpret_cast<uint32_t*>(out) = pack_bf16x2(o[0] * f, o[1] * f);
+        }
     }
 }
 
 // Many rows: a wave has a tile of its own and goes through all that it sees; the tiles with the most tokens first.
 template <int D, int NQ>
-__global__ __launch_bounds__(kWaves * kWave) void attention_rows_kernel(Attention a, CacheView c) {
+__global__ __launch_bounds__(kWaves * kWave, 2) void attention_rows_kernel(Attention a, CacheView c) {
     constexpr int NJ = D / 16;
     constexpr int kRows = 16 * NQ;
     const int lane = threadIdx.x % kWave, wave = uniform(threadIdx.x / kWave);
     const int group = a.heads / c.heads;
     const Lane<D> ln(lane);
-    auto weight = [&](int64_t s) -> int64_t {
-        return ((int64_t)span_of(a, c.page_bits, s).n * group + kRows * kWaves - 1) / (kRows * kWaves);
-    };
-    const Layout<decltype(weight)> plan(weight, a.seqs, lane);
-    const int64_t at = plan.total - 1 - (int64_t)blockIdx.x / c.heads;
-    if (at < 0) return;
-    const int head = (int)(blockIdx.x % c.heads);
-    int64_t seq, begin;
-    plan.find(at, seq, begin);
-    Span s = span_of(a, c.page_bits, seq);
-    s.first = uniform64(s.first, 0);
-    s.n = uniform(s.n);
-    s.len = uniform(s.len);
-    const int64_t row0 = ((at - begin) * kWaves + wave) * kRows;
-    const int64_t rows_left = (int64_t)s.n * group - row0;
+    auto weight = [&](const Span& s) { return tiles_of(s, group, kRows * kWaves); };
+    const Plan plan(a, c.page_bits, lane, weight);
+    const int at = (int)plan.total - 1 - (int)(blockIdx.x / (uint32_t)c.heads);
+    if (at < 0 || !plan.ok) return;
+    const int head = (int)(blockIdx.x % (uint32_t)c.heads);
+    uint32_t begin;
+    const int seq = plan.find((uint32_t)at, begin, weight);
+    const Span s = plan.span(seq);
+    const int row0 = ((at - (int)begin) * kWaves + wave) * kRows;
+    const int rows_left = s.n * group - row0;
     if (rows_left <= 0) return;
     Sums<D, NQ> sums;
     run_steps<D, NQ>(a, c, a.page_table + seq * a.table_width, s, head, group, row0, 0, kFarRight, 1, sums, ln);
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
         const int r = 16 * i + ln.n;
-        float l = sums.l[i];
-        l += __shfl_xor(l, 16, kWave);
-        l += __shfl_xor(l, 32, kWave);
         if (r < rows_left) {
-            const int64_t row = row0 + r, q = row / group;
-            const int h = head * group + (int)(row - q * group);
-            const float f = last_factor(sums.m[i], l, a.sinks, h);
-            uint16_t* out = a.out + ((s.first + q) * a.heads + h) * D;
+            const int row = row0 + r, q = (int)((uint32_t)row / (uint32_t)group);
+            const int h = head * group + (row - q * group);
+            const float f = last_factor(sums.top(i), sums.l[i][0], a.sinks, h);
+            uint16_t* out = a.out + ((int64_t)(s.first + q) * a.heads + h) * D;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 float o[NJ];
@@ -790,26 +886,32 @@ struct Form {
     bool split;
     int nq;
     int workers;
+    int64_t segments;   // at most
+    int join_rows;      // workgroups a segment's rows are joined by
+    int records() const { return (int)(segments < workers ? segments : workers); }
 };
 
 // Which form a call takes, from what the host knows: rows a sequence on the average, tiles in all.
 Form form_of(int64_t tokens, int64_t seqs, int64_t heads, int64_t kv_heads) {
     const int64_t group = heads / kv_heads, cus = device_cu_count();
     const int64_t mean = (tokens + seqs - 1) / seqs * group;
-    const int64_t wide = most_tiles(tokens, seqs, group, 64 * kWaves) * kv_heads;
-    if (mean > 64 && wide >= cus) return {false, 4, 0};
-    if (mean > 32) return {true, 4, (int)(cus)};
-    if (mean > 16) return {true, 2, (int)(2 * cus)};
-    return {true, 1, (int)(3 * cus)};
+    const int64_t wide = most_tiles(tokens, seqs, group, 32 * kWaves) * kv_heads;
+    if (mean > 64 && wide >= cus) return {false, 2, 0, 0, 0};
+    const int nq = mean > 16 ? 2 : 1;
+    return {true, nq, (int)(2 * cus), most_tiles(tokens, seqs, group, 16 * nq) * kv_heads,
+            (int)(((mean < 16 * nq ? mean : 16 * nq) + kWaves - 1) / kWaves)};
 }
 
 template <int D, int NQ>
-hipError_t split_form(const Attention& a, const CacheView& c, int workers, void* workspace, hipStream_t stream) {
+hipError_t split_form(const Attention& a, const CacheView& c, const Form& f, void* workspace, hipStream_t stream) {
     Record* records = static_cast<Record*>(workspace);
-    float* parts = reinterpret_cast<float*>(records + workers);
-    attention_split_kernel<D, NQ><<<workers, kWaves * kWave, 0, stream>>>(a, c, parts, records, workers);
+    float* parts = reinterpret_cast<float*>(records + f.records());
+    int unit_bits = 7;   // four steps, more where the number of units would not fit 32 bits
+    while (f.segments > ((int64_t)1 << 30) / (((a.table_width << c.page_bits) >> unit_bits) + 2)) ++unit_bits;
+    attention_split_kernel<D, NQ><<<f.workers, kWaves * kWave, 0, stream>>>(a, c, parts, records, f.workers, unit_bits, f.records(),
+                                                                            f.segments <= f.workers);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-    attention_join_kernel<D, NQ><<<dim3(workers, 4 * NQ), kWaves * kWave, 0, stream>>>(a, c, parts, records);
+    attention_join_kernel<D, NQ><<<dim3(f.records(), f.join_rows), kWaves * kWave, 0, stream>>>(a, c, parts, records);
     return hipGetLastError();
 }
 
@@ -817,13 +919,11 @@ template <int D>
 hipError_t attend(const Attention& a, const CacheView& c, void* workspace, hipStream_t stream) {
     const Form f = form_of(a.tokens, a.seqs, a.heads, c.heads);
     if (!f.split) {
-        const int64_t grid = most_tiles(a.tokens, a.seqs, a.heads / c.heads, 64 * kWaves) * c.heads;
-        attention_rows_kernel<D, 4><<<(unsigned)grid, kWaves * kWave, 0, stream>>>(a, c);
+        const int64_t grid = most_tiles(a.tokens, a.seqs, a.heads / c.heads, 32 * kWaves) * c.heads;
+        attention_rows_kernel<D, 2><<<(unsigned)grid, kWaves * kWave, 0, stream>>>(a, c);
         return hipGetLastError();
     }
-    if (f.nq == 4) return split_form<D, 4>(a, c, f.workers, workspace, stream);
-    if (f.nq == 2) return split_form<D, 2>(a, c, f.workers, workspace, stream);
-    return split_form<D, 1>(a, c, f.workers, workspace, stream);
+    return f.nq == 2 ? split_form<D, 2>(a, c, f, workspace, stream) : split_form<D, 1>(a, c, f, workspace, stream);
 }
 
 }  // namespace
@@ -831,7 +931,7 @@ hipError_t attend(const Attention& a, const CacheView& c, void* workspace, hipSt
 size_t attention_workspace_bytes(int64_t tokens, int64_t seqs, int64_t heads, int64_t kv_heads, int64_t head_dim) {
     const Form f = form_of(tokens, seqs, heads, kv_heads);
     if (!f.split) return 0;
-    return (size_t)f.workers * (sizeof(Record) + 2 * (size_t)16 * f.nq * (head_dim + 2) * sizeof(float));
+    return f.records() * sizeof(Record) + (size_t)f.workers * 2 * 16 * f.nq * (head_dim + 2) * sizeof(float);
 }
 
 hipError_t launch_attention(const Attention& a, const CacheView& c, void* workspace, hipStream_t stream) {

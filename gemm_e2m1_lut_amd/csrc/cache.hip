@@ -24,6 +24,8 @@
 // a branch that the whole workgroup takes alike. The codes of a head are 64 (or
 // 32) contiguous bytes and its scales 4 (or 2): [page][head][place], the layout
 // in which attention reads a head's tokens in one run.
+#include <limits.h>
+
 #include "device.hpp"
 #include "kernels.hpp"
 
@@ -246,31 +248,32 @@ __device__ __forceinline__ uint4 decode8(uint32_t c, uint32_t e) {
                       fp4x2_to_bf16x2<3>(c, sc));
 }
 
-// One group of lanes per token and head, keys and values together.
+// One group of lanes per token and head, keys and values together; a grid that does not cover all rows goes round.
 template <int D>
 __global__ __launch_bounds__(kThreads) void cache_read_kernel(CacheView c, const int64_t* __restrict__ slots,
                                                               uint16_t* __restrict__ k_out, uint16_t* __restrict__ v_out,
-                                                              int64_t tokens, int32_t* err_flag) {
+                                                              int64_t rows, int32_t* err_flag) {
     constexpr int kLanes = D / 8;
     const int lane = threadIdx.x % kLanes;
-    const int64_t row = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / kLanes;
-    if (row >= tokens * c.heads) return;
-    const int64_t t = row / c.heads;
-    const int head = (int)(row - t * c.heads);
-    const int64_t slot = slots[t];
-    uint4 ko = make_uint4(0, 0, 0, 0), vo = ko;
-    if (slot >= 0 && slot < c.slots) {
-        const int64_t at = cache_row(slot, head, c);
-        const uint32_t kc = *reinterpret_cast<const uint32_t*>(c.k_codes + at * (D / 2) + lane * 4);
-        const uint32_t vc = *reinterpret_cast<const uint32_t*>(c.v_codes + at * (D / 2) + lane * 4);
-        const uint32_t ke = c.k_scales[at * (D / 32) + lane / 4], ve = c.v_scales[at * (D / 32) + lane / 4];
-        ko = decode8(kc, ke);
-        vo = decode8(vc, ve);
-    } else if (slot >= 0 && err_flag) {
-        *err_flag = 1;
+    for (int64_t row = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / kLanes; row < rows;
+         row += (int64_t)gridDim.x * (kThreads / kLanes)) {
+        const int64_t t = rows <= INT_MAX ? (int64_t)((uint32_t)row / (uint32_t)c.heads) : row / c.heads;
+        const int head = (int)(row - t * c.heads);
+        const int64_t slot = slots[t];
+        uint4 ko = make_uint4(0, 0, 0, 0), vo = ko;
+        if (slot >= 0 && slot < c.slots) {
+            const int64_t at = cache_row(slot, head, c);
+            const uint32_t kc = *reinterpret_cast<const uint32_t*>(c.k_codes + at * (D / 2) + lane * 4);
+            const uint32_t vc = *reinterpret_cast<const uint32_t*>(c.v_codes + at * (D / 2) + lane * 4);
+            const uint32_t ke = c.k_scales[at * (D / 32) + lane / 4], ve = c.v_scales[at * (D / 32) + lane / 4];
+            ko = decode8(kc, ke);
+            vo = decode8(vc, ve);
+        } else if (slot >= 0 && err_flag) {
+            *err_flag = 1;
+        }
+        store_nt16(k_out + row * D + lane * 8, ko.x, ko.y, ko.z, ko.w);
+        store_nt16(v_out + row * D + lane * 8, vo.x, vo.y, vo.z, vo.w);
     }
-    store_nt16(k_out + row * D + lane * 8, ko.x, ko.y, ko.z, ko.w);
-    store_nt16(v_out + row * D + lane * 8, vo.x, vo.y, vo.z, vo.w);
 }
 
 // Heads a group takes one after another: all of a token's angles are read again by each of its groups, so a large call
@@ -334,11 +337,13 @@ hipError_t launch_norm_rope_write(const NormRope& a, bool bf16, const CacheView&
 
 hipError_t launch_cache_read(const CacheView& c, const int64_t* slots, uint16_t* k_out, uint16_t* v_out, int64_t tokens,
                              int32_t* err_flag, hipStream_t stream) {
-    const int64_t grid = (tokens * c.heads * (c.head_dim / 8) + kThreads - 1) / kThreads;
+    const int64_t rows = tokens * c.heads;
+    const int64_t need = (rows * (c.head_dim / 8) + kThreads - 1) / kThreads;
+    const unsigned grid = (unsigned)(need < 1 << 20 ? need : 1 << 20);
     if (c.head_dim == 128)
-        cache_read_kernel<128><<<(unsigned)grid, kThreads, 0, stream>>>(c, slots, k_out, v_out, tokens, err_flag);
+        cache_read_kernel<128><<<grid, kThreads, 0, stream>>>(c, slots, k_out, v_out, rows, err_flag);
     else
-        cache_read_kernel<64><<<(unsigned)grid, kThreads, 0, stream>>>(c, slots, k_out, v_out, tokens, err_flag);
+        cache_read_kernel<64><<<grid, kThreads, 0, stream>>>(c, slots, k_out, v_out, rows, err_flag);
     return hipGetLastError();
 }
 

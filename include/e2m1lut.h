@@ -321,6 +321,7 @@ int int8_gemm(const int8_t* x, const float* x_scale, const int8_t* w, const floa
 #define E2M1_CACHE_MAX_PAGE 65536
 #define E2M1_CACHE_MAX_TOKENS ((int64_t)1 << 26)
 #define E2M1_ATTENTION_MAX_ROWS ((int64_t)1 << 29)   /* tokens * heads of one mxfp4_attention call */
+#define E2M1_ATTENTION_MAX_LENGTH ((int64_t)1 << 30) /* tokens its page table has room for, a sequence */
 
 /*
  * mxfp4_cache_write -- rows of keys and values into the cache.
@@ -401,12 +402,12 @@ size_t mxfp4_attention_workspace_size(int64_t tokens, int64_t seqs, int64_t head
  * Head h reads kv head h / (heads / kv_heads):
  *   out = sum_j exp(s_j) v_j / (sum_j exp(s_j) + exp(sinks[h])), s_j = scale q . k_j
  * over the tokens it sees (no sink term where sinks is NULL), zeros where it
- * sees none. Scores, maxima and sums are fp32, an element of q counts to within
- * 2^-16 of the largest magnitude of its 32 channels (or 2^-131, if that is more);
- * the weights exp(s_j - max) are rounded to bf16 before they meet the values,
- * out is rounded to bf16 once. A query that sees
- * a token with a scale byte 255 in its key or value of that head is NaN in that head;
- * what is in tokens that it does not see changes nothing.
+ * sees none. Scores, maxima and sums are fp32, an element of scale q counts to
+ * within 2^-13 of the largest magnitude of its 32 channels (or 2^-130, if that is
+ * more), the weights exp(s_j - max) are rounded to bf16, out is rounded to bf16
+ * once. A query that sees a key with a scale byte 255 is NaN in that head, one that
+ * sees a value with it in that block's 32 channels; what is in tokens that it does not
+ * see changes nothing.
  *   q           bf16 [tokens, heads, head_dim] (16-byte aligned), a token's heads dense, tokens q_stride
  *               elements apart (at least heads * head_dim, a multiple of 8)
  *   page_table  int32 [seqs, table_width]; entries past a sequence's tokens are not read
@@ -420,10 +421,12 @@ size_t mxfp4_attention_workspace_size(int64_t tokens, int64_t seqs, int64_t head
  *               where that size is 0); the call writes it, so calls that overlap
  *               in time need workspaces of their own
  * A token on a page outside [0, pages) is not seen, tokens past table_width
- * pages neither, and err_flag is set for both. A negative length counts as 0.
+ * pages neither, and err_flag is set for both. A negative length counts as 0,
+ * an offset outside 0 .. tokens as the nearer end. Where an offset is below the
+ * one before it nothing is written but err_flag.
  * Requires heads a multiple of kv_heads, at most E2M1_CACHE_MAX_HEADS, tokens *
  * heads <= E2M1_ATTENTION_MAX_ROWS, 0 <= seqs <= E2M1_CACHE_MAX_TOKENS,
- * table_width * page_size < 2^31, 0 <= scale <= 2^126, window >= 0 (0: none) and
+ * table_width * page_size <= E2M1_ATTENTION_MAX_LENGTH, 0 <= scale <= 2^126, window >= 0 (0: none) and
  * 0 without causal.
  * Errors: E2M1_ERR_WORKSPACE as in ternary_gemm.
  */

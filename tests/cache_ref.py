@@ -77,10 +77,11 @@ def rotate(x: np.ndarray, cos: np.ndarray, sin: np.ndarray, interleaved: bool):
 def attention(q, keys, values, scale: float, causal: bool, window: int, sinks=None):
     """One sequence: q [n, heads, d], keys and values [l, kv, d] in 64 bits -> (out, bound of what rounding may add).
 
-    The bound counts: the weights' rounding to bf16 (half a step of each, relative, times |v|), the result's own, and the
-    scores' errors, which enter the weights and the sum (twice). A score's: a query is taken as sums of parts that
-    leave at most 2^-16 of its block's largest magnitude (or 2^-131), products add in fp32 (d terms and the accumulator's roundings),
-    then one product and the exponential's argument, and the exponential itself (2 steps).
+    The bound counts: the weights' rounding to bf16 (half a step u of each, relative, in the product and in the sum: with
+    weights p (1 + e) the result moves by sum p e (v - out) / sum p (1 + e), at most u (sum p |v| / sum p + |out|) /
+    (1 - u)), the result's own, and the scores' errors, which enter the weights and the sum (twice). A score's: a query times
+    the scale is taken as sums of parts that leave at most 2^-13 of its block's largest magnitude (or 2^-130), products add in
+    fp32 (d terms and the accumulator's roundings), with the maximum taken off, and the exponential itself (2 steps).
     A weight below the smallest normal number counts as zero. The maximum in use is never above the row's, so the
     largest weight, and the sum with it, is at least 1, and what is lost of the result is at most 2^-126 |v| a token."""
     n, heads, d = q.shape
@@ -96,13 +97,13 @@ def attention(q, keys, values, scale: float, causal: bool, window: int, sinks=No
             seen &= j > pos - window
     for h in range(heads):
         k, v = keys[:, h // (heads // kv)], values[:, h // (heads // kv)]
-        bad = np.isnan(k).any(-1) | np.isnan(v).any(-1)
-        k, v = np.where(bad[:, None], 0.0, k), np.where(bad[:, None], 0.0, v)
+        bad_k, bad_v = np.isnan(k).any(-1), np.isnan(v)
+        k, v = np.where(bad_k[:, None], 0.0, k), np.where(bad_v, 0.0, v)
         x = np.asarray(q[:, h], np.float64)
         s = scale * (x @ k.T)
         size = scale * (np.abs(x) @ np.abs(k).T)
-        blocks = np.maximum(2.0**-16 * np.abs(x).reshape(n, d // 32, 32).max(-1), 2.0**-131)
-        parts = scale * (blocks @ np.abs(k).reshape(length, d // 32, 32).sum(-1).T)
+        blocks = np.maximum(2.0**-13 * scale * np.abs(x).reshape(n, d // 32, 32).max(-1), 2.0**-130)
+        parts = (blocks @ np.abs(k).reshape(length, d // 32, 32).sum(-1).T)
         delta = np.where(seen, parts + (d + 8) * U_F32 * size + 4 * U_F32 * np.abs(s), 0.0).max(1, initial=0.0)
         delta = np.expm1(2 * delta + 8 * U_F32)
         s = np.where(seen, s, -np.inf)
@@ -116,9 +117,11 @@ def attention(q, keys, values, scale: float, causal: bool, window: int, sinks=No
         o = (p @ v) / total[:, None]
         mag = (p @ np.abs(v)) / total[:, None]
         # sums of `length` terms in fp32, in any order
-        bound[:, h] = mag * (U_BF16 * (1 + delta[:, None]) + 2 * delta[:, None] + (length + 8) * U_F32)
+        bound[:, h] = (mag + np.abs(o)) * U_BF16 * (1 + delta[:, None]) / (1 - U_BF16)
+        bound[:, h] += mag * (2 * delta[:, None] + 2 * (length + 8) * U_F32)
         bound[:, h] += 2.0**-126 * (seen.astype(np.float64) @ np.abs(v))
         bound[:, h] += U_BF16 * (np.abs(o) + bound[:, h]) + 2.0**-134
-        o[(seen & bad[None, :]).any(1)] = np.nan
+        o[(seen & bad_k[None, :]).any(1)] = np.nan
+        o[(seen.astype(np.float64) @ bad_v.astype(np.float64)) > 0] = np.nan
         out[:, h] = o
     return out, bound

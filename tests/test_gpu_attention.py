@@ -134,6 +134,25 @@ def test_scales(gpu, scale, size):
     run(gpu, Case([(1, 300), (20, 300), (90, 400)], 4, 2, 128, 16, 4, qsize=size), scale=scale)
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+def test_scores_of_single_channels(gpu, dim):
+    """Keys with one channel each against queries of many sizes: here the bound of a score has a single term, far below what
+    a missing or misplaced part of a query would be off."""
+    say(f"attention: single channels of {dim}")
+    case = Case([(3, 2)] * dim, 2, 1, dim, 16, 26)
+    r = np.random.default_rng(27)
+    q = np.sign(r.standard_normal((case.tokens, 2, dim))) * np.exp2(r.uniform(-8, 0, (case.tokens, 2, dim)))
+    case.q = torch.from_numpy(q.astype(np.float32)).bfloat16()
+    for s in range(dim):
+        page = case.table[s, 0]
+        for i in (0, 2):
+            x = np.zeros((2, 1, dim))
+            x[0, 0, s] = 64.0 if i == 0 else 1.0
+            x[1, 0, s] = 0.0 if i == 0 else -1.0
+            case.host[i][page, :, :2], case.host[i + 1][page, :, :2] = (t.transpose(1, 0, 2) for t in ref.encode(x))
+    run(gpu, case, causal=False, scale=0.5)
+
+
 def test_sinks_at_the_ends(gpu):
     say("attention: sinks of all sizes")
     sinks = np.array([-np.inf, -1e4, 0, 80, 1e4, -3e38], np.float32)
@@ -153,12 +172,17 @@ def test_what_is_not_seen_changes_nothing(gpu, garbage):
 
 @pytest.mark.parametrize("dim", [64, 128])
 @pytest.mark.parametrize("n", [1, 6, 90])
-def test_blocks_that_are_nan(gpu, dim, n):
-    """Keys and values with scale byte 255 make NaN of the rows and heads that see them, and of no other."""
+@pytest.mark.parametrize("zeros", [False, True])
+def test_blocks_that_are_nan(gpu, dim, n, zeros):
+    """Scale byte 255 in a key makes NaN of the rows and heads that see it, in a value of its block's channels there, and of
+    nothing else."""
     say(f"attention: NaN blocks, {n} queries, heads of {dim}")
     case = Case([(n, 200), (n, 150)], 4, 2, dim, 16, 7)
     for j, what, head in ((197, 1, 0), (199, 3, 1), (150, 3, 0), (60, 1, 1)):
-        case.host[what][case.table[0, j // 16], head, j % 16, dim // 32 - 1] = 255
+        at = case.table[0, j // 16], head, j % 16
+        case.host[what][at][dim // 32 - 1] = 255
+        if zeros:       # as the writer leaves them
+            case.host[what - 1][at][dim // 2 - 16:] = 0
     run(gpu, case)
     run(gpu, case, window=3)
     run(gpu, case, causal=False)
@@ -257,7 +281,32 @@ def test_rows_outside_the_sequences(gpu, lens):
     bad[-1] = 2**31 - 1        # past the rows: as far as they go
     bad[0] = -2**31
     gpu.mxfp4_attention(**{**d, "q_offsets": bad}, out=out)
-    torch.cuda.synchronize()
+    assert not (out == 7).all(-1).any()
+
+
+@pytest.mark.parametrize("n", [1, 90])
+@pytest.mark.parametrize("seqs", [3, 200])
+def test_offsets_that_descend(gpu, n, seqs):
+    """Nothing is written and the flag is set, also where rows would belong to many sequences."""
+    say(f"attention: descending offsets, {seqs} sequences of {n}")
+    case = Case([(n, 100)] * seqs, 4, 2, 64, 16, 25)
+    d = case.device()
+    flag = torch.zeros(1, dtype=torch.int32, device=DEV)
+    for change in ((1, 0, 10**6), (seqs - 1, seqs, -3), (0, seqs + 1, None)):
+        off = d["q_offsets"].clone()
+        if change[2] is None:
+            off[0::2] = 0
+            off[1::2] = case.tokens
+        else:
+            off[change[0]:change[1] + 1] = change[2]
+            off[1] = case.tokens
+        out = torch.full_like(d["q"], 7.0)
+        flag.zero_()
+        gpu.mxfp4_attention(**{**d, "q_offsets": off}, out=out, err_flag=flag)
+        descends = bool((off[1:] < off[:-1]).any())
+        assert descends and flag.item() == 1 and (out == 7).all()
+    out = gpu.mxfp4_attention(**d)
+    case.check(out, 64 ** -0.5)
 
 
 def test_strided_queries(gpu):
