@@ -21,13 +21,18 @@
 //     key is unpacked. The accumulator starts at minus the maximum in use: the
 //     result is the exponent of the weight. Heads of 64 channels fill half of the
 //     instruction's 128: the other half takes the second part of the same keys.
-//   * The scores come out transposed (a lane has 4 tokens of one query row), which
-//     is what the values' product takes as its B operand: the weights never
-//     leave their lane. Its A operand is the values transposed, 8 tokens of a
-//     channel a lane: a lane loads the codes of 8 channels of its 8 tokens,
-//     v_cvt_scalef32_pk_bf16_fp4 decodes pairs of channels with the token's scale
-//     and v_perm_b32 pairs the tokens: one operation an element, for all NQ tiles.
-//     The weights' sum is one more such product, with ones.
+//   * The scores come out transposed (a lane has 8 tokens of one query row), which
+//     is what the values' product takes as an operand: the weights never leave
+//     their lane. The values are its other operand, 8 tokens of 2 channels a lane:
+//     a lane loads the codes of D / 16 channels of 8 tokens, and
+//     v_cvt_scalef32_pk_bf16_fp4 decodes two channels of one token with the
+//     token's scale. A dense product wants two tokens of one channel side by side;
+//     here the contraction runs over (token, channel parity) instead and the
+//     weights are a 2:4 sparse operand (v_smfmac_f32_16x16x64_bf16) that is zero
+//     for the other parity: two products, of the even and of the odd channels, take
+//     the same registers with two index words, in the time of dense ones over the
+//     tokens, and nothing is permuted. Half an operation an element, for all NQ
+//     tiles. The weights' sum is one more such product, with ones.
 //   * The maximum is replaced only when a score passes it by 2^8 (a vote per step):
 //     weights are then at most 2^8, the sums fp32, and the usual step has no
 //     exchange between lanes and no rescaling.
@@ -45,14 +50,13 @@ namespace {
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr int kWaves = 4;          // of a workgroup
 constexpr int kStep = 32;          // tokens a wave takes at a time
-// Steps whose bytes a wave holds or waits for.
-template <int NQ>
-constexpr int kAhead = NQ == 1 ? 3 : 2;
 constexpr float kSlack = 8.0f;     // how far a score may pass the maximum in use, in powers of two
 constexpr int kFarRight = 0x7FFFFFFF;
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x6 __attribute__((ext_vector_type(6)));
+typedef uint32_t u32x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x32 __attribute__((ext_vector_type(32)));
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
@@ -199,15 +203,26 @@ struct Plan {
 };
 
 // ------------------------------------------------------------------- step --
+// Tokens of a step: as scores, lane group g has 8 g + 4 t + r (r = 0..3) of product t; as values, 16 t + 4 g + r. Halves of
+// 16 tokens lie in one page each.
 
-// The bytes of 32 tokens of a kv head, as loaded.
+// Where a step's halves are: rows of the cache's [pages, heads, page]; ok: they are there and some row sees a token.
+struct Place {
+    int64_t row[2];
+    bool ok[2];
+    int base;   // first token
+};
+
 template <int D>
-struct Stage {
-    u32x4 k[2];       // 16 bytes of token lane % 16 of each half
-    uint32_t ks[2];   // its scale byte
-    uint32_t v[8];    // D / 16 codes each of tokens 4 g + r and 16 + 4 g + r
-    uint32_t vs[2][D / 32];   // the scale bytes of these four tokens
-    bool ok[2];       // whether the half holds tokens (uniform)
+struct Keys {
+    u32x4 k[2];       // 32 channels of the token of row lane % 16 of product t
+    uint32_t ks[2];   // their scale byte
+};
+
+template <int D>
+struct Values {
+    uint32_t v[8];            // D / 16 channels of each token
+    uint32_t vs[2][D / 32];   // the tokens' scale bytes
 };
 
 // A wave's rows.
@@ -215,46 +230,49 @@ template <int NQ>
 struct Rows {
     i32x8 q[NQ][3];       // the parts of 32 channels of row lane % 16
     uint32_t qs[NQ];      // their scale bytes, one a part
-    int lo[NQ], hi[NQ];   // the tokens that the lane's row sees
+    int lo[NQ], hi[NQ];   // the tokens that row lane % 16 sees
     int lo_all, hi_all;   // the tokens that some row sees
     int lo_max, hi_min;   // the tokens that every row sees
 };
 
-// Sums of row lane % 16: 32 of its D channels, the weights' (four times the same number), the maximum in use and how far
-// above it a score may be: nothing at all before there is one.
+// o: channels D / 16 (lane % 16) + 2 b + c of rows 4 g + r; l: the weights' sums of these rows. Of row lane % 16: minus the
+// maximum in use (four times, as the scores' accumulator) and how far above it a score may be: nothing before there is one.
 template <int D, int NQ>
 struct Sums {
     f32x4 o[NQ][D / 16];
     f32x4 l[NQ];
-    float m[NQ], slack[NQ];
-    __device__ __forceinline__ float top(int i) const { return slack[i] < 0.0f ? -INFINITY : m[i]; }
+    f32x4 less[NQ];
+    float slack[NQ];
+    __device__ __forceinline__ float top(int i) const { return slack[i] < 0.0f ? -INFINITY : -less[i][0]; }
     __device__ __forceinline__ void clear() {
 #pragma unroll
         for (int i = 0; i < NQ; ++i) {
-            m[i] = 0.0f;
             slack[i] = -INFINITY;
-            l[i] = f32x4{0, 0, 0, 0};
+            l[i] = less[i] = f32x4{0, 0, 0, 0};
 #pragma unroll
             for (int j = 0; j < D / 16; ++j) o[i][j] = f32x4{0, 0, 0, 0};
         }
     }
 };
 
-// Lane constants of the loads.
+// Lane constants of the loads: byte offsets in a run of 16 tokens.
 template <int D>
 struct Lane {
     int n, g;
-    uint32_t k, ks, v, vs;   // byte offsets in a run of 16 tokens
-    uint32_t turn;           // rotation that brings the scale of the lane's channels to an exponent field
+    uint32_t k, ks, v, vs;
+    uint32_t turn;   // rotation that brings the scale of the lane's channels to an exponent field
+    int own;         // the block of its channels
     __device__ __forceinline__ explicit Lane(int lane) {
         n = lane % 16;
         g = lane / 16;
         const int block = D == 128 ? g : g & 1;
-        k = n * (D / 2) + block * 16;
-        ks = n * (D / 32) + block;
+        const int token = 8 * (n / 4 % 2) + n % 4;   // of product 0; 4 on in product 1
+        k = token * (D / 2) + block * 16;
+        ks = token * (D / 32) + block;
         v = 4 * g * (D / 2) + n * (D / 32);
         vs = 4 * g * (D / 32);
-        turn = 8 * (n * (D / 16) / 32) + 9;
+        own = n * (D / 16) / 32;
+        turn = 8 * own + 9;
     }
 };
 
@@ -270,34 +288,56 @@ __device__ __forceinline__ int pages_ahead(const Attention& a, const CacheView& 
     return -1;
 }
 
-// The bytes of a step, the `i`-th that `pages` holds; where there is none, those of the cache's first tokens.
-template <int D>
-__device__ __forceinline__ void load_step(Stage<D>& s, const CacheView& c, int pages, int i, int head, int base,
-                                          const Lane<D>& ln) {
+// The `i`-th step that `pages` holds; halves that are not there are read as the cache's first tokens.
+__device__ __forceinline__ Place place_of(const CacheView& c, int pages, int i, int head, int base) {
+    Place p;
+    p.base = base;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-        const int pg = __builtin_amdgcn_readlane(pages, 2 * i + t);
-        s.ok[t] = pg >= 0;
-        const int64_t row = s.ok[t] ? ((((int64_t)pg * c.heads + head) << c.page_bits) +
-                                       ((base + 16 * t) & ((1 << c.page_bits) - 1)))
-                                    : 0;
-        const uint8_t* kc = c.k_codes + row * (D / 2);
-        const uint8_t* kx = c.k_scales + row * (D / 32);
-        const uint8_t* vc = c.v_codes + row * (D / 2);
-        const uint8_t* vx = c.v_scales + row * (D / 32);
-        s.k[t] = *reinterpret_cast<const u32x4*>(kc + ln.k);
-        s.ks[t] = kx[ln.ks];
+        const int pg = from_lane(pages, 2 * i + t);
+        p.ok[t] = pg >= 0;
+        p.row[t] = p.ok[t] ? ((((int64_t)pg * c.heads + head) << c.page_bits) + ((base + 16 * t) & ((1 << c.page_bits) - 1)))
+                           : 0;
+    }
+    return p;
+}
+
+// A 32-bit offset that stays one at its load, whose address is then a scalar base and this.
+__device__ __forceinline__ uint32_t here(uint32_t offset) {
+    asm("" : "+v"(offset));
+    return offset;
+}
+
+template <int D>
+__device__ __forceinline__ void load_keys(Keys<D>& s, const CacheView& c, const Place& p, const Lane<D>& ln) {
+    const int64_t row = ln.n < 8 ? p.row[0] : p.row[1];
+    const uint8_t* k = c.k_codes + row * (D / 2) + ln.k;
+    const uint8_t* x = c.k_scales + row * (D / 32) + ln.ks;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        s.k[t] = *reinterpret_cast<const u32x4*>(k + t * 4 * (D / 2));
+        s.ks[t] = x[t * 4 * (D / 32)];
+    }
+}
+
+template <int D>
+__device__ __forceinline__ void load_values(Values<D>& s, const CacheView& c, const Place& p, const Lane<D>& ln) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const uint8_t* v = c.v_codes + p.row[t] * (D / 2);
+        const uint8_t* x = c.v_scales + p.row[t] * (D / 32);
+        const uint32_t at = here(ln.v);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            if constexpr (D == 128) s.v[4 * t + r] = *reinterpret_cast<const uint32_t*>(vc + ln.v + r * 64);
-            else s.v[4 * t + r] = *reinterpret_cast<const uint16_t*>(vc + ln.v + r * 32);
+            if constexpr (D == 128) s.v[4 * t + r] = *reinterpret_cast<const uint32_t*>(v + at + r * 64);
+            else s.v[4 * t + r] = *reinterpret_cast<const uint16_t*>(v + at + r * 32);
         }
         if constexpr (D == 128) {
-            const u32x4 w = *reinterpret_cast<const u32x4*>(vx + ln.vs);
+            const u32x4 w = *reinterpret_cast<const u32x4*>(x + here(ln.vs));
 #pragma unroll
             for (int r = 0; r < 4; ++r) s.vs[t][r] = w[r];
         } else {
-            const u32x2 w = *reinterpret_cast<const u32x2*>(vx + ln.vs);
+            const u32x2 w = *reinterpret_cast<const u32x2*>(x + here(ln.vs));
             s.vs[t][0] = w.x;
             s.vs[t][1] = w.y;
         }
@@ -312,7 +352,7 @@ __device__ __forceinline__ uint32_t scale_bytes(const uint32_t (&vs)[D / 32], in
 }
 
 template <int D>
-__device__ __forceinline__ void clear_token(Stage<D>& s, int t, int r, bool clear) {
+__device__ __forceinline__ void clear_token(Values<D>& s, int t, int r, bool clear) {
     s.v[4 * t + r] = clear ? 0u : s.v[4 * t + r];
     if constexpr (D == 128) s.vs[t][r] = clear ? 0u : s.vs[t][r];
     else s.vs[t][r / 2] &= clear ? (r % 2 ? 0x0000FFFFu : 0xFFFF0000u) : 0xFFFFFFFFu;
@@ -324,45 +364,15 @@ __device__ __forceinline__ uint32_t pack_weights(float a, float b) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
 }
 
-// Values with scale byte 255 in a step that not all rows see whole: NaN for the rows that see the token, in its block's
-// channels (which a lane group has to itself), and zeros for the product with the others' weights.
+// Scores of a step's tokens, less the maximum in use.
 template <int D, int NQ>
-__device__ void values_not_finite(Stage<D>& s, const Rows<NQ>& rows, Sums<D, NQ>& sums, int base, const Lane<D>& ln) {
-    const int block = ln.g * (D / 4) / 32, own = ln.n * (D / 16) / 32;
-    bool sees[NQ] = {};
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const uint32_t w = scale_bytes<D>(s.vs[t], r);
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const uint32_t there = (uint32_t)from_lane((int)w, 16 * g);   // of token j
-                const int j = base + 16 * t + 4 * g + r;
-#pragma unroll
-                for (int i = 0; i < NQ; ++i)
-                    sees[i] |= ((there >> (8 * block)) & 255u) == 255u && j >= rows.lo[i] && j < rows.hi[i];
-            }
-            clear_token<D>(s, t, r, ((w >> (8 * own)) & 255u) == 255u);
-        }
-#pragma unroll
-    for (int i = 0; i < NQ; ++i)
-#pragma unroll
-        for (int j = 0; j < D / 16; ++j) sums.o[i][j] += sees[i] ? __uint_as_float(0x7FC00000u) : 0.0f;
-}
-
-template <int D, int NQ>
-__device__ __forceinline__ void take_step(Stage<D>& s, const Rows<NQ>& rows, Sums<D, NQ>& sums, int base,
-                                          const Lane<D>& ln) {
-    constexpr int NJ = D / 16;
-    // scores of 2 x 16 tokens, less the maximum in use
-    f32x4 x[NQ][2];
+__device__ __forceinline__ void score(f32x4 (&x)[NQ][2], const Keys<D>& s, const Rows<NQ>& rows, const Sums<D, NQ>& sums) {
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
         const i32x8 k = {(int)s.k[t].x, (int)s.k[t].y, (int)s.k[t].z, (int)s.k[t].w, 0, 0, 0, 0};
 #pragma unroll
         for (int i = 0; i < NQ; ++i) {
-            f32x4 z = {-sums.m[i], -sums.m[i], -sums.m[i], -sums.m[i]};
+            f32x4 z = sums.less[i];
             z = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(k, rows.q[i][0], z, 4, 2, 0, s.ks[t], 0, rows.qs[i]);
             z = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(k, rows.q[i][1], z, 4, 2, 0, s.ks[t], 1, rows.qs[i]);
             if constexpr (D == 128)
@@ -370,23 +380,71 @@ __device__ __forceinline__ void take_step(Stage<D>& s, const Rows<NQ>& rows, Sum
             x[i][t] = z;
         }
     }
-    if (base < rows.lo_max || base + kStep > rows.hi_min || !(s.ok[0] && s.ok[1])) {   // not every row sees every token
-        const int j0 = base + 4 * ln.g;
+}
+
+// Bits [lo, hi) of 32.
+__device__ __forceinline__ uint32_t bits_between(int lo, int hi) {
+    const uint32_t upto = hi <= 0 ? 0u : hi >= 32 ? 0xFFFFFFFFu : (1u << hi) - 1;
+    const uint32_t under = lo <= 0 ? 0u : lo >= 32 ? 0xFFFFFFFFu : (1u << lo) - 1;
+    return upto & ~under;
+}
+
+// Values with scale byte 255 in a step that not all rows see whole: NaN for the rows that see the token, in its block's
+// channels, and zeros for the product with the others' weights.
+template <int D, int NQ>
+__device__ __forceinline__ void values_not_finite(Values<D>& s, const Rows<NQ>& rows, Sums<D, NQ>& sums, int base,
+                                                  const Lane<D>& ln) {
+    uint32_t bad = 0;   // bit 16 t + 4 g + r: that token, in the block of the lane's channels
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const uint32_t w = scale_bytes<D>(s.vs[t], r);
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const uint32_t there = (uint32_t)from_lane((int)w, 16 * g);
+                bad |= ((there >> (8 * ln.own)) & 255u) == 255u ? 1u << (16 * t + 4 * g + r) : 0u;
+            }
+            clear_token<D>(s, t, r, ((w >> (8 * ln.own)) & 255u) == 255u);
+        }
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+        f32x4 z;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int lo = __shfl(rows.lo[i], 4 * ln.g + e, kWave), hi = __shfl(rows.hi[i], 4 * ln.g + e, kWave);
+            z[e] = (bad & bits_between(lo - base, hi - base)) ? __uint_as_float(0x7FC00000u) : 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) sums.o[i][j] += z;
+    }
+}
+
+// Weights of a step's tokens, and their products with its values.
+template <int D, int NQ>
+__device__ __forceinline__ void take_step(const Keys<D>& keys, Values<D>& s, const Place& p, const Rows<NQ>& rows,
+                                          Sums<D, NQ>& sums, const Lane<D>& ln) {
+    constexpr int NJ = D / 16;
+    f32x4 x[NQ][2];
+    score<D, NQ>(x, keys, rows, sums);
+    if (p.base < rows.lo_max || p.base + kStep > rows.hi_min || !(p.ok[0] && p.ok[1])) {   // not every row sees every token
+        const bool there = ln.g < 2 ? p.ok[0] : p.ok[1];
         bool high = false;
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int j = j0 + 16 * t + r;
-                // values that no row sees stay finite whatever is there
-                clear_token<D>(s, t, r, !(s.ok[t] && j >= rows.lo_all && j < rows.hi_all));
+                const int j = p.base + 8 * ln.g + 4 * t + r;
 #pragma unroll
                 for (int i = 0; i < NQ; ++i)
-                    x[i][t][r] = s.ok[t] && j >= rows.lo[i] && j < rows.hi[i] ? x[i][t][r] : -INFINITY;
+                    x[i][t][r] = there && j >= rows.lo[i] && j < rows.hi[i] ? x[i][t][r] : -INFINITY;
+                // values that no row sees stay finite whatever is there
+                const int jv = p.base + 16 * t + 4 * ln.g + r;
+                clear_token<D>(s, t, r, !(p.ok[t] && jv >= rows.lo_all && jv < rows.hi_all));
                 const uint32_t w = scale_bytes<D>(s.vs[t], r);
                 high |= (w & (w << 1) & 0x80808080u) != 0;   // bytes from 192 on: rare enough to be looked at one by one
             }
-        if (__any(high)) values_not_finite<D, NQ>(s, rows, sums, base, ln);
+        if (__any(high)) values_not_finite<D, NQ>(s, rows, sums, p.base, ln);
     }
     // the maximum is left alone until a score is 2^8 above it
     bool past = false;
@@ -408,38 +466,40 @@ __device__ __forceinline__ void take_step(Stage<D>& s, const Rows<NQ>& rows, Sum
             const float by = v == -INFINITY ? 0.0f : none ? v : fmaxf(v, 0.0f);
             const float f = none ? 1.0f : exp2_raw(-by);
             if (v != -INFINITY) sums.slack[i] = kSlack;
-            sums.m[i] += by;
-            sums.l[i] *= f;
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) sums.o[i][j] *= f;
+            sums.less[i] -= by;
 #pragma unroll
             for (int t = 0; t < 2; ++t) x[i][t] -= by;
+            const f32x4 f4 = {__shfl(f, 4 * ln.g, kWave), __shfl(f, 4 * ln.g + 1, kWave), __shfl(f, 4 * ln.g + 2, kWave),
+                              __shfl(f, 4 * ln.g + 3, kWave)};   // of the rows that this lane has the sums of
+            sums.l[i] *= f4;
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) sums.o[i][j] *= f4;
         }
     }
-    // weights, and their sum by a product with ones
+    constexpr int kEven = (int)0x88888888u, kOdd = (int)0xDDDDDDDDu;   // places 0 and 2, 1 and 3 of every four
     const uint32_t one = 0x3F803F80u;
     const u32x4 ones = {one, one, one, one};
-    bf16x8 p[NQ];
+    bf16x8 w[NQ];
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
-        float w[8];
+        float e[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = exp2_raw(x[i][e / 4][e % 4]);
-        const u32x4 pk = {pack_weights(w[0], w[1]), pack_weights(w[2], w[3]), pack_weights(w[4], w[5]),
-                          pack_weights(w[6], w[7])};
-        p[i] = __builtin_bit_cast(bf16x8, pk);
-        sums.l[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, ones), p[i], sums.l[i], 0, 0, 0);
+        for (int k = 0; k < 8; ++k) e[k] = exp2_raw(x[i][k / 4][k % 4]);
+        const u32x4 pk = {pack_weights(e[0], e[1]), pack_weights(e[2], e[3]), pack_weights(e[4], e[5]),
+                          pack_weights(e[6], e[7])};
+        w[i] = __builtin_bit_cast(bf16x8, pk);
+        sums.l[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[i], __builtin_bit_cast(bf16x8, ones), sums.l[i], 0, 0, 0);
     }
     // values: a byte (two channels) of all eight tokens at a time
     float sc[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        const uint32_t w = D == 128 ? s.vs[e / 4][e % 4] : s.vs[e / 4][(e % 4) / 2];
-        sc[e] = __uint_as_float(__builtin_amdgcn_alignbit(w, w, D == 128 ? ln.turn : ln.turn + 16 * (e % 2)));
+        const uint32_t b = D == 128 ? s.vs[e / 4][e % 4] : s.vs[e / 4][(e % 4) / 2];
+        sc[e] = __uint_as_float(__builtin_amdgcn_alignbit(b, b, D == 128 ? ln.turn : ln.turn + 16 * (e % 2)));
     }
 #pragma unroll
     for (int b = 0; b < NJ / 2; ++b) {
-        uint32_t d[8];
+        u32x8 d;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             bf16x2 v;
@@ -449,18 +509,11 @@ __device__ __forceinline__ void take_step(Stage<D>& s, const Rows<NQ>& rows, Sum
             else v = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(s.v[e], sc[e], 3);
             d[e] = __builtin_bit_cast(uint32_t, v);
         }
-        u32x4 even, odd;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            even[e] = __builtin_amdgcn_perm(d[2 * e + 1], d[2 * e], 0x05040100u);
-            odd[e] = __builtin_amdgcn_perm(d[2 * e + 1], d[2 * e], 0x07060302u);
-        }
+        const bf16x16 both = __builtin_bit_cast(bf16x16, d);
 #pragma unroll
         for (int i = 0; i < NQ; ++i) {
-            sums.o[i][2 * b] =
-                __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, even), p[i], sums.o[i][2 * b], 0, 0, 0);
-            sums.o[i][2 * b + 1] =
-                __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, odd), p[i], sums.o[i][2 * b + 1], 0, 0, 0);
+            sums.o[i][2 * b] = __builtin_amdgcn_smfmac_f32_16x16x64_bf16(w[i], both, sums.o[i][2 * b], kEven, 0, 0);
+            sums.o[i][2 * b + 1] = __builtin_amdgcn_smfmac_f32_16x16x64_bf16(w[i], both, sums.o[i][2 * b + 1], kOdd, 0, 0);
         }
     }
 }
@@ -594,30 +647,36 @@ __device__ __forceinline__ void run_steps(const Attention& a, const CacheView& c
     const int lane = threadIdx.x % kWave;
     int pages = pages_ahead(a, c, table, at, stride, rows.lo_all, rows.hi_all, lane);
     int later = pages_ahead(a, c, table, at + 32 * stride, stride, rows.lo_all, rows.hi_all, lane);
-    int i = 0;       // place in `pages` of the step to load next
-    int ahead = at;  // and the step
-    Stage<D> st[kAhead<NQ>];
-    auto load = [&](Stage<D>& stage) {
-        load_step<D>(stage, c, pages, i, kv_head, ahead * kStep, ln);
+    int i = 0;       // place in `pages` of the step whose keys are loaded next
+    int ahead = at;  // and the step; past the end they are the cache's first tokens or a neighbour's, and not used
+    auto next_place = [&] {
+        const Place p = place_of(c, pages, i, kv_head, ahead * kStep);
         ahead += stride;
         if (++i == 32) {
             i = 0;
             pages = later;
             later = pages_ahead(a, c, table, ahead + 32 * stride, stride, rows.lo_all, rows.hi_all, lane);
         }
+        return p;
     };
-#pragma unroll
-    for (int b = 0; b + 1 < kAhead<NQ>; ++b) load(st[b]);
+    Keys<D> keys[2];
+    Values<D> values[2];
+    Place p0 = next_place(), p1;
+    load_keys<D>(keys[0], c, p0, ln);
+    load_values<D>(values[0], c, p0, ln);
 #pragma unroll
     for (int b = 0; b < NQ; ++b) split_query<D>(w[b], a.scale * kLog2e, ln.g, rows.q[b], rows.qs[b]);
     for (;;) {
-#pragma unroll
-        for (int b = 0; b < kAhead<NQ>; ++b) {
-            load(st[(b + kAhead<NQ> - 1) % kAhead<NQ>]);   // past the end too: then it is the cache's first tokens, or a neighbour's
-            take_step<D, NQ>(st[b], rows, sums, at * kStep, ln);
-            at += stride;
-            if (at >= end) return;
-        }
+        p1 = next_place();
+        load_keys<D>(keys[1], c, p1, ln);
+        load_values<D>(values[1], c, p1, ln);
+        take_step<D, NQ>(keys[0], values[0], p0, rows, sums, ln);
+        if ((at += stride) >= end) return;
+        p0 = next_place();
+        load_keys<D>(keys[0], c, p0, ln);
+        load_values<D>(values[0], c, p0, ln);
+        take_step<D, NQ>(keys[1], values[1], p1, rows, sums, ln);
+        if ((at += stride) >= end) return;
     }
 }
 
@@ -731,25 +790,25 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void attention_split_kernel(Atte
             for (int j = 0; j < NJ; ++j)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) lo_o[wave][r * NJ + j][lane] = sums.o[i][j][r];
-            if (lane < 16) {
-                lo_ml[wave][lane][0] = sums.top(i);
-                lo_ml[wave][lane][1] = sums.l[i][0];
-            }
-            __syncthreads();
-            float m = lo_ml[0][ln.n][0];
+            if (lane < 16) lo_ml[wave][lane][0] = sums.top(i);
+            if (ln.n == 0)
 #pragma unroll
-            for (int w = 1; w < kWaves; ++w) m = fmaxf(m, lo_ml[w][ln.n][0]);
+                for (int r = 0; r < 4; ++r) lo_ml[wave][4 * ln.g + r][1] = sums.l[i][r];
+            __syncthreads();
+            const int mine = 4 * ln.g + wave;   // this lane's row, its channels are NJ n + j
+            float m = lo_ml[0][mine][0];
+#pragma unroll
+            for (int w = 1; w < kWaves; ++w) m = fmaxf(m, lo_ml[w][mine][0]);
             const float m0 = finite_or_zero(m);
             float o[NJ] = {}, total = 0.0f;
 #pragma unroll
             for (int w = 0; w < kWaves; ++w) {
-                const float f = exp2_raw(lo_ml[w][ln.n][0] - m0);
-                total += f * lo_ml[w][ln.n][1];
+                const float f = exp2_raw(lo_ml[w][mine][0] - m0);
+                total += f * lo_ml[w][mine][1];
 #pragma unroll
                 for (int j = 0; j < NJ; ++j) o[j] += f * lo_o[w][wave * NJ + j][lane];
             }
-            const int at = 16 * i + ln.n;
-            const int d = NJ * (4 * ln.g + wave);   // this lane's channels of row `at`
+            const int at = 16 * i + mine, d = NJ * ln.n;
             if (at < rows_left) {
                 if (whole) {
                     const int row = row0 + at, q = (int)((uint32_t)row / (uint32_t)group);
@@ -762,7 +821,7 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void attention_split_kernel(Atte
 #pragma unroll
                     for (int j = 0; j < NJ; j += 4)
                         *reinterpret_cast<f32x4*>(part + (size_t)at * D + d + j) = f32x4{o[j], o[j + 1], o[j + 2], o[j + 3]};
-                    if (ln.g == 0 && wave == 0) {
+                    if (ln.n == 0) {
                         part[(size_t)kRows * D + 2 * at] = m;
                         part[(size_t)kRows * D + 2 * at + 1] = total;
                     }
@@ -859,22 +918,21 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void attention_rows_kernel(Atten
     Sums<D, NQ> sums;
     run_steps<D, NQ>(a, c, a.page_table + seq * a.table_width, s, head, group, row0, 0, kFarRight, 1, sums, ln);
 #pragma unroll
-    for (int i = 0; i < NQ; ++i) {
-        const int r = 16 * i + ln.n;
-        if (r < rows_left) {
-            const int row = row0 + r, q = (int)((uint32_t)row / (uint32_t)group);
-            const int h = head * group + (row - q * group);
-            const float f = last_factor(sums.top(i), sums.l[i][0], a.sinks, h);
-            uint16_t* out = a.out + ((int64_t)(s.first + q) * a.heads + h) * D;
+    for (int i = 0; i < NQ; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < 4; ++e) {
+            const int r = 16 * i + 4 * ln.g + e;
+            const float m = __shfl(sums.top(i), 4 * ln.g + e, kWave);
+            if (r < rows_left) {
+                const int row = row0 + r, q = (int)((uint32_t)row / (uint32_t)group);
+                const int h = head * group + (row - q * group);
+                const float f = last_factor(m, sums.l[i][e], a.sinks, h);
                 float o[NJ];
 #pragma unroll
                 for (int j = 0; j < NJ; ++j) o[j] = sums.o[i][j][e] * f;
-                store_out<NJ>(out + NJ * (4 * ln.g + e), o);
+                store_out<NJ>(a.out + ((int64_t)(s.first + q) * a.heads + h) * D + NJ * ln.n, o);
             }
         }
-    }
 }
 
 // Tiles of `rows` rows that the sequences of a call can have.
