@@ -48,7 +48,7 @@ namespace e2m1 {
 namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f;
-constexpr int kWaves = 4;          // of a workgroup
+constexpr int kRowWaves = 4;       // of a workgroup of attention_rows_kernel
 constexpr int kStep = 32;          // tokens a wave takes at a time
 constexpr float kSlack = 8.0f;     // how far a score may pass the maximum in use, in powers of two
 constexpr int kFarRight = 0x7FFFFFFF;
@@ -212,6 +212,11 @@ struct Place {
     bool ok[2];
 };
 
+struct Keys {
+    u32x4 k[2];   // 32 channels of the token of row lane % 16 of product t
+    int ks[2];    // their scale byte
+};
+
 template <int D>
 struct Values {
     uint32_t v[8];            // D / 16 channels of each token
@@ -260,7 +265,7 @@ struct Stage {
     static constexpr int kBytes = kScales + 256;
     static constexpr int kRequests = D == 128 ? 5 : 3;
 };
-constexpr int kStages = 4;
+constexpr int kStages = 4;   // of a wave's ring
 
 // Lane constants: places of a wave's reads in a stage, and where its requests read in a run of 16 tokens.
 template <int D>
@@ -373,6 +378,15 @@ __device__ __forceinline__ void request_step(const CacheView& c, const Place& p,
 }
 
 template <int D>
+__device__ __forceinline__ void read_keys(Keys& s, const uint8_t* stage, const Lane<D>& ln) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        s.k[t] = *reinterpret_cast<const u32x4*>(stage + ln.k + t * (D == 128 ? 512 : 256));
+        s.ks[t] = stage[ln.ks + t * (D / 8)];
+    }
+}
+
+template <int D>
 __device__ __forceinline__ void read_values(Values<D>& s, const uint8_t* stage, const Lane<D>& ln) {
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
@@ -415,13 +429,11 @@ __device__ __forceinline__ uint32_t pack_weights(float a, float b) {
 
 // Scores of a step's tokens, less the maximum in use.
 template <int D, int NQ>
-__device__ __forceinline__ void score(f32x4 (&x)[NQ][2], const uint8_t* stage, const Rows<NQ>& rows,
-                                      const Sums<D, NQ>& sums, const Lane<D>& ln) {
+__device__ __forceinline__ void score(f32x4 (&x)[NQ][2], const Keys& s, const Rows<NQ>& rows, const Sums<D, NQ>& sums) {
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-        const u32x4 w = *reinterpret_cast<const u32x4*>(stage + ln.k + t * (D == 128 ? 512 : 256));
-        const int ks = stage[ln.ks + t * (D / 8)];
-        const i32x8 k = {(int)w.x, (int)w.y, (int)w.z, (int)w.w, 0, 0, 0, 0};
+        const i32x8 k = {(int)s.k[t].x, (int)s.k[t].y, (int)s.k[t].z, (int)s.k[t].w, 0, 0, 0, 0};
+        const int ks = s.ks[t];
 #pragma unroll
         for (int i = 0; i < NQ; ++i) {
             f32x4 z = sums.less[i];
@@ -472,15 +484,15 @@ __device__ __forceinline__ void values_not_finite(Values<D>& s, const Rows<NQ>& 
     }
 }
 
-// Weights of a step's tokens, and their products with its values.
-template <int D, int NQ>
-__device__ __forceinline__ void take_step(const uint8_t* stage, int base, bool ok0, bool ok1, const Rows<NQ>& rows,
-                                          Sums<D, NQ>& sums, const Lane<D>& ln) {
+// Weights of a step's tokens, and their products with its values. next_keys: called when the keys' registers are free.
+template <int D, int NQ, typename F>
+__device__ __forceinline__ void take_step(const Keys& keys, const uint8_t* stage, int base, bool ok0, bool ok1,
+                                          const Rows<NQ>& rows, Sums<D, NQ>& sums, const Lane<D>& ln, F next_keys) {
     constexpr int NJ = D / 16;
-    f32x4 x[NQ][2];
-    score<D, NQ>(x, stage, rows, sums, ln);
     Values<D> s;
     read_values<D>(s, stage, ln);
+    f32x4 x[NQ][2];
+    score<D, NQ>(x, keys, rows, sums);
     if (base < rows.lo_max || base + kStep > rows.hi_min || !(ok0 && ok1)) {   // not every row sees every token
         const bool there = ln.g < 2 ? ok0 : ok1;
         bool high = false;
@@ -544,6 +556,7 @@ __device__ __forceinline__ void take_step(const uint8_t* stage, int base, bool o
         w[i] = __builtin_bit_cast(bf16x8, pk);
         sums.l[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[i], __builtin_bit_cast(bf16x8, ones), sums.l[i], 0, 0, 0);
     }
+    next_keys();
     // values: a byte (two channels) of all eight tokens at a time
     float sc[8];
 #pragma unroll
@@ -724,16 +737,21 @@ __device__ __forceinline__ void run_steps(const Attention& a, const CacheView& c
     __builtin_amdgcn_sched_barrier(0);   // no zeros in registers before this
     sums.clear();
     int stage = 0;
-    for (; at < end; at += stride) {
-        if (ahead < end) {
-            request(stage == 0 ? kStages - 1 : stage - 1);
-            wait_vm<Stage<D>::kRequests * (kStages - 1)>();
-        } else {
-            wait_vm<0>();
-        }
+    Keys keys;
+    auto wait_and_read = [&](int of) {   // the oldest step under way is there when all but those after it are
+        if (ahead < end) wait_vm<Stage<D>::kRequests * (kStages - 2)>();
+        else wait_vm<0>();
+        read_keys<D>(keys, ring + of * Stage<D>::kBytes, ln);
+    };
+    wait_and_read(0);
+    for (;;) {
+        const int next = stage == kStages - 1 ? 0 : stage + 1;
         const int ok = there >> (2 * stage);
-        take_step<D, NQ>(ring + stage * Stage<D>::kBytes, at * kStep, (ok & 1) != 0, (ok & 2) != 0, rows, sums, ln);
-        stage = stage == kStages - 1 ? 0 : stage + 1;
+        if (ahead < end) request(stage == 0 ? kStages - 1 : stage - 1);
+        take_step<D, NQ>(keys, ring + stage * Stage<D>::kBytes, at * kStep, (ok & 1) != 0, (ok & 2) != 0, rows, sums, ln,
+                         [&] { if (at + stride < end) wait_and_read(next); });
+        stage = next;
+        if ((at += stride) >= end) return;
     }
 }
 
@@ -759,7 +777,8 @@ __device__ __forceinline__ void store_out(uint16_t* p, const float (&v)[NJ]) {
 #pragma unroll
     for (int j = 0; j < NJ / 2; ++j) w[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
     if constexpr (NJ == 8) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-    else *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    else if constexpr (NJ == 4) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint32_t*>(p) = w[0];
 }
 
 // Where a segment (a tile of a sequence) was cut: its parts are the second one of worker `from` and the first ones of the
@@ -776,19 +795,19 @@ struct Record {
 template <int D, int NQ>
 constexpr size_t part_floats() { return (size_t)16 * NQ * (D + 2); }
 
-// Split form: workers take equal shares of all units (2^unit_bits tokens of a tile), in a row; the waves of one take every
-// fourth step of its share and join in LDS.
-template <int D, int NQ>
-__global__ __launch_bounds__(kWaves * kWave, 2) void attention_split_kernel(Attention a, CacheView c, float* parts,
-                                                                            Record* records, int workers,
-                                                                            int unit_bits, int record_count, bool by_segment) {
+// Split form: workers take equal shares of all units (2^unit_bits tokens of a tile), in a row. A worker is kW waves, which
+// take every kW-th step of its share and join in LDS. Without records every segment is one unit, and nothing is left to join.
+template <int D, int NQ, int kW>
+__global__ __launch_bounds__(kW * kWave, 2) void attention_split_kernel(Attention a, CacheView c, float* parts,
+                                                                        Record* records, int workers, int unit_bits,
+                                                                        int record_count, bool by_segment) {
     constexpr int NJ = D / 16;
     constexpr int kRows = 16 * NQ;
     // each wave's ring; between segments the waves' sums
-    __shared__ __attribute__((aligned(16))) uint8_t ring[kWaves][kStages * Stage<D>::kBytes];
-    static_assert(sizeof(ring) >= sizeof(float) * kWaves * (4 * NJ * kWave + 32), "the sums fit the rings");
+    __shared__ __attribute__((aligned(16))) uint8_t ring[kW][kStages * Stage<D>::kBytes];
+    static_assert(kW == 1 || sizeof(ring) >= sizeof(float) * kW * (4 * NJ * kWave + 32), "the sums fit the rings");
     float(*lo_o)[4 * NJ][kWave] = reinterpret_cast<float(*)[4 * NJ][kWave]>(&ring[0][0]);
-    float(*lo_ml)[16][2] = reinterpret_cast<float(*)[16][2]>(&ring[0][0] + sizeof(float) * kWaves * 4 * NJ * kWave);
+    float(*lo_ml)[16][2] = reinterpret_cast<float(*)[16][2]>(&ring[0][0] + sizeof(float) * kW * 4 * NJ * kWave);
     const int lane = threadIdx.x % kWave, wave = uniform(threadIdx.x / kWave);
     // neighbours in the order of work on the same XCD, whose L2 then holds what they share
     const int per_xcd = workers / 8;
@@ -814,7 +833,7 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void attention_split_kernel(Atte
         segs_before = plan.sum_before(seq, segments, all);
         if (threadIdx.x == 0 && id < record_count && (uint32_t)id >= all) records[id].from = records[id].to = 0;
     } else if (idle) {
-        if (threadIdx.x == 0) records[id].from = records[id].to = 0;
+        if (threadIdx.x == 0 && id < record_count) records[id].from = records[id].to = 0;
     }
     if (idle) return;
     Span s = plan.span(seq);
@@ -837,58 +856,73 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void attention_split_kernel(Atte
         const int row0 = (int)(segment - head * tiles) * kRows;
         const int origin = first_seen(a, s, 0) / kStep, steps = unit_bits - 5;
         Sums<D, NQ> sums;
-        run_steps<D, NQ>(a, c, a.page_table + seq * a.table_width, s, head, group, row0, origin + (u0 << steps) + wave,
-                         origin + (u1 << steps), kWaves, sums, ring[wave], ln);
+        run_steps<D, NQ>(a, c, a.page_table + seq * a.table_width, s, head, group, row0,
+                         origin + (u0 << steps) + wave, origin + (u1 << steps), kW, sums, ring[wave], ln);
         const bool whole = u0 == 0 && u1 == (int)units;
         float* part = parts + (2 * (size_t)id + (u0 > 0 ? 0 : 1)) * part_floats<D, NQ>();
         const int rows_left = s.n * group - row0;
+        // sums of row `at`, channels d on
+        auto put = [&](auto& o, int at, int d, float m, float total) {
+            constexpr int kN = sizeof(o) / sizeof(float);
+            if (at >= rows_left) return;
+            if (whole) {
+                const int row = row0 + at, q = (int)((uint32_t)row / (uint32_t)group);
+                const int h = head * group + (row - q * group);
+                const float f = last_factor(m, total, a.sinks, h);
+#pragma unroll
+                for (int j = 0; j < kN; ++j) o[j] *= f;
+                store_out<kN>(a.out + ((int64_t)(s.first + q) * a.heads + h) * D + d, o);
+            } else {
+#pragma unroll
+                for (int j = 0; j < kN; ++j) part[(size_t)at * D + d + j] = o[j];
+                if (d == 0) {
+                    part[(size_t)kRows * D + 2 * at] = m;
+                    part[(size_t)kRows * D + 2 * at + 1] = total;
+                }
+            }
+        };
 #pragma unroll
         for (int i = 0; i < NQ; ++i) {
             if (16 * i >= rows_left) break;
-            __syncthreads();
+            if constexpr (kW == 1) {
 #pragma unroll
-            for (int j = 0; j < NJ; ++j)
+                for (int e = 0; e < 4; ++e) {
+                    const float m = __shfl(sums.top(i), 4 * ln.g + e, kWave);
+                    float o[NJ];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) lo_o[wave][r * NJ + j][lane] = sums.o[i][j][r];
-            if (lane < 16) lo_ml[wave][lane][0] = sums.top(i);
-            if (ln.n == 0)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) lo_ml[wave][4 * ln.g + r][1] = sums.l[i][r];
-            __syncthreads();
-            const int mine = 4 * ln.g + wave;   // this lane's row, its channels are NJ n + j
-            float m = lo_ml[0][mine][0];
-#pragma unroll
-            for (int w = 1; w < kWaves; ++w) m = fmaxf(m, lo_ml[w][mine][0]);
-            const float m0 = finite_or_zero(m);
-            float o[NJ] = {}, total = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kWaves; ++w) {
-                const float f = exp2_raw(lo_ml[w][mine][0] - m0);
-                total += f * lo_ml[w][mine][1];
-#pragma unroll
-                for (int j = 0; j < NJ; ++j) o[j] += f * lo_o[w][wave * NJ + j][lane];
-            }
-            const int at = 16 * i + mine, d = NJ * ln.n;
-            if (at < rows_left) {
-                if (whole) {
-                    const int row = row0 + at, q = (int)((uint32_t)row / (uint32_t)group);
-                    const int h = head * group + (row - q * group);
-                    const float f = last_factor(m, total, a.sinks, h);
-#pragma unroll
-                    for (int j = 0; j < NJ; ++j) o[j] *= f;
-                    store_out<NJ>(a.out + ((int64_t)(s.first + q) * a.heads + h) * D + d, o);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < NJ; j += 4)
-                        *reinterpret_cast<f32x4*>(part + (size_t)at * D + d + j) = f32x4{o[j], o[j + 1], o[j + 2], o[j + 3]};
-                    if (ln.n == 0) {
-                        part[(size_t)kRows * D + 2 * at] = m;
-                        part[(size_t)kRows * D + 2 * at + 1] = total;
-                    }
+                    for (int j = 0; j < NJ; ++j) o[j] = sums.o[i][j][e];
+                    put(o, 16 * i + 4 * ln.g + e, NJ * ln.n, m, sums.l[i][e]);
                 }
+            } else {
+                __syncthreads();
+#pragma unroll
+                for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) lo_o[wave][r * NJ + j][lane] = sums.o[i][j][r];
+                if (lane < 16) lo_ml[wave][lane][0] = sums.top(i);
+                if (ln.n == 0)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) lo_ml[wave][4 * ln.g + r][1] = sums.l[i][r];
+                __syncthreads();
+                // wave w joins row 4 g + w % 4, its channels in kW / 4 runs
+                constexpr int kN = NJ * 4 / kW;
+                const int mine = 4 * ln.g + wave % 4, j0 = wave / 4 * kN;
+                float m = lo_ml[0][mine][0];
+#pragma unroll
+                for (int w = 1; w < kW; ++w) m = fmaxf(m, lo_ml[w][mine][0]);
+                const float m0 = finite_or_zero(m);
+                float o[kN] = {}, total = 0.0f;
+#pragma unroll
+                for (int w = 0; w < kW; ++w) {
+                    const float f = exp2_raw(lo_ml[w][mine][0] - m0);
+                    total += f * lo_ml[w][mine][1];
+#pragma unroll
+                    for (int j = 0; j < kN; ++j) o[j] += f * lo_o[w][wave % 4 * NJ + j0 + j][lane];
+                }
+                put(o, 16 * i + mine, NJ * ln.n + j0, m, total);
             }
         }
-        __syncthreads();   // the rings are free again
+        if constexpr (kW > 1) __syncthreads();   // the rings are free again
         if (u1 == (int)units) {   // the segment ends here
             Record r = {row0, s.first, 0, 0, min(kRows, rows_left), head, {0, 0}};
             if (u0 > 0) {
@@ -901,12 +935,14 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void attention_split_kernel(Atte
         }
         u = seg_begin + u1;
     }
-    if (!by_segment && threadIdx.x == 0) records[id] = cut;
+    if (!by_segment && threadIdx.x == 0 && id < record_count) records[id] = cut;
 }
+
+constexpr int kJoinWaves = 4;
 
 // Joins the parts of a segment, a wave a row: two parts at a time, half a wave each, sixteen of them on their way.
 template <int D, int NQ>
-__global__ __launch_bounds__(kWaves * kWave) void attention_join_kernel(Attention a, CacheView c, const float* parts,
+__global__ __launch_bounds__(kJoinWaves * kWave) void attention_join_kernel(Attention a, CacheView c, const float* parts,
                                                                         const Record* records) {
     constexpr int kRows = 16 * NQ;
     constexpr int kEach = D / 32;
@@ -915,7 +951,7 @@ __global__ __launch_bounds__(kWaves * kWave) void attention_join_kernel(Attentio
     const int lane = threadIdx.x % kWave, half = lane / 32, place = lane % 32;
     const int count = r.to - r.from + 1;
     const int group = a.heads / c.heads;
-    for (int at = blockIdx.y * kWaves + threadIdx.x / kWave; at < r.rows; at += gridDim.y * kWaves) {
+    for (int at = blockIdx.y * kJoinWaves + threadIdx.x / kWave; at < r.rows; at += gridDim.y * kJoinWaves) {
         auto part_of = [&](int i) { return parts + (2 * (size_t)(r.from + i) + (i == 0 ? 1 : 0)) * part_floats<D, NQ>(); };
         float m = -INFINITY;
         for (int i = lane; i < count; i += kWave) m = fmaxf(m, part_of(i)[(size_t)kRows * D + 2 * at]);
@@ -959,22 +995,26 @@ __global__ __launch_bounds__(kWaves * kWave) void attention_join_kernel(Attentio
 
 // Many rows: a wave has a tile of its own and goes through all that it sees; the tiles with the most tokens first.
 template <int D, int NQ>
-__global__ __launch_bounds__(kWaves * kWave, 2) void attention_rows_kernel(Attention a, CacheView c) {
+__global__ __launch_bounds__(kRowWaves * kWave, 2) void attention_rows_kernel(Attention a, CacheView c, int round) {
     constexpr int NJ = D / 16;
     constexpr int kRows = 16 * NQ;
-    __shared__ __attribute__((aligned(16))) uint8_t ring[kWaves][kStages * Stage<D>::kBytes];
+    __shared__ __attribute__((aligned(16))) uint8_t ring[kRowWaves][kStages * Stage<D>::kBytes];
     const int lane = threadIdx.x % kWave, wave = uniform(threadIdx.x / kWave);
     const int group = a.heads / c.heads;
     const Lane<D> ln(c, lane);
-    auto weight = [&](const Span& s) { return tiles_of(s, group, kRows * kWaves); };
+    auto weight = [&](const Span& s) { return tiles_of(s, group, kRows * kRowWaves); };
     const Plan plan(a, c.page_bits, lane, weight);
-    const int at = (int)plan.total - 1 - (int)(blockIdx.x / (uint32_t)c.heads);
+    // rounds of `round` tile groups, one a compute unit and head: every other one backwards, so that a unit that had the
+    // longest of one round gets the shortest of the next
+    int turn = (int)(blockIdx.x / (uint32_t)c.heads);
+    if (const int k = turn / round; k % 2 == 1) turn = k * round + (round - 1 - (turn - k * round));
+    const int at = (int)plan.total - 1 - turn;
     if (at < 0 || !plan.ok) return;
     const int head = (int)(blockIdx.x % (uint32_t)c.heads);
     uint32_t begin;
     const int seq = plan.find((uint32_t)at, begin, weight);
     const Span s = plan.span(seq);
-    const int row0 = ((at - (int)begin) * kWaves + wave) * kRows;
+    const int row0 = ((at - (int)begin) * kRowWaves + wave) * kRows;
     const int rows_left = s.n * group - row0;
     if (rows_left <= 0) return;
     Sums<D, NQ> sums;
@@ -1002,55 +1042,89 @@ int64_t most_tiles(int64_t tokens, int64_t seqs, int64_t group, int64_t rows) {
     return tokens * group / rows + (seqs < tokens ? seqs : tokens);
 }
 
+// How a call is worked on, from what the host knows: numbers of rows and sequences, and how many tokens a row can see.
+enum Kind { kRowsForm, kWholeForm, kSplitForm };
 struct Form {
-    bool split;
-    int nq;
+    Kind kind;
+    int nq;              // tiles of 16 rows a wave takes
+    int waves;           // of a worker
     int workers;
-    int64_t segments;   // at most
-    int join_rows;      // workgroups a segment's rows are joined by
-    int records() const { return (int)(segments < workers ? segments : workers); }
+    int64_t segments;    // at most
+    int join_rows;       // workgroups a segment's rows are joined by
+    int records() const { return kind == kSplitForm ? (int)(segments < workers ? segments : workers) : 0; }
 };
 
-// Which form a call takes, from what the host knows: rows a sequence on the average, tiles in all.
-Form form_of(int64_t tokens, int64_t seqs, int64_t heads, int64_t kv_heads) {
+Form split_of(int64_t tokens, int64_t seqs, int64_t heads, int64_t kv_heads, int64_t mean) {
     const int64_t group = heads / kv_heads, cus = device_cu_count();
-    const int64_t mean = (tokens + seqs - 1) / seqs * group;
-    const int64_t wide = most_tiles(tokens, seqs, group, 32 * kWaves) * kv_heads;
-    if (mean > 64 && wide >= cus) return {false, 2, 0, 0, 0};
     const int nq = mean > 16 ? 2 : 1;
-    return {true, nq, (int)(2 * cus), most_tiles(tokens, seqs, group, 16 * nq) * kv_heads,
-            (int)(((mean < 16 * nq ? mean : 16 * nq) + kWaves - 1) / kWaves)};
+    const int64_t segments = most_tiles(tokens, seqs, group, 16 * nq) * kv_heads;
+    const int waves = segments >= cus / 2 ? 1 : 4;
+    return {kSplitForm, nq, waves, (int)(8 / waves * cus), segments,
+            (int)(((mean < 16 * nq ? mean : 16 * nq) + kJoinWaves - 1) / kJoinWaves)};
+}
+
+Form form_of(int64_t tokens, int64_t seqs, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t length) {
+    const int64_t group = heads / kv_heads, cus = device_cu_count();
+    const int64_t queries = (tokens + seqs - 1) / seqs, mean = queries * group;
+    const int wide = head_dim == 128 ? 2 : 3;
+    if (mean > 64) {
+        if (most_tiles(tokens, seqs, group, 16 * wide * kRowWaves) * kv_heads >= 2 * cus) return {kRowsForm, wide, 0, 0, 0, 0};
+        if (most_tiles(tokens, seqs, group, 16 * kRowWaves) * kv_heads >= cus / 8 && length <= 4 * queries)
+            return {kRowsForm, 1, 0, 0, 0, 0};
+    }
+    Form f = split_of(tokens, seqs, heads, kv_heads, mean);
+    if (length <= 1024 && f.segments <= 2 * cus) {
+        f.kind = kWholeForm;
+        f.waves = f.segments <= cus ? 8 : 4;
+        f.workers = (int)(f.segments < 1 << 20 ? f.segments : 1 << 20);
+    }
+    return f;
+}
+
+template <int D, int NQ, int kW>
+hipError_t split_form(const Attention& a, const CacheView& c, const Form& f, void* workspace, hipStream_t stream) {
+    Record* records = f.kind == kSplitForm ? static_cast<Record*>(workspace) : nullptr;
+    float* parts = reinterpret_cast<float*>(records + f.records());
+    int unit_bits = f.kind == kSplitForm ? 7 : 30;   // four steps, more where the number of units would not fit 32 bits
+    while (f.segments > ((int64_t)1 << 30) / (((a.table_width << c.page_bits) >> unit_bits) + 2)) ++unit_bits;
+    attention_split_kernel<D, NQ, kW><<<f.workers, kW * kWave, 0, stream>>>(a, c, parts, records, f.workers, unit_bits,
+                                                                            f.records(),
+                                                                            records && f.segments <= f.workers);
+    if (hipError_t e = hipGetLastError(); e != hipSuccess || !records) return e;
+    attention_join_kernel<D, NQ><<<dim3(f.records(), f.join_rows), kJoinWaves * kWave, 0, stream>>>(a, c, parts, records);
+    return hipGetLastError();
 }
 
 template <int D, int NQ>
-hipError_t split_form(const Attention& a, const CacheView& c, const Form& f, void* workspace, hipStream_t stream) {
-    Record* records = static_cast<Record*>(workspace);
-    float* parts = reinterpret_cast<float*>(records + f.records());
-    int unit_bits = 7;   // four steps, more where the number of units would not fit 32 bits
-    while (f.segments > ((int64_t)1 << 30) / (((a.table_width << c.page_bits) >> unit_bits) + 2)) ++unit_bits;
-    attention_split_kernel<D, NQ><<<f.workers, kWaves * kWave, 0, stream>>>(a, c, parts, records, f.workers, unit_bits, f.records(),
-                                                                            f.segments <= f.workers);
-    if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-    attention_join_kernel<D, NQ><<<dim3(f.records(), f.join_rows), kWaves * kWave, 0, stream>>>(a, c, parts, records);
+hipError_t split_waves(const Attention& a, const CacheView& c, const Form& f, void* workspace, hipStream_t stream) {
+    if (f.waves == 1) return split_form<D, NQ, 1>(a, c, f, workspace, stream);
+    if (f.waves == 4) return split_form<D, NQ, 4>(a, c, f, workspace, stream);
+    return split_form<D, NQ, 8>(a, c, f, workspace, stream);
+}
+
+template <int D, int NQ>
+hipError_t rows_form(const Attention& a, const CacheView& c, hipStream_t stream) {
+    const int round = device_cu_count() > c.heads ? device_cu_count() / c.heads : 1;
+    const int64_t tiles = most_tiles(a.tokens, a.seqs, a.heads / c.heads, 16 * NQ * kRowWaves);
+    const int64_t grid = (tiles + round - 1) / round * round * c.heads;   // whole rounds: see the kernel's order
+    attention_rows_kernel<D, NQ><<<(unsigned)grid, kRowWaves * kWave, 0, stream>>>(a, c, round);
     return hipGetLastError();
 }
 
 template <int D>
 hipError_t attend(const Attention& a, const CacheView& c, void* workspace, hipStream_t stream) {
-    const Form f = form_of(a.tokens, a.seqs, a.heads, c.heads);
-    if (!f.split) {
-        const int64_t grid = most_tiles(a.tokens, a.seqs, a.heads / c.heads, 32 * kWaves) * c.heads;
-        attention_rows_kernel<D, 2><<<(unsigned)grid, kWaves * kWave, 0, stream>>>(a, c);
-        return hipGetLastError();
-    }
-    return f.nq == 2 ? split_form<D, 2>(a, c, f, workspace, stream) : split_form<D, 1>(a, c, f, workspace, stream);
+    const int64_t most = a.table_width << c.page_bits, seen = a.window + (a.tokens + a.seqs - 1) / a.seqs;
+    const Form f = form_of(a.tokens, a.seqs, a.heads, c.heads, D, a.window > 0 && seen < most ? seen : most);
+    if (f.kind == kRowsForm)
+        return f.nq == 1 ? rows_form<D, 1>(a, c, stream) : rows_form<D, (D == 128 ? 2 : 3)>(a, c, stream);
+    return f.nq == 2 ? split_waves<D, 2>(a, c, f, workspace, stream) : split_waves<D, 1>(a, c, f, workspace, stream);
 }
 
 }  // namespace
 
 size_t attention_workspace_bytes(int64_t tokens, int64_t seqs, int64_t heads, int64_t kv_heads, int64_t head_dim) {
-    const Form f = form_of(tokens, seqs, heads, kv_heads);
-    if (!f.split) return 0;
+    const Form f = form_of(tokens, seqs, heads, kv_heads, head_dim, (int64_t)1 << 30);
+    if (f.kind != kSplitForm) return 0;
     return f.records() * sizeof(Record) + (size_t)f.workers * 2 * 16 * f.nq * (head_dim + 2) * sizeof(float);
 }
 
