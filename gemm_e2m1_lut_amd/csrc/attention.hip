@@ -210,11 +210,13 @@ struct Plan {
 struct Place {
     int64_t row[2];
     bool ok[2];
+    int base;   // first token
 };
 
+template <int D>
 struct Keys {
-    u32x4 k[2];   // 32 channels of the token of row lane % 16 of product t
-    int ks[2];    // their scale byte
+    u32x4 k[2];       // 32 channels of the token of row lane % 16 of product t
+    uint32_t ks[2];   // their scale byte
 };
 
 template <int D>
@@ -253,61 +255,24 @@ struct Sums {
     }
 };
 
-// A stage of a wave's ring in LDS: the bytes of one step, 16-byte pieces (and scale words) in the order in which the lanes
-// read them, so that no two lanes of a read meet in a bank. Each request writes its lanes' pieces one after another; the
-// order comes from where each lane reads.
-template <int D>
-struct Stage {
-    static constexpr int kKeys = 0;
-    static constexpr int kUpper = D == 128 ? 1152 : 512;   // the second half's keys, half the banks on (128 channels)
-    static constexpr int kValues = D == 128 ? 2176 : 1024;
-    static constexpr int kScales = D == 128 ? 4224 : 2048;
-    static constexpr int kBytes = kScales + 256;
-    static constexpr int kRequests = D == 128 ? 5 : 3;
-};
-constexpr int kStages = 4;   // of a wave's ring
-
-// Lane constants: places of a wave's reads in a stage, and where its requests read in a run of 16 tokens.
+// Lane constants of the loads: byte offsets in a run of 16 tokens.
 template <int D>
 struct Lane {
     int lane, n, g;
     uint32_t k, ks, v, vs;
-    uint32_t from_k, from_v;              // byte offsets
-    const uint8_t *at_k, *at_v, *at_s;    // pointers, where a request's lanes read from two halves or arrays
-    bool upper_kv, upper_s;               // this lane's half in such a request
     uint32_t turn;   // rotation that brings the scale of the lane's channels to an exponent field
     int own;         // the block of its channels
-    __device__ __forceinline__ Lane(const CacheView& c, int lane_) : lane(lane_) {
+    __device__ __forceinline__ Lane(const CacheView&, int lane_) : lane(lane_) {
         n = lane % 16;
         g = lane / 16;
+        const int block = D == 128 ? g : g & 1;
+        const int token = 8 * (n / 4 % 2) + n % 4;   // of product 0; 4 on in product 1
+        k = token * (D / 2) + block * 16;
+        ks = token * (D / 32) + block;
+        v = 4 * g * (D / 2) + n * (D / 32);
+        vs = 4 * g * (D / 32);
         own = n * (D / 16) / 32;
         turn = 8 * own + 9;
-        const int token = 8 * (n / 4) + n % 4;   // of product 0; 4 on in product 1
-        if constexpr (D == 128) {
-            k = (n < 8 ? 0 : Stage<D>::kUpper) + g * 128 + (n % 8) * 16;
-            ks = Stage<D>::kScales + token * 4 + g;
-            v = Stage<D>::kValues + lane * 4;
-            vs = Stage<D>::kScales + 128 + g * 16;
-            // keys: product, block, row of the product; values: token % 4, token / 4, piece
-            from_k = (8 * (lane % 8 / 4) + 4 * (lane / 32) + lane % 4) * 64 + (lane / 8 % 4) * 16;
-            from_v = (4 * (lane / 4 % 4) + lane / 16) * 64 + (lane % 4) * 16;
-            at_k = at_v = nullptr;
-            at_s = (lane < 32 ? c.k_scales : c.v_scales) + (lane % 16) * 4;
-            upper_kv = false;
-            upper_s = lane % 32 >= 16;
-        } else {
-            k = (n < 8 ? 0 : Stage<D>::kUpper) + (g % 2) * 128 + (n % 8) * 16;
-            ks = Stage<D>::kScales + token * 2 + g % 2;
-            v = Stage<D>::kValues + lane * 2;
-            vs = Stage<D>::kScales + 64 + g * 8;
-            from_k = from_v = 0;
-            const int s = lane % 32;
-            at_k = c.k_codes + (8 * (s % 8 / 4) + 4 * (s / 16) + s % 4) * 32 + (s / 8 % 2) * 16;
-            at_v = c.v_codes + (4 * (s / 2 % 4) + s / 8) * 32 + (s % 2) * 16;
-            at_s = (s < 16 ? c.k_scales : c.v_scales) + (s % 8) * 4;
-            upper_kv = lane >= 32;
-            upper_s = s % 16 >= 8;
-        }
     }
 };
 
@@ -326,6 +291,7 @@ __device__ __forceinline__ int pages_ahead(const Attention& a, const CacheView& 
 // The `i`-th step that `pages` holds; halves that are not there are read as the cache's first tokens.
 __device__ __forceinline__ Place place_of(const CacheView& c, int pages, int i, int head, int base) {
     Place p;
+    p.base = base;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
         const int pg = from_lane(pages, 2 * i + t);
@@ -336,71 +302,42 @@ __device__ __forceinline__ Place place_of(const CacheView& c, int pages, int i, 
     return p;
 }
 
-// The lane's 16 (or 4) bytes -> LDS lds + 16 (4) * lane. The compiler does not see these loads: a wave waits for its own
-// with s_waitcnt vmcnt; loads that the compiler sees in between make such a wait longer, never shorter. M0 is set here and used by
-// nothing else in these kernels.
-__device__ __forceinline__ void request16(const uint8_t* base, uint32_t offset, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" :: "s"(lds), "v"(offset), "s"(base) : "memory");
-}
-
-__device__ __forceinline__ void request16(const uint8_t* p, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" :: "s"(lds), "v"(p) : "memory");
-}
-
-__device__ __forceinline__ void request4(const uint8_t* p, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" :: "s"(lds), "v"(p) : "memory");
-}
-
-// At most kN of this wave's requests are in flight.
-template <int kN>
-__device__ __forceinline__ void wait_vm() {
-    asm volatile("s_waitcnt vmcnt(%0)" :: "n"(kN) : "memory");
-}
-
-// This wave's LDS accesses are done.
-__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
-
-// Requests a step's bytes into the stage at LDS address `lds`, which the wave has read to the end.
-template <int D>
-__device__ __forceinline__ void request_step(const CacheView& c, const Place& p, uint32_t lds, const Lane<D>& ln) {
-    wait_lds();
-    if constexpr (D == 128) {
-        request16(c.k_codes + p.row[0] * 64, ln.from_k, lds + Stage<D>::kKeys);
-        request16(c.k_codes + p.row[1] * 64, ln.from_k, lds + Stage<D>::kUpper);
-        request16(c.v_codes + p.row[0] * 64, ln.from_v, lds + Stage<D>::kValues);
-        request16(c.v_codes + p.row[1] * 64, ln.from_v, lds + Stage<D>::kValues + 1024);
-    } else {
-        const int64_t row = ln.upper_kv ? p.row[1] : p.row[0];
-        request16(ln.at_k + row * 32, lds + Stage<D>::kKeys);
-        request16(ln.at_v + row * 32, lds + Stage<D>::kValues);
-    }
-    request4(ln.at_s + (ln.upper_s ? p.row[1] : p.row[0]) * (D / 32), lds + Stage<D>::kScales);
+// A 32-bit offset that stays one at its load, whose address is then a scalar base and this.
+__device__ __forceinline__ uint32_t here(uint32_t offset) {
+    asm("" : "+v"(offset));
+    return offset;
 }
 
 template <int D>
-__device__ __forceinline__ void read_keys(Keys& s, const uint8_t* stage, const Lane<D>& ln) {
+__device__ __forceinline__ void load_keys(Keys<D>& s, const CacheView& c, const Place& p, const Lane<D>& ln) {
+    const int64_t row = ln.n < 8 ? p.row[0] : p.row[1];
+    const uint8_t* k = c.k_codes + row * (D / 2) + ln.k;
+    const uint8_t* x = c.k_scales + row * (D / 32) + ln.ks;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-        s.k[t] = *reinterpret_cast<const u32x4*>(stage + ln.k + t * (D == 128 ? 512 : 256));
-        s.ks[t] = stage[ln.ks + t * (D / 8)];
+        s.k[t] = *reinterpret_cast<const u32x4*>(k + t * 4 * (D / 2));
+        s.ks[t] = x[t * 4 * (D / 32)];
     }
 }
 
 template <int D>
-__device__ __forceinline__ void read_values(Values<D>& s, const uint8_t* stage, const Lane<D>& ln) {
+__device__ __forceinline__ void load_values(Values<D>& s, const CacheView& c, const Place& p, const Lane<D>& ln) {
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
+        const uint8_t* v = c.v_codes + p.row[t] * (D / 2);
+        const uint8_t* x = c.v_scales + p.row[t] * (D / 32);
+        const uint32_t at = here(ln.v);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            if constexpr (D == 128) s.v[4 * t + r] = *reinterpret_cast<const uint32_t*>(stage + ln.v + t * 1024 + r * 256);
-            else s.v[4 * t + r] = *reinterpret_cast<const uint16_t*>(stage + ln.v + t * 512 + r * 128);
+            if constexpr (D == 128) s.v[4 * t + r] = *reinterpret_cast<const uint32_t*>(v + at + r * 64);
+            else s.v[4 * t + r] = *reinterpret_cast<const uint16_t*>(v + at + r * 32);
         }
         if constexpr (D == 128) {
-            const u32x4 w = *reinterpret_cast<const u32x4*>(stage + ln.vs + t * 64);
+            const u32x4 w = *reinterpret_cast<const u32x4*>(x + here(ln.vs));
 #pragma unroll
             for (int r = 0; r < 4; ++r) s.vs[t][r] = w[r];
         } else {
-            const u32x2 w = *reinterpret_cast<const u32x2*>(stage + ln.vs + t * 32);
+            const u32x2 w = *reinterpret_cast<const u32x2*>(x + here(ln.vs));
             s.vs[t][0] = w.x;
             s.vs[t][1] = w.y;
         }
@@ -429,18 +366,17 @@ __device__ __forceinline__ uint32_t pack_weights(float a, float b) {
 
 // Scores of a step's tokens, less the maximum in use.
 template <int D, int NQ>
-__device__ __forceinline__ void score(f32x4 (&x)[NQ][2], const Keys& s, const Rows<NQ>& rows, const Sums<D, NQ>& sums) {
+__device__ __forceinline__ void score(f32x4 (&x)[NQ][2], const Keys<D>& s, const Rows<NQ>& rows, const Sums<D, NQ>& sums) {
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
         const i32x8 k = {(int)s.k[t].x, (int)s.k[t].y, (int)s.k[t].z, (int)s.k[t].w, 0, 0, 0, 0};
-        const int ks = s.ks[t];
 #pragma unroll
         for (int i = 0; i < NQ; ++i) {
             f32x4 z = sums.less[i];
-            z = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(k, rows.q[i][0], z, 4, 2, 0, ks, 0, rows.qs[i]);
-            z = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(k, rows.q[i][1], z, 4, 2, 0, ks, 1, rows.qs[i]);
+            z = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(k, rows.q[i][0], z, 4, 2, 0, s.ks[t], 0, rows.qs[i]);
+            z = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(k, rows.q[i][1], z, 4, 2, 0, s.ks[t], 1, rows.qs[i]);
             if constexpr (D == 128)
-                z = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(k, rows.q[i][2], z, 4, 2, 0, ks, 2, rows.qs[i]);
+                z = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(k, rows.q[i][2], z, 4, 2, 0, s.ks[t], 2, rows.qs[i]);
             x[i][t] = z;
         }
     }
@@ -484,33 +420,31 @@ __device__ __forceinline__ void values_not_finite(Values<D>& s, const Rows<NQ>& 
     }
 }
 
-// Weights of a step's tokens, and their products with its values. next_keys: called when the keys' registers are free.
-template <int D, int NQ, typename F>
-__device__ __forceinline__ void take_step(const Keys& keys, const uint8_t* stage, int base, bool ok0, bool ok1,
-                                          const Rows<NQ>& rows, Sums<D, NQ>& sums, const Lane<D>& ln, F next_keys) {
+// Weights of a step's tokens, and their products with its values.
+template <int D, int NQ>
+__device__ __forceinline__ void take_step(const Keys<D>& keys, Values<D>& s, const Place& p, const Rows<NQ>& rows,
+                                          Sums<D, NQ>& sums, const Lane<D>& ln) {
     constexpr int NJ = D / 16;
-    Values<D> s;
-    read_values<D>(s, stage, ln);
     f32x4 x[NQ][2];
     score<D, NQ>(x, keys, rows, sums);
-    if (base < rows.lo_max || base + kStep > rows.hi_min || !(ok0 && ok1)) {   // not every row sees every token
-        const bool there = ln.g < 2 ? ok0 : ok1;
+    if (p.base < rows.lo_max || p.base + kStep > rows.hi_min || !(p.ok[0] && p.ok[1])) {   // not every row sees every token
+        const bool there = ln.g < 2 ? p.ok[0] : p.ok[1];
         bool high = false;
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int j = base + 8 * ln.g + 4 * t + r;
+                const int j = p.base + 8 * ln.g + 4 * t + r;
 #pragma unroll
                 for (int i = 0; i < NQ; ++i)
                     x[i][t][r] = there && j >= rows.lo[i] && j < rows.hi[i] ? x[i][t][r] : -INFINITY;
                 // values that no row sees stay finite whatever is there
-                const int jv = base + 16 * t + 4 * ln.g + r;
-                clear_token<D>(s, t, r, !((t ? ok1 : ok0) && jv >= rows.lo_all && jv < rows.hi_all));
+                const int jv = p.base + 16 * t + 4 * ln.g + r;
+                clear_token<D>(s, t, r, !(p.ok[t] && jv >= rows.lo_all && jv < rows.hi_all));
                 const uint32_t w = scale_bytes<D>(s.vs[t], r);
                 high |= (w & (w << 1) & 0x80808080u) != 0;   // bytes from 192 on: rare enough to be looked at one by one
             }
-        if (__any(high)) values_not_finite<D, NQ>(s, rows, sums, base, ln);
+        if (__any(high)) values_not_finite<D, NQ>(s, rows, sums, p.base, ln);
     }
     // the maximum is left alone until a score is 2^8 above it
     bool past = false;
@@ -556,7 +490,6 @@ __device__ __forceinline__ void take_step(const Keys& keys, const uint8_t* stage
         w[i] = __builtin_bit_cast(bf16x8, pk);
         sums.l[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[i], __builtin_bit_cast(bf16x8, ones), sums.l[i], 0, 0, 0);
     }
-    next_keys();
     // values: a byte (two channels) of all eight tokens at a time
     float sc[8];
 #pragma unroll
@@ -685,21 +618,20 @@ __device__ __forceinline__ void set_ranges(Rows<NQ>& rows, const Attention& a, c
 
 // Steps first, first + stride, .. below `last` of a wave's rows. The bytes of the steps to come are on their way while
 // one is worked on.
-template <int D, int NQ>
+template <int D, int NQ, int kAhead>
 __device__ __forceinline__ void run_steps(const Attention& a, const CacheView& c, const int32_t* table, const Span& s,
                                           int kv_head, int group, int row0, int first, int last, int stride,
-                                          Sums<D, NQ>& sums, const uint8_t* ring, const Lane<D>& ln) {
+                                          Sums<D, NQ>& sums, const Lane<D>& ln) {
     Rows<NQ> rows;
     set_ranges<D, NQ>(rows, a, s, group, row0, ln);
+    sums.clear();
+    if (c.slots == 0) return;   // no page is there
     // steps with a token that some row sees
     int at = first;
     const int low = rows.lo_all / kStep;
     if (at < low) at += (int)((uint32_t)(low - at + stride - 1) / (uint32_t)stride) * stride;
     const int end = min(last, (int)(((uint32_t)rows.hi_all + kStep - 1) / kStep));
-    if (at >= end || c.slots == 0) {   // nothing to see, or no page is there
-        sums.clear();
-        return;
-    }
+    if (at >= end) return;
     // the queries' bytes first: their parts are made while the first tokens are on their way
     u32x4 w[NQ][4];
 #pragma unroll
@@ -712,46 +644,40 @@ __device__ __forceinline__ void run_steps(const Attention& a, const CacheView& c
 #pragma unroll
         for (int b = 0; b < 4; ++b) w[i][b] = *reinterpret_cast<const u32x4*>(p + 8 * b);
     }
-    int pages = pages_ahead(a, c, table, at, stride, rows.lo_all, rows.hi_all, ln.lane);
-    int later = pages_ahead(a, c, table, at + 32 * stride, stride, rows.lo_all, rows.hi_all, ln.lane);
-    const uint32_t lds = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t*)ring;
-    int i = 0;       // place in `pages` of the step to request next
-    int ahead = at;  // and the step
-    int there = 0;   // bit 2 s + t: half t of the step of stage s is there
-    auto request = [&](int stage) {
+    const int lane = threadIdx.x % kWave;
+    int pages = pages_ahead(a, c, table, at, stride, rows.lo_all, rows.hi_all, lane);
+    int later = pages_ahead(a, c, table, at + 32 * stride, stride, rows.lo_all, rows.hi_all, lane);
+    int i = 0;       // place in `pages` of the step whose keys are loaded next
+    int ahead = at;  // and the step; past the end they are the cache's first tokens or a neighbour's, and not used
+    auto next_place = [&] {
         const Place p = place_of(c, pages, i, kv_head, ahead * kStep);
-        there = (there & ~(3 << (2 * stage))) | ((p.ok[0] ? 1 : 0) | (p.ok[1] ? 2 : 0)) << (2 * stage);
-        request_step<D>(c, p, lds + stage * Stage<D>::kBytes, ln);
         ahead += stride;
         if (++i == 32) {
             i = 0;
             pages = later;
-            later = pages_ahead(a, c, table, ahead + 32 * stride, stride, rows.lo_all, rows.hi_all, ln.lane);
+            later = pages_ahead(a, c, table, ahead + 32 * stride, stride, rows.lo_all, rows.hi_all, lane);
         }
+        return p;
+    };
+    Keys<D> keys[kAhead];
+    Values<D> values[kAhead];
+    Place places[kAhead];
+    auto load = [&](int b) {
+        places[b] = next_place();
+        load_keys<D>(keys[b], c, places[b], ln);
+        load_values<D>(values[b], c, places[b], ln);
     };
 #pragma unroll
-    for (int b = 0; b + 1 < kStages; ++b)
-        if (ahead < end) request(b);
+    for (int b = 0; b + 1 < kAhead; ++b) load(b);
 #pragma unroll
     for (int b = 0; b < NQ; ++b) split_query<D>(w[b], a.scale * kLog2e, ln.g, rows.q[b], rows.qs[b]);
-    __builtin_amdgcn_sched_barrier(0);   // no zeros in registers before this
-    sums.clear();
-    int stage = 0;
-    Keys keys;
-    auto wait_and_read = [&](int of) {   // the oldest step under way is there when all but those after it are
-        if (ahead < end) wait_vm<Stage<D>::kRequests * (kStages - 2)>();
-        else wait_vm<0>();
-        read_keys<D>(keys, ring + of * Stage<D>::kBytes, ln);
-    };
-    wait_and_read(0);
     for (;;) {
-        const int next = stage == kStages - 1 ? 0 : stage + 1;
-        const int ok = there >> (2 * stage);
-        if (ahead < end) request(stage == 0 ? kStages - 1 : stage - 1);
-        take_step<D, NQ>(keys, ring + stage * Stage<D>::kBytes, at * kStep, (ok & 1) != 0, (ok & 2) != 0, rows, sums, ln,
-                         [&] { if (at + stride < end) wait_and_read(next); });
-        stage = next;
-        if ((at += stride) >= end) return;
+#pragma unroll
+        for (int b = 0; b < kAhead; ++b) {
+            load((b + kAhead - 1) % kAhead);
+            take_step<D, NQ>(keys[b], values[b], places[b], rows, sums, ln);
+            if ((at += stride) >= end) return;
+        }
     }
 }
 
@@ -803,11 +729,8 @@ __global__ __launch_bounds__(kW * kWave, 2) void attention_split_kernel(Attentio
                                                                         int record_count, bool by_segment) {
     constexpr int NJ = D / 16;
     constexpr int kRows = 16 * NQ;
-    // each wave's ring; between segments the waves' sums
-    __shared__ __attribute__((aligned(16))) uint8_t ring[kW][kStages * Stage<D>::kBytes];
-    static_assert(kW == 1 || sizeof(ring) >= sizeof(float) * kW * (4 * NJ * kWave + 32), "the sums fit the rings");
-    float(*lo_o)[4 * NJ][kWave] = reinterpret_cast<float(*)[4 * NJ][kWave]>(&ring[0][0]);
-    float(*lo_ml)[16][2] = reinterpret_cast<float(*)[16][2]>(&ring[0][0] + sizeof(float) * kW * 4 * NJ * kWave);
+    __shared__ float lo_o[kW == 1 ? 1 : kW][kW == 1 ? 1 : 4 * NJ][kWave];   // the waves' sums
+    __shared__ float lo_ml[kW][16][2];
     const int lane = threadIdx.x % kWave, wave = uniform(threadIdx.x / kWave);
     // neighbours in the order of work on the same XCD, whose L2 then holds what they share
     const int per_xcd = workers / 8;
@@ -856,8 +779,8 @@ __global__ __launch_bounds__(kW * kWave, 2) void attention_split_kernel(Attentio
         const int row0 = (int)(segment - head * tiles) * kRows;
         const int origin = first_seen(a, s, 0) / kStep, steps = unit_bits - 5;
         Sums<D, NQ> sums;
-        run_steps<D, NQ>(a, c, a.page_table + seq * a.table_width, s, head, group, row0,
-                         origin + (u0 << steps) + wave, origin + (u1 << steps), kW, sums, ring[wave], ln);
+        run_steps<D, NQ, 2>(a, c, a.page_table + seq * a.table_width, s, head, group, row0,
+                                          origin + (u0 << steps) + wave, origin + (u1 << steps), kW, sums, ln);
         const bool whole = u0 == 0 && u1 == (int)units;
         float* part = parts + (2 * (size_t)id + (u0 > 0 ? 0 : 1)) * part_floats<D, NQ>();
         const int rows_left = s.n * group - row0;
@@ -922,8 +845,7 @@ __global__ __launch_bounds__(kW * kWave, 2) void attention_split_kernel(Attentio
                 put(o, 16 * i + mine, NJ * ln.n + j0, m, total);
             }
         }
-        if constexpr (kW > 1) __syncthreads();   // the rings are free again
-        if (u1 == (int)units) {   // the segment ends here
+                if (u1 == (int)units) {   // the segment ends here
             Record r = {row0, s.first, 0, 0, min(kRows, rows_left), head, {0, 0}};
             if (u0 > 0) {
                 const uint32_t edge = more * (share + 1);
@@ -998,7 +920,6 @@ template <int D, int NQ>
 __global__ __launch_bounds__(kRowWaves * kWave, 2) void attention_rows_kernel(Attention a, CacheView c, int round) {
     constexpr int NJ = D / 16;
     constexpr int kRows = 16 * NQ;
-    __shared__ __attribute__((aligned(16))) uint8_t ring[kRowWaves][kStages * Stage<D>::kBytes];
     const int lane = threadIdx.x % kWave, wave = uniform(threadIdx.x / kWave);
     const int group = a.heads / c.heads;
     const Lane<D> ln(c, lane);
@@ -1018,7 +939,7 @@ __global__ __launch_bounds__(kRowWaves * kWave, 2) void attention_rows_kernel(At
     const int rows_left = s.n * group - row0;
     if (rows_left <= 0) return;
     Sums<D, NQ> sums;
-    run_steps<D, NQ>(a, c, a.page_table + seq * a.table_width, s, head, group, row0, 0, kFarRight, 1, sums, ring[wave], ln);
+    run_steps<D, NQ, 2>(a, c, a.page_table + seq * a.table_width, s, head, group, row0, 0, kFarRight, 1, sums, ln);
 #pragma unroll
     for (int i = 0; i < NQ; ++i)
 #pragma unroll
@@ -1073,10 +994,16 @@ Form form_of(int64_t tokens, int64_t seqs, int64_t heads, int64_t kv_heads, int6
             return {kRowsForm, 1, 0, 0, 0, 0};
     }
     Form f = split_of(tokens, seqs, heads, kv_heads, mean);
-    if (length <= 1024 && f.segments <= 2 * cus) {
+    // Whole segments save the second launch and pay in longer chains of steps: 6.5 us and 1.1 a step for each round of workers
+    // against 12.4 and 1.1 a step of an equal share (one token of 777: 10.7 against 12.7; 16 of 2048: 16.5 against 17.2;
+    // of 2048 alone: 15.4 against 12.4).
+    const int waves = f.segments <= cus ? 8 : f.segments <= 2 * cus ? 4 : 1;
+    const int64_t steps = (length + kStep * waves - 1) / (kStep * waves);
+    const int64_t rounds = (f.segments * waves + 8 * cus - 1) / (8 * cus);
+    if (steps <= 8 && f.segments < 1 << 20 && rounds * (65 + 11 * steps) < 124 + 11 * f.segments * steps * waves / (8 * cus)) {
         f.kind = kWholeForm;
-        f.waves = f.segments <= cus ? 8 : 4;
-        f.workers = (int)(f.segments < 1 << 20 ? f.segments : 1 << 20);
+        f.waves = waves;
+        f.workers = (int)f.segments;
     }
     return f;
 }
