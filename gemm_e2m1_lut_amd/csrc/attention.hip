@@ -59,6 +59,24 @@ typedef uint32_t u32x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x32 __attribute__((ext_vector_type(32)));
 
+// Quotients of numbers below 2^29 by `d` below 2^13 (Granlund and Montgomery): with 2^bits >= d and mul = ceil(2^(29 + bits) / d),
+// n mul / 2^(29 + bits) exceeds n / d by less than 1 / d.
+struct Divisor {
+    uint32_t mul;
+    int bits;
+};
+
+Divisor divisor_of(uint32_t d) {
+    Divisor v = {0, 0};
+    while ((1u << v.bits) < d) ++v.bits;
+    v.mul = (uint32_t)((((uint64_t)1 << (29 + v.bits)) + d - 1) / d);
+    return v;
+}
+
+__device__ __forceinline__ int divide(int n, const Divisor& d) {
+    return (int)(__umulhi((uint32_t)n << 3, d.mul) >> d.bits);
+}
+
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 __device__ __forceinline__ float exp2_raw(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -302,12 +320,6 @@ __device__ __forceinline__ Place place_of(const CacheView& c, int pages, int i, 
     return p;
 }
 
-// A 32-bit offset that stays one at its load, whose address is then a scalar base and this.
-__device__ __forceinline__ uint32_t here(uint32_t offset) {
-    asm("" : "+v"(offset));
-    return offset;
-}
-
 template <int D>
 __device__ __forceinline__ void load_keys(Keys<D>& s, const CacheView& c, const Place& p, const Lane<D>& ln) {
     const int64_t row = ln.n < 8 ? p.row[0] : p.row[1];
@@ -326,18 +338,17 @@ __device__ __forceinline__ void load_values(Values<D>& s, const CacheView& c, co
     for (int t = 0; t < 2; ++t) {
         const uint8_t* v = c.v_codes + p.row[t] * (D / 2);
         const uint8_t* x = c.v_scales + p.row[t] * (D / 32);
-        const uint32_t at = here(ln.v);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            if constexpr (D == 128) s.v[4 * t + r] = *reinterpret_cast<const uint32_t*>(v + at + r * 64);
-            else s.v[4 * t + r] = *reinterpret_cast<const uint16_t*>(v + at + r * 32);
+            if constexpr (D == 128) s.v[4 * t + r] = *reinterpret_cast<const uint32_t*>(v + ln.v + r * 64);
+            else s.v[4 * t + r] = *reinterpret_cast<const uint16_t*>(v + ln.v + r * 32);
         }
         if constexpr (D == 128) {
-            const u32x4 w = *reinterpret_cast<const u32x4*>(x + here(ln.vs));
+            const u32x4 w = *reinterpret_cast<const u32x4*>(x + ln.vs);
 #pragma unroll
             for (int r = 0; r < 4; ++r) s.vs[t][r] = w[r];
         } else {
-            const u32x2 w = *reinterpret_cast<const u32x2*>(x + here(ln.vs));
+            const u32x2 w = *reinterpret_cast<const u32x2*>(x + ln.vs);
             s.vs[t][0] = w.x;
             s.vs[t][1] = w.y;
         }
@@ -594,10 +605,10 @@ __device__ __forceinline__ void split_query(const u32x4 (&w)[4], float scale, in
 
 // The rows [row0, row0 + 16 NQ) of a sequence's (query, head of the group) pairs; rows past the last one see what it sees.
 template <int D, int NQ>
-__device__ __forceinline__ void set_ranges(Rows<NQ>& rows, const Attention& a, const Span& s, int group, int row0,
+__device__ __forceinline__ void set_ranges(Rows<NQ>& rows, const Attention& a, const Span& s, int group, const Divisor& by, int row0,
                                            const Lane<D>& ln) {
     const int last = s.n * group - 1;
-    const int i_first = row0 / group, i_last = min(row0 + 16 * NQ - 1, last) / group;
+    const int i_first = divide(row0, by), i_last = divide(min(row0 + 16 * NQ - 1, last), by);
     const int p0 = s.len - s.n;   // position of query 0
     if (a.causal) {
         rows.lo_all = first_seen(a, s, i_first);
@@ -610,7 +621,7 @@ __device__ __forceinline__ void set_ranges(Rows<NQ>& rows, const Attention& a, c
     }
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
-        const int q = (int)((uint32_t)min(row0 + 16 * i + ln.n, last) / (uint32_t)group);
+        const int q = divide(min(row0 + 16 * i + ln.n, last), by);
         rows.lo[i] = a.causal ? first_seen(a, s, q) : 0;
         rows.hi[i] = a.causal ? max(0, p0 + q + 1) : s.len;
     }
@@ -618,18 +629,19 @@ __device__ __forceinline__ void set_ranges(Rows<NQ>& rows, const Attention& a, c
 
 // Steps first, first + stride, .. below `last` of a wave's rows. The bytes of the steps to come are on their way while
 // one is worked on.
-template <int D, int NQ, int kAhead>
+template <int D, int NQ>
 __device__ __forceinline__ void run_steps(const Attention& a, const CacheView& c, const int32_t* table, const Span& s,
-                                          int kv_head, int group, int row0, int first, int last, int stride,
+                                          int kv_head, int group, const Divisor& by, int row0, int first, int last,
+                                          int stride,
                                           Sums<D, NQ>& sums, const Lane<D>& ln) {
     Rows<NQ> rows;
-    set_ranges<D, NQ>(rows, a, s, group, row0, ln);
+    set_ranges<D, NQ>(rows, a, s, group, by, row0, ln);
     sums.clear();
     if (c.slots == 0) return;   // no page is there
     // steps with a token that some row sees
     int at = first;
     const int low = rows.lo_all / kStep;
-    if (at < low) at += (int)((uint32_t)(low - at + stride - 1) / (uint32_t)stride) * stride;
+    if (at < low) at += (low - at + stride - 1) & ~(stride - 1);   // stride: a power of two
     const int end = min(last, (int)(((uint32_t)rows.hi_all + kStep - 1) / kStep));
     if (at >= end) return;
     // the queries' bytes first: their parts are made while the first tokens are on their way
@@ -637,7 +649,7 @@ __device__ __forceinline__ void run_steps(const Attention& a, const CacheView& c
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
         const int row = min(row0 + 16 * i + ln.n, s.n * group - 1);
-        const int q = (int)((uint32_t)row / (uint32_t)group);
+        const int q = divide(row, by);
         const int block = D == 128 ? ln.g : ln.g & 1;
         const uint16_t* p =
             a.q + (int64_t)(s.first + q) * a.q_stride + (int64_t)(kv_head * group + (row - q * group)) * D + block * 32;
@@ -659,25 +671,24 @@ __device__ __forceinline__ void run_steps(const Attention& a, const CacheView& c
         }
         return p;
     };
-    Keys<D> keys[kAhead];
-    Values<D> values[kAhead];
-    Place places[kAhead];
-    auto load = [&](int b) {
-        places[b] = next_place();
-        load_keys<D>(keys[b], c, places[b], ln);
-        load_values<D>(values[b], c, places[b], ln);
-    };
-#pragma unroll
-    for (int b = 0; b + 1 < kAhead; ++b) load(b);
+    Keys<D> keys[2];
+    Values<D> values[2];
+    Place p0 = next_place(), p1;
+    load_keys<D>(keys[0], c, p0, ln);
+    load_values<D>(values[0], c, p0, ln);
 #pragma unroll
     for (int b = 0; b < NQ; ++b) split_query<D>(w[b], a.scale * kLog2e, ln.g, rows.q[b], rows.qs[b]);
     for (;;) {
-#pragma unroll
-        for (int b = 0; b < kAhead; ++b) {
-            load((b + kAhead - 1) % kAhead);
-            take_step<D, NQ>(keys[b], values[b], places[b], rows, sums, ln);
-            if ((at += stride) >= end) return;
-        }
+        p1 = next_place();
+        load_keys<D>(keys[1], c, p1, ln);
+        load_values<D>(values[1], c, p1, ln);
+        take_step<D, NQ>(keys[0], values[0], p0, rows, sums, ln);
+        if ((at += stride) >= end) return;
+        p0 = next_place();
+        load_keys<D>(keys[0], c, p0, ln);
+        load_values<D>(values[0], c, p0, ln);
+        take_step<D, NQ>(keys[1], values[1], p1, rows, sums, ln);
+        if ((at += stride) >= end) return;
     }
 }
 
@@ -694,17 +705,18 @@ __device__ __forceinline__ float last_factor(float m, float l, const float* sink
         f = exp2_raw(m - mn);
         l = l * f + exp2_raw(s - mn);
     }
-    return l == 0.0f ? 0.0f : f / l;
+    return l == 0.0f ? 0.0f : f * __builtin_amdgcn_rcpf(l);
 }
 
 template <int NJ>
 __device__ __forceinline__ void store_out(uint16_t* p, const float (&v)[NJ]) {
-    uint32_t w[NJ / 2];
+    uint32_t w[NJ / 2 + 1];
 #pragma unroll
-    for (int j = 0; j < NJ / 2; ++j) w[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+    for (int j = 0; j < NJ / 2; ++j) w[j] = pack_weights(v[2 * j], v[2 * j + 1]);
     if constexpr (NJ == 8) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
     else if constexpr (NJ == 4) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
-    else *reinterpret_cast<uint32_t*>(p) = w[0];
+    else if constexpr (NJ == 2) *reinterpret_cast<uint32_t*>(p) = w[0];
+    else *p = (uint16_t)pack_weights(v[0], v[0]);
 }
 
 // Where a segment (a tile of a sequence) was cut: its parts are the second one of worker `from` and the first ones of the
@@ -726,11 +738,12 @@ constexpr size_t part_floats() { return (size_t)16 * NQ * (D + 2); }
 template <int D, int NQ, int kW>
 __global__ __launch_bounds__(kW * kWave, 2) void attention_split_kernel(Attention a, CacheView c, float* parts,
                                                                         Record* records, int workers, int unit_bits,
-                                                                        int record_count, bool by_segment) {
+                                                                        int record_count, bool by_segment, Divisor by) {
     constexpr int NJ = D / 16;
     constexpr int kRows = 16 * NQ;
-    __shared__ float lo_o[kW == 1 ? 1 : kW][kW == 1 ? 1 : 4 * NJ][kWave];   // the waves' sums
-    __shared__ float lo_ml[kW][16][2];
+    __shared__ f32x4 lo_o[kW == 1 ? 1 : kW][kW == 1 ? 1 : NJ][kWave];   // the waves' sums
+    __shared__ __attribute__((aligned(16))) float lo_m[kW][16];
+    __shared__ f32x4 lo_l[kW][4];
     const int lane = threadIdx.x % kWave, wave = uniform(threadIdx.x / kWave);
     // neighbours in the order of work on the same XCD, whose L2 then holds what they share
     const int per_xcd = workers / 8;
@@ -745,7 +758,9 @@ __global__ __launch_bounds__(kW * kWave, 2) void attention_split_kernel(Attentio
         if (threadIdx.x == 0 && id < record_count) records[id].from = records[id].to = 0;
         return;
     }
-    const uint32_t share = plan.total / (uint32_t)workers, more = plan.total - share * workers;
+    // without records a worker has one segment
+    const uint32_t share = records ? plan.total / (uint32_t)workers : 0;
+    const uint32_t more = plan.total - share * workers;
     uint32_t u = id * share + min((uint32_t)id, more);
     const uint32_t u_end = u + share + ((uint32_t)id < more ? 1 : 0);
     const bool idle = u >= u_end;
@@ -770,16 +785,16 @@ __global__ __launch_bounds__(kW * kWave, 2) void attention_split_kernel(Attentio
             units = units_of(a, s, unit_bits);
             segs = segments(s);
         }
-        const uint32_t segment = (u - begin) / units;
+        const uint32_t segment = units == 1 ? u - begin : (u - begin) / units;
         const uint32_t seg_begin = begin + segment * units;
         const int u0 = (int)(u - seg_begin);
         const int u1 = (int)min(units, u_end - seg_begin);
-        const uint32_t tiles = segs / (uint32_t)c.heads;
-        const int head = (int)(segment / tiles);
+        const uint32_t tiles = tiles_of(s, group, kRows);
+        const int head = (int)(tiles == 1 ? segment : segment / tiles);
         const int row0 = (int)(segment - head * tiles) * kRows;
         const int origin = first_seen(a, s, 0) / kStep, steps = unit_bits - 5;
         Sums<D, NQ> sums;
-        run_steps<D, NQ, 2>(a, c, a.page_table + seq * a.table_width, s, head, group, row0,
+        run_steps<D, NQ>(a, c, a.page_table + seq * a.table_width, s, head, group, by, row0,
                                           origin + (u0 << steps) + wave, origin + (u1 << steps), kW, sums, ln);
         const bool whole = u0 == 0 && u1 == (int)units;
         float* part = parts + (2 * (size_t)id + (u0 > 0 ? 0 : 1)) * part_floats<D, NQ>();
@@ -789,7 +804,7 @@ __global__ __launch_bounds__(kW * kWave, 2) void attention_split_kernel(Attentio
             constexpr int kN = sizeof(o) / sizeof(float);
             if (at >= rows_left) return;
             if (whole) {
-                const int row = row0 + at, q = (int)((uint32_t)row / (uint32_t)group);
+                const int row = row0 + at, q = divide(row, by);
                 const int h = head * group + (row - q * group);
                 const float f = last_factor(m, total, a.sinks, h);
 #pragma unroll
@@ -819,33 +834,42 @@ __global__ __launch_bounds__(kW * kWave, 2) void attention_split_kernel(Attentio
             } else {
                 __syncthreads();
 #pragma unroll
-                for (int j = 0; j < NJ; ++j)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) lo_o[wave][r * NJ + j][lane] = sums.o[i][j][r];
-                if (lane < 16) lo_ml[wave][lane][0] = sums.top(i);
-                if (ln.n == 0)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) lo_ml[wave][4 * ln.g + r][1] = sums.l[i][r];
+                for (int j = 0; j < NJ; ++j) lo_o[wave][j][lane] = sums.o[i][j];
+                if (lane < 16) lo_m[wave][lane] = sums.top(i);
+                if (ln.n == 0) lo_l[wave][ln.g] = sums.l[i];
                 __syncthreads();
-                // wave w joins row 4 g + w % 4, its channels in kW / 4 runs
-                constexpr int kN = NJ * 4 / kW;
-                const int mine = 4 * ln.g + wave % 4, j0 = wave / 4 * kN;
-                float m = lo_ml[0][mine][0];
+                // wave w joins channels [w kN, ..) of every run of NJ, for this lane's four rows
+                constexpr int kN = NJ >= kW ? NJ / kW : 1;
+                if (wave * kN < NJ) {
+                    f32x4 m = *reinterpret_cast<const f32x4*>(&lo_m[0][4 * ln.g]);
 #pragma unroll
-                for (int w = 1; w < kW; ++w) m = fmaxf(m, lo_ml[w][mine][0]);
-                const float m0 = finite_or_zero(m);
-                float o[kN] = {}, total = 0.0f;
+                    for (int w = 1; w < kW; ++w) {
+                        const f32x4 v = *reinterpret_cast<const f32x4*>(&lo_m[w][4 * ln.g]);
 #pragma unroll
-                for (int w = 0; w < kW; ++w) {
-                    const float f = exp2_raw(lo_ml[w][mine][0] - m0);
-                    total += f * lo_ml[w][mine][1];
+                        for (int r = 0; r < 4; ++r) m[r] = fmaxf(m[r], v[r]);
+                    }
+                    f32x4 o[kN] = {}, total = {0, 0, 0, 0};
 #pragma unroll
-                    for (int j = 0; j < kN; ++j) o[j] += f * lo_o[w][wave % 4 * NJ + j0 + j][lane];
+                    for (int w = 0; w < kW; ++w) {
+                        const f32x4 v = *reinterpret_cast<const f32x4*>(&lo_m[w][4 * ln.g]);
+                        f32x4 f;
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) f[r] = exp2_raw(v[r] - finite_or_zero(m[r]));
+                        total += f * lo_l[w][ln.g];
+#pragma unroll
+                        for (int j = 0; j < kN; ++j) o[j] += f * lo_o[w][wave * kN + j][lane];
+                    }
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        float v[kN];
+#pragma unroll
+                        for (int j = 0; j < kN; ++j) v[j] = o[j][r];
+                        put(v, 16 * i + 4 * ln.g + r, NJ * ln.n + wave * kN, m[r], total[r]);
+                    }
                 }
-                put(o, 16 * i + mine, NJ * ln.n + j0, m, total);
             }
         }
-                if (u1 == (int)units) {   // the segment ends here
+        if (u1 == (int)units) {   // the segment ends here
             Record r = {row0, s.first, 0, 0, min(kRows, rows_left), head, {0, 0}};
             if (u0 > 0) {
                 const uint32_t edge = more * (share + 1);
@@ -865,7 +889,7 @@ constexpr int kJoinWaves = 4;
 // Joins the parts of a segment, a wave a row: two parts at a time, half a wave each, sixteen of them on their way.
 template <int D, int NQ>
 __global__ __launch_bounds__(kJoinWaves * kWave) void attention_join_kernel(Attention a, CacheView c, const float* parts,
-                                                                        const Record* records) {
+                                                                        const Record* records, Divisor by) {
     constexpr int kRows = 16 * NQ;
     constexpr int kEach = D / 32;
     const Record r = records[blockIdx.x];
@@ -903,21 +927,21 @@ __global__ __launch_bounds__(kJoinWaves * kWave) void attention_join_kernel(Atte
         total += __shfl_xor(total, 32, kWave);
 #pragma unroll
         for (int e = 0; e < kEach; ++e) o[e] += __shfl_xor(o[e], 32, kWave);
-        const int row = r.row0 + at, q = (int)((uint32_t)row / (uint32_t)group);
+        const int row = r.row0 + at, q = divide(row, by);
         const int h = r.head * group + (row - q * group);
         const float f = last_factor(m, total, a.sinks, h);
         if (half == 0) {
             uint16_t* out = a.out + ((int64_t)(r.first + q) * a.heads + h) * D + place * kEach;
             if constexpr (kEach == 4)
-                *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(o[0] * f, o[1] * f), pack_bf16x2(o[2] * f, o[3] * f));
-            else *reinterpret_cast<uint32_t*>(out) = pack_bf16x2(o[0] * f, o[1] * f);
+                *reinterpret_cast<uint2*>(out) = make_uint2(pack_weights(o[0] * f, o[1] * f), pack_weights(o[2] * f, o[3] * f));
+            else *reinterpret_cast<uint32_t*>(out) = pack_weights(o[0] * f, o[1] * f);
         }
     }
 }
 
 // Many rows: a wave has a tile of its own and goes through all that it sees; the tiles with the most tokens first.
 template <int D, int NQ>
-__global__ __launch_bounds__(kRowWaves * kWave, 2) void attention_rows_kernel(Attention a, CacheView c, int round) {
+__global__ __launch_bounds__(kRowWaves * kWave, 2) void attention_rows_kernel(Attention a, CacheView c, int round, Divisor by) {
     constexpr int NJ = D / 16;
     constexpr int kRows = 16 * NQ;
     const int lane = threadIdx.x % kWave, wave = uniform(threadIdx.x / kWave);
@@ -939,7 +963,7 @@ __global__ __launch_bounds__(kRowWaves * kWave, 2) void attention_rows_kernel(At
     const int rows_left = s.n * group - row0;
     if (rows_left <= 0) return;
     Sums<D, NQ> sums;
-    run_steps<D, NQ, 2>(a, c, a.page_table + seq * a.table_width, s, head, group, row0, 0, kFarRight, 1, sums, ln);
+    run_steps<D, NQ>(a, c, a.page_table + seq * a.table_width, s, head, group, by, row0, 0, kFarRight, 1, sums, ln);
 #pragma unroll
     for (int i = 0; i < NQ; ++i)
 #pragma unroll
@@ -947,7 +971,7 @@ __global__ __launch_bounds__(kRowWaves * kWave, 2) void attention_rows_kernel(At
             const int r = 16 * i + 4 * ln.g + e;
             const float m = __shfl(sums.top(i), 4 * ln.g + e, kWave);
             if (r < rows_left) {
-                const int row = row0 + r, q = (int)((uint32_t)row / (uint32_t)group);
+                const int row = row0 + r, q = divide(row, by);
                 const int h = head * group + (row - q * group);
                 const float f = last_factor(m, sums.l[i][e], a.sinks, h);
                 float o[NJ];
@@ -979,7 +1003,7 @@ Form split_of(int64_t tokens, int64_t seqs, int64_t heads, int64_t kv_heads, int
     const int64_t group = heads / kv_heads, cus = device_cu_count();
     const int nq = mean > 16 ? 2 : 1;
     const int64_t segments = most_tiles(tokens, seqs, group, 16 * nq) * kv_heads;
-    const int waves = segments >= cus / 2 ? 1 : 4;
+    const int waves = segments >= cus / 2 && nq == 1 ? 1 : 4;
     return {kSplitForm, nq, waves, (int)(8 / waves * cus), segments,
             (int)(((mean < 16 * nq ? mean : 16 * nq) + kJoinWaves - 1) / kJoinWaves)};
 }
@@ -1016,9 +1040,11 @@ hipError_t split_form(const Attention& a, const CacheView& c, const Form& f, voi
     while (f.segments > ((int64_t)1 << 30) / (((a.table_width << c.page_bits) >> unit_bits) + 2)) ++unit_bits;
     attention_split_kernel<D, NQ, kW><<<f.workers, kW * kWave, 0, stream>>>(a, c, parts, records, f.workers, unit_bits,
                                                                             f.records(),
-                                                                            records && f.segments <= f.workers);
+                                                                            records && f.segments <= f.workers,
+                                                                            divisor_of(a.heads / c.heads));
     if (hipError_t e = hipGetLastError(); e != hipSuccess || !records) return e;
-    attention_join_kernel<D, NQ><<<dim3(f.records(), f.join_rows), kJoinWaves * kWave, 0, stream>>>(a, c, parts, records);
+    attention_join_kernel<D, NQ><<<dim3(f.records(), f.join_rows), kJoinWaves * kWave, 0, stream>>>(a, c, parts, records,
+                                                                                             divisor_of(a.heads / c.heads));
     return hipGetLastError();
 }
 
@@ -1034,7 +1060,7 @@ hipError_t rows_form(const Attention& a, const CacheView& c, hipStream_t stream)
     const int round = device_cu_count() > c.heads ? device_cu_count() / c.heads : 1;
     const int64_t tiles = most_tiles(a.tokens, a.seqs, a.heads / c.heads, 16 * NQ * kRowWaves);
     const int64_t grid = (tiles + round - 1) / round * round * c.heads;   // whole rounds: see the kernel's order
-    attention_rows_kernel<D, NQ><<<(unsigned)grid, kRowWaves * kWave, 0, stream>>>(a, c, round);
+    attention_rows_kernel<D, NQ><<<(unsigned)grid, kRowWaves * kWave, 0, stream>>>(a, c, round, divisor_of(a.heads / c.heads));
     return hipGetLastError();
 }
 
