@@ -35,23 +35,48 @@ namespace {
 constexpr int kThreads = 256;
 constexpr uint32_t kInfBits = 0x7F800000u;
 
-// Eight channels of a row as fp32.
-__device__ __forceinline__ void load8(const uint16_t* p, float (&x)[8]) {
-    const uint4 a = load_nt16(p);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+// Eight channels of a row as they lie in memory.
+template <typename T>
+struct Raw;
+
+template <>
+struct Raw<uint16_t> {
+    uint4 a;
+    __device__ __forceinline__ void load(const uint16_t* p) { a = load_nt16(p); }
+    __device__ __forceinline__ void get(float (&x)[8]) const {
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(w[i] << 16);
+            x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
     }
+};
+
+template <>
+struct Raw<float> {
+    uint4 a, b;
+    __device__ __forceinline__ void load(const float* p) {
+        // not streaming: the two halves of a line come with two instructions, and a streaming load would fetch it twice (4097
+        // tokens of 8 heads of 64: 10.3 us with the read back instead of 14.4)
+        a = *reinterpret_cast<const uint4*>(p);
+        b = *reinterpret_cast<const uint4*>(p + 4);
+    }
+    __device__ __forceinline__ void get(float (&x)[8]) const {
+        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
+    }
+};
+
+// Two bf16 numbers, rounded to nearest, ties to even.
+__device__ __forceinline__ uint32_t round_bf16x2(float lo, float hi) {
+    const f32x2 v = {lo, hi};
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
 }
 
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-    const uint4 a = load_nt16(p), b = load_nt16(p + 4);
-    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
-}
+// Rows that a group has on their way at a time.
+constexpr int kAtOnce = 4;
 
 template <int kCtrl>
 __device__ __forceinline__ uint32_t dpp_u32(uint32_t v) {
@@ -100,6 +125,13 @@ __device__ __forceinline__ void norm_wide(float (&x)[8], const float (&w)[8], fl
     for (int i = 0; i < 8; ++i) x[i] = (float)((double)x[i] * f * w[i]);
 }
 
+template <typename T>
+__device__ __forceinline__ void load_row(const T* p, float (&x)[8]) {
+    Raw<T> raw;
+    raw.load(p);
+    raw.get(x);
+}
+
 template <int D>
 __device__ __forceinline__ void store_row(const float (&x)[8], uint8_t* codes, uint8_t* scales, int64_t row, int lane,
                                           bool live) {
@@ -133,13 +165,23 @@ __global__ __launch_bounds__(kThreads) void cache_write_kernel(const T* __restri
     const bool live = in && slot >= 0 && slot < c.slots;
     if (in && slot >= c.slots && err_flag) *err_flag = 1;
     const int first = blockIdx.y * rows_per, last = min(first + rows_per, 2 * c.heads);
-    for (int r = first; r < last; ++r) {
-        const bool is_v = r >= c.heads;
-        const int head = is_v ? r - c.heads : r;
-        float x[8];
-        load8((is_v ? v + t * v_stride : k + t * k_stride) + head * D + lane * 8, x);
-        store_row<D>(x, is_v ? c.v_codes : c.k_codes, is_v ? c.v_scales : c.k_scales,
-                     cache_row(live ? slot : 0, head, c), lane, live);
+    for (int r0 = first; r0 < last; r0 += kAtOnce) {
+        Raw<T> raw[kAtOnce];
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            const int r = min(r0 + i, last - 1);
+            raw[i].load((r >= c.heads ? v + t * v_stride + (r - c.heads) * D : k + t * k_stride + r * D) + lane * 8);
+        }
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            const int r = r0 + i;
+            if (r >= last) break;
+            const bool is_v = r >= c.heads;
+            float x[8];
+            raw[i].get(x);
+            store_row<D>(x, is_v ? c.v_codes : c.k_codes, is_v ? c.v_scales : c.k_scales,
+                         cache_row(live ? slot : 0, is_v ? r - c.heads : r, c), lane, live);
+        }
     }
 }
 
@@ -169,72 +211,80 @@ __global__ __launch_bounds__(kThreads) void norm_rope_write_kernel(
     float cs[8], sn[8];
     if (turns && first < heads + c.heads) {
         const float* row = cos_sin + (placed ? pos : 0) * rot;
-        if (kInterleaved) {
+        const int i0 = kInterleaved ? lane * 4 : high ? lane * 8 - rot / 2 : lane * 8;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                cs[i] = row[lane * 4 + i];
-                sn[i] = row[rot / 2 + lane * 4 + i];
-            }
-        } else {
-            const int i0 = high ? lane * 8 - rot / 2 : lane * 8;
+        for (int i = 0; i < (kInterleaved ? 4 : 8); i += 4) {
+            const f32x4 a = *reinterpret_cast<const f32x4*>(row + i0 + i);
+            const f32x4 b = *reinterpret_cast<const f32x4*>(row + rot / 2 + i0 + i);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                cs[i] = row[i0 + i];
-                sn[i] = row[rot / 2 + i0 + i];
-                if (!high) sn[i] = -sn[i];
+            for (int e = 0; e < 4; ++e) {
+                cs[i + e] = a[e];
+                sn[i + e] = kInterleaved || high ? b[e] : -b[e];
             }
         }
     }
-    for (int r = first; r < last; ++r) {
-        float x[8];
-        load8(qkv + t * stride + (int64_t)r * D + lane * 8, x);
-        const int kind = r < heads ? 0 : r < heads + c.heads ? 1 : 2;
-        if (kind < 2) {
-            const T* weight = kind == 0 ? q_weight : k_weight;
-            if (weight) {
-                float w[8], ss = 0.0f;
-                load8(weight + lane * 8, w);
+    float wq[8], wk[8];   // the norms' weights
+    if (q_weight && first < heads) load_row(q_weight + lane * 8, wq);
+    if (k_weight && first < heads + c.heads && last > heads) load_row(k_weight + lane * 8, wk);
+    const T* row = qkv + t * stride + lane * 8;
+    for (int r0 = first; r0 < last; r0 += kAtOnce) {
+        Raw<T> raw[kAtOnce];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) ss += x[i] * x[i];
-                ss = group_sum<kLanes>(ss);
-                if (ss > 0x1p-80f && ss < 0x1p100f) {
-                    const float f = 1.0f / sqrtf(ss * (1.0f / D) + eps);
+        for (int i = 0; i < kAtOnce; ++i) raw[i].load(row + (int64_t)min(r0 + i, last - 1) * D);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] = x[i] * f * w[i];
-                } else {
-                    norm_wide<kLanes>(x, w, eps);   // squares past the fp32 range, or nearly so: the whole group alike
-                }
-            }
-            if (kInterleaved) {
-                if (turns) {
+        for (int n = 0; n < kAtOnce; ++n) {
+            const int r = r0 + n;
+            if (r >= last) break;
+            float x[8];
+            raw[n].get(x);
+            const int kind = r < heads ? 0 : r < heads + c.heads ? 1 : 2;
+            if (kind < 2) {
+                if (kind == 0 ? q_weight != nullptr : k_weight != nullptr) {
+                    float w[8], ss = 0.0f;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float a = x[2 * i], b = x[2 * i + 1];
-                        x[2 * i] = a * cs[i] - b * sn[i];
-                        x[2 * i + 1] = b * cs[i] + a * sn[i];
+                    for (int i = 0; i < 8; ++i) w[i] = kind == 0 ? wq[i] : wk[i];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) ss += x[i] * x[i];
+                    ss = group_sum<kLanes>(ss);
+                    if (ss > 0x1p-80f && ss < 0x1p100f) {
+                        const float f = __builtin_amdgcn_rsqf(ss * (1.0f / D) + eps);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) x[i] = x[i] * f * w[i];
+                    } else {
+                        norm_wide<kLanes>(x, w, eps);   // squares past the fp32 range, or nearly so: the whole group alike
                     }
                 }
-            } else {
-                float o[8];   // every lane takes part in the exchange, those past rot for nothing
+                if (kInterleaved) {
+                    if (turns) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] = __shfl(x[i], partner & (kWave - 1), kWave);
-                if (turns) {
+                        for (int i = 0; i < 4; ++i) {
+                            const float a = x[2 * i], b = x[2 * i + 1];
+                            x[2 * i] = a * cs[i] - b * sn[i];
+                            x[2 * i + 1] = b * cs[i] + a * sn[i];
+                        }
+                    }
+                } else {
+                    float o[8];   // every lane takes part in the exchange, those past rot for nothing
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] = x[i] * cs[i] + o[i] * sn[i];
+                    for (int i = 0; i < 8; ++i) o[i] = __shfl(x[i], partner & (kWave - 1), kWave);
+                    if (turns) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) x[i] = x[i] * cs[i] + o[i] * sn[i];
+                    }
                 }
             }
-        }
-        if (kind == 0) {
-            if (in) {
-                uint4 o = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                                     pack_bf16x2(x[6], x[7]));
-                if (!placed) o = make_uint4(0, 0, 0, 0);
-                *reinterpret_cast<uint4*>(q_out + (t * heads + r) * D + lane * 8) = o;
+            if (kind == 0) {
+                if (in) {
+                    uint4 o = make_uint4(round_bf16x2(x[0], x[1]), round_bf16x2(x[2], x[3]), round_bf16x2(x[4], x[5]),
+                                         round_bf16x2(x[6], x[7]));
+                    if (!placed) o = make_uint4(0, 0, 0, 0);
+                    store_nt16(q_out + (t * heads + r) * D + lane * 8, o.x, o.y, o.z, o.w);
+                }
+            } else {
+                const int head = kind == 1 ? r - heads : r - heads - c.heads;
+                store_row<D>(x, kind == 1 ? c.k_codes : c.v_codes, kind == 1 ? c.k_scales : c.v_scales,
+                             cache_row(live ? slot : 0, head, c), lane, live);
             }
-        } else {
-            const int head = kind == 1 ? r - heads : r - heads - c.heads;
-            store_row<D>(x, kind == 1 ? c.k_codes : c.v_codes, kind == 1 ? c.k_scales : c.v_scales,
-                         cache_row(live ? slot : 0, head, c), lane, live);
         }
     }
 }
