@@ -885,26 +885,31 @@ __global__ __launch_bounds__(kW * kWave, 2) void attention_split_kernel(Attentio
 }
 
 constexpr int kJoinWaves = 4;
+constexpr int kSpreadRecords = 64;   // 8 segments of 64 parts: 4.5 us instead of 7; 520 of 3: 3 more
 
-// Joins the parts of a segment, a wave a row: two parts at a time, half a wave each, sixteen of them on their way.
-template <int D, int NQ>
+// Joins the parts of a segment: a wave a row, or, where there are few segments and so many parts of each, a workgroup a row
+// (kSpread). Two parts at a time, half a wave each, sixteen of them on their way.
+template <int D, int NQ, bool kSpread>
 __global__ __launch_bounds__(kJoinWaves * kWave) void attention_join_kernel(Attention a, CacheView c, const float* parts,
-                                                                        const Record* records, Divisor by) {
+                                                                            const Record* records, Divisor by) {
     constexpr int kRows = 16 * NQ;
     constexpr int kEach = D / 32;
+    __shared__ float sums[kSpread ? kJoinWaves : 1][kEach + 1][32];
     const Record r = records[blockIdx.x];
     if (r.from == r.to) return;
     const int lane = threadIdx.x % kWave, half = lane / 32, place = lane % 32;
+    const int wave = uniform(threadIdx.x / kWave);
     const int count = r.to - r.from + 1;
     const int group = a.heads / c.heads;
-    for (int at = blockIdx.y * kJoinWaves + threadIdx.x / kWave; at < r.rows; at += gridDim.y * kJoinWaves) {
+    constexpr int kStride = kSpread ? 1 : kJoinWaves;
+    for (int at = blockIdx.y * kStride + (kSpread ? 0 : wave); at < r.rows; at += gridDim.y * kStride) {
         auto part_of = [&](int i) { return parts + (2 * (size_t)(r.from + i) + (i == 0 ? 1 : 0)) * part_floats<D, NQ>(); };
         float m = -INFINITY;
         for (int i = lane; i < count; i += kWave) m = fmaxf(m, part_of(i)[(size_t)kRows * D + 2 * at]);
         for (int x = 32; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor(m, x, kWave));
         const float m0 = finite_or_zero(m);
         float total = 0.0f, o[kEach] = {};
-        for (int i0 = 0; i0 < count; i0 += 16) {
+        for (int i0 = kSpread ? 16 * wave : 0; i0 < count; i0 += kSpread ? 16 * kJoinWaves : 16) {
             float v[8][kEach], ml[8][2];
 #pragma unroll
             for (int b = 0; b < 8; ++b) {
@@ -927,10 +932,28 @@ __global__ __launch_bounds__(kJoinWaves * kWave) void attention_join_kernel(Atte
         total += __shfl_xor(total, 32, kWave);
 #pragma unroll
         for (int e = 0; e < kEach; ++e) o[e] += __shfl_xor(o[e], 32, kWave);
+        if constexpr (kSpread) {
+            __syncthreads();   // the row before is done with
+            if (half == 0) {
+#pragma unroll
+                for (int e = 0; e < kEach; ++e) sums[wave][e][place] = o[e];
+                sums[wave][kEach][place] = total;
+            }
+            __syncthreads();
+            total = 0.0f;
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) o[e] = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kJoinWaves; ++w) {
+                total += sums[w][kEach][place];
+#pragma unroll
+                for (int e = 0; e < kEach; ++e) o[e] += sums[w][e][place];
+            }
+        }
         const int row = r.row0 + at, q = divide(row, by);
         const int h = r.head * group + (row - q * group);
         const float f = last_factor(m, total, a.sinks, h);
-        if (half == 0) {
+        if (half == 0 && (!kSpread || wave == 0)) {
             uint16_t* out = a.out + ((int64_t)(r.first + q) * a.heads + h) * D + place * kEach;
             if constexpr (kEach == 4)
                 *reinterpret_cast<uint2*>(out) = make_uint2(pack_weights(o[0] * f, o[1] * f), pack_weights(o[2] * f, o[3] * f));
@@ -1036,15 +1059,18 @@ template <int D, int NQ, int kW>
 hipError_t split_form(const Attention& a, const CacheView& c, const Form& f, void* workspace, hipStream_t stream) {
     Record* records = f.kind == kSplitForm ? static_cast<Record*>(workspace) : nullptr;
     float* parts = reinterpret_cast<float*>(records + f.records());
-    int unit_bits = f.kind == kSplitForm ? 7 : 30;   // four steps, more where the number of units would not fit 32 bits
+    int unit_bits = f.kind == kSplitForm ? 5 : 30;   // one step, more where the number of units would not fit 32 bits
     while (f.segments > ((int64_t)1 << 30) / (((a.table_width << c.page_bits) >> unit_bits) + 2)) ++unit_bits;
     attention_split_kernel<D, NQ, kW><<<f.workers, kW * kWave, 0, stream>>>(a, c, parts, records, f.workers, unit_bits,
                                                                             f.records(),
                                                                             records && f.segments <= f.workers,
                                                                             divisor_of(a.heads / c.heads));
     if (hipError_t e = hipGetLastError(); e != hipSuccess || !records) return e;
-    attention_join_kernel<D, NQ><<<dim3(f.records(), f.join_rows), kJoinWaves * kWave, 0, stream>>>(a, c, parts, records,
-                                                                                             divisor_of(a.heads / c.heads));
+    const Divisor by = divisor_of(a.heads / c.heads);
+    if (f.records() <= kSpreadRecords)
+        attention_join_kernel<D, NQ, true><<<dim3(f.records(), 16 * NQ), kJoinWaves * kWave, 0, stream>>>(a, c, parts, records, by);
+    else
+        attention_join_kernel<D, NQ, false><<<dim3(f.records(), f.join_rows), kJoinWaves * kWave, 0, stream>>>(a, c, parts, records, by);
     return hipGetLastError();
 }
 
