@@ -1112,3 +1112,11 @@ hipError_t launch_attention(const Attention& a, const CacheView& c, void* worksp
 }
 
 }  // namespace e2m1
+
+extern "C" int e2m1_mxfp4_attention_form(int64_t tokens, int64_t seqs, int64_t heads, int64_t kv_heads, int64_t head_dim,
+                                         int64_t length) {
+    const e2m1::Form f = e2m1::form_of(tokens, seqs, heads, kv_heads, head_dim, length);
+    const bool by_worker = f.kind == e2m1::kSplitForm && f.segments > f.workers;
+    const bool spread = f.kind == e2m1::kSplitForm && f.records() <= e2m1::kSpreadRecords;
+    return 1000 * (spread ? 2 : by_worker ? 1 : 0) + 100 * f.kind + 10 * f.nq + f.waves;
+}

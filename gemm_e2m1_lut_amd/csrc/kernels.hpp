@@ -138,3 +138,9 @@ hipError_t launch_moe(const uint16_t* x, const uint8_t* w13, const uint8_t* w13s
 // rows of whole 128-byte lines or in the other one, one more for 256 x 256 tiles whose last round is halved. Host only;
 // exported for the tests, which have to reach every form.
 extern "C" int e2m1_int8_gemm_variant(int64_t m, int64_t n, int64_t k, int whole_lines, int cus);
+
+// Which form mxfp4_attention takes for rows that see up to `length` tokens: 10 * tiles of 16 rows a wave + waves of a
+// worker, + 100 for whole segments, + 200 for cut ones, + 1000 where their joins go by worker, + 2000 where a workgroup
+// joins a row. Host only; exported for the tests, which have to reach every form.
+extern "C" int e2m1_mxfp4_attention_form(int64_t tokens, int64_t seqs, int64_t heads, int64_t kv_heads, int64_t head_dim,
+                                         int64_t length);

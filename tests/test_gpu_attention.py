@@ -1,6 +1,8 @@
 """GPU parity of mxfp4_attention against a 64-bit softmax over the cache's values (bounds derived in cache_ref)."""
 from __future__ import annotations
 
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -118,6 +120,68 @@ def test_without_a_mask(gpu, lens):
     r = np.random.default_rng(3)
     run(gpu, Case(LENS[lens], 8, 2, 128, 16, 1), causal=False)
     run(gpu, Case(LENS[lens], 16, 2, 64, 32, 2), causal=False, sinks=r.standard_normal(16).astype(np.float32))
+
+
+def ragged(seed, seqs, most, queries):
+    r = np.random.default_rng(seed)
+    return [(int(r.integers(0, queries + 1)) if i else queries, int(r.integers(1, most + 1))) for i in range(seqs)]
+
+
+# (form, heads, kv heads, head dim, page, sequences, table's extra pages)
+FORMS = [
+    (10, 8, 2, 128, 16, [(90, 90), (70, 70), (85, 85)], 0), (10, 16, 4, 64, 64, [(200, 300), (1, 5), (90, 90)], 0),
+    (20, 32, 8, 128, 64, [(1500, 1500), (600, 700), (1, 900), (0, 8)], 0), (30, 64, 16, 64, 64, [(900, 900), (640, 700)], 0),
+    (118, 8, 2, 128, 16, ragged(1, 7, 900, 1), 0), (118, 8, 2, 64, 16, ragged(2, 20, 700, 2), 0),
+    (128, 16, 2, 128, 32, ragged(3, 5, 600, 4), 0), (128, 16, 2, 64, 32, ragged(4, 12, 600, 4), 0),
+    (114, 32, 8, 128, 16, ragged(5, 60, 300, 1), 0), (114, 16, 8, 64, 64, ragged(6, 50, 300, 2), 0),
+    (124, 64, 8, 128, 16, ragged(7, 24, 200, 4), 0), (111, 32, 8, 128, 16, ragged(8, 150, 90, 1), 0),
+    (111, 16, 8, 64, 16, ragged(9, 90, 60, 3), 0), (121, 64, 8, 64, 16, ragged(10, 70, 40, 4), 0),
+    (211, 16, 8, 128, 16, ragged(11, 160, 700, 1), 0), (211, 16, 8, 64, 64, ragged(12, 80, 500, 2), 0),
+    (1211, 16, 8, 128, 16, ragged(13, 600, 150, 1), 40), (1211, 32, 8, 64, 16, ragged(14, 600, 100, 1), 40),
+    (2214, 8, 2, 128, 64, ragged(15, 3, 5000, 2), 0), (2214, 8, 2, 64, 16, ragged(16, 4, 3000, 4), 0),
+    (214, 8, 4, 128, 16, ragged(17, 40, 2500, 1), 0), (224, 16, 4, 128, 16, ragged(18, 20, 2500, 8), 0),
+    (224, 16, 4, 64, 64, ragged(19, 24, 2500, 8), 0), (2224, 16, 2, 128, 16, [(30, 4000), (5, 2000)], 0),
+    (2224, 16, 2, 64, 16, [(9, 4000), (0, 9), (12, 2100)], 0), (1224, 32, 8, 128, 64, [(500, 700), (99, 2600)], 0),
+    (1224, 64, 8, 64, 64, [(300, 2500)], 0),
+]
+
+
+@pytest.mark.parametrize("form,heads,kv,dim,page,lens,wide", FORMS, ids=lambda v: str(v) if isinstance(v, int) else None)
+def test_every_form(gpu, form, heads, kv, dim, page, lens, wide):
+    """Each form that a call can take, on ragged sequences, with a mask and without, a window, sinks and a missing page."""
+    say(f"attention: form {form}, {heads} / {kv} heads of {dim}, {len(lens)} sequences")
+    case = Case(lens, heads, kv, dim, page, form + dim, wide=wide)
+    width = case.table.shape[1] * page
+    choose = gpu.load_library().e2m1_mxfp4_attention_form
+    choose.argtypes = [ctypes.c_int64] * 6
+    assert choose(case.tokens, len(lens), heads, kv, dim, width) == form
+    r = np.random.default_rng(form)
+    sinks = (2 * r.standard_normal(heads)).astype(np.float32)
+    run(gpu, case)
+    run(gpu, case, causal=False, sinks=sinks)
+    run(gpu, case, window=2**30, sinks=sinks)      # as wide as it likes: the same form
+    run(gpu, case, window=77)
+    d = case.device()
+    s = max((i for i in range(len(lens)) if lens[i][0]), key=lambda i: lens[i][1])
+    flag = torch.zeros(1, dtype=torch.int32, device=DEV)
+    size = gpu.mxfp4_attention_workspace_size(case.tokens, len(lens), heads, kv, dim)
+    memory = torch.full((size + 4096,), 0xA5, dtype=torch.uint8, device=DEV)
+    clean = gpu.mxfp4_attention(**d, workspace=memory[:size])
+    assert (memory[size:] == 0xA5).all()
+    assert torch.equal(clean, gpu.mxfp4_attention(**d))
+    d["page_table"][s, 0] = 2**30
+    out = gpu.mxfp4_attention(**d, err_flag=flag)
+    assert flag.item() == 1
+    a, b = case.offsets[s], case.offsets[s + 1]
+    assert torch.equal(out[:a], clean[:a]) and torch.equal(out[b:], clean[b:])
+    n, length = lens[s]
+    k, v = case.rows_of(s)
+    pos = length - n
+    for i in sorted({0, n - 1}):     # without the first page's tokens
+        if n and pos + i >= page:
+            want, bound = ref.attention(case.q[a + i:a + i + 1].double().numpy(), k[page:pos + i + 1], v[page:pos + i + 1],
+                                        dim ** -0.5, True, 0)
+            assert (np.abs(out[a + i:a + i + 1].double().cpu().numpy() - want) <= bound).all()
 
 
 @pytest.mark.parametrize("group", [1, 2, 3, 4, 5, 7, 8, 12, 16, 17, 32, 33, 64])
@@ -342,6 +406,21 @@ def test_the_same_bits(gpu, lens):
         assert torch.equal(out, want)
 
 
+def test_two_calls_at_once(gpu):
+    """Calls on two streams with workspaces of their own, and outputs and workspaces that the calls allocate."""
+    say("attention: two streams at once")
+    cases = [Case(LENS["long"], 8, 2, 128, 16, 28), Case(ragged(29, 40, 900, 2), 16, 8, 64, 16, 29)]
+    devs = [c.device() for c in cases]
+    want = [gpu.mxfp4_attention(**d) for d in devs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(4):
+        got = [gpu.mxfp4_attention(**d, stream=s) for _ in range(3) for d, s in zip(devs, streams)]
+        torch.cuda.synchronize()
+        for i, g in enumerate(got):
+            assert torch.equal(g, want[i % 2])
+
+
 def test_graphs_that_share_a_workspace(gpu):
     """Two captured calls with one workspace, replayed in turn with eager calls between."""
     say("attention: graphs")
@@ -367,7 +446,7 @@ def test_graphs_that_share_a_workspace(gpu):
         torch.cuda.synchronize()
         for o, w in zip(outs, want):
             assert torch.equal(o, w), rep
-        gpu.mxfp4_attention(**devs[rep % 3], out=outs[0][:0] if False else torch.empty_like(want[rep % 3]), workspace=ws)
+        gpu.mxfp4_attention(**devs[rep % 3], out=torch.empty_like(want[rep % 3]), workspace=ws)
     # lengths are read at each replay, as a decoding loop needs them
     devs[0]["kv_lens"] -= 1
     graphs[0].replay()
