@@ -1059,7 +1059,8 @@ template <int D, int NQ, int kW>
 hipError_t split_form(const Attention& a, const CacheView& c, const Form& f, void* workspace, hipStream_t stream) {
     Record* records = f.kind == kSplitForm ? static_cast<Record*>(workspace) : nullptr;
     float* parts = reinterpret_cast<float*>(records + f.records());
-    int unit_bits = f.kind == kSplitForm ? 5 : 30;   // one step, more where the number of units would not fit 32 bits
+    // one step, more where the number of units would not fit 32 bits: the segments of 2^28 rows are fewer than 2^29
+    int unit_bits = f.kind == kSplitForm ? 5 : 30;
     while (f.segments > ((int64_t)1 << 30) / (((a.table_width << c.page_bits) >> unit_bits) + 2)) ++unit_bits;
     attention_split_kernel<D, NQ, kW><<<f.workers, kW * kWave, 0, stream>>>(a, c, parts, records, f.workers, unit_bits,
                                                                             f.records(),
@@ -1085,7 +1086,9 @@ template <int D, int NQ>
 hipError_t rows_form(const Attention& a, const CacheView& c, hipStream_t stream) {
     const int round = device_cu_count() > c.heads ? device_cu_count() / c.heads : 1;
     const int64_t tiles = most_tiles(a.tokens, a.seqs, a.heads / c.heads, 16 * NQ * kRowWaves);
-    const int64_t grid = (tiles + round - 1) / round * round * c.heads;   // whole rounds: see the kernel's order
+    // whole rounds: see the kernel's order. Of 2^28 rows, with more than 64 a sequence: under 2^24 workgroups (a launch may
+    // have 2^32 threads), at most 2^28 / 64 + 2^28 / 33 + 4096
+    const int64_t grid = (tiles + round - 1) / round * round * c.heads;
     attention_rows_kernel<D, NQ><<<(unsigned)grid, kRowWaves * kWave, 0, stream>>>(a, c, round, divisor_of(a.heads / c.heads));
     return hipGetLastError();
 }

@@ -320,7 +320,7 @@ int int8_gemm(const int8_t* x, const float* x_scale, const int8_t* w, const floa
 #define E2M1_CACHE_MAX_HEADS 4096
 #define E2M1_CACHE_MAX_PAGE 65536
 #define E2M1_CACHE_MAX_TOKENS ((int64_t)1 << 26)
-#define E2M1_ATTENTION_MAX_ROWS ((int64_t)1 << 29)   /* tokens * heads of one mxfp4_attention call */
+#define E2M1_ATTENTION_MAX_ROWS ((int64_t)1 << 28)   /* tokens * heads of one mxfp4_attention call */
 #define E2M1_ATTENTION_MAX_LENGTH ((int64_t)1 << 30) /* tokens its page table has room for, a sequence */
 
 /*

@@ -176,12 +176,41 @@ def test_attention_workspace(lib):
     no = ctypes.c_size_t(-1).value
     assert size(0, 3, 8, 8, 64) == 0 and size(3, 0, 8, 8, 64) == 0
     assert size(1, 1, 9, 8, 64) == no and size(1, 1, 8, 8, 32) == no and size(-1, 1, 8, 8, 64) == no
+    assert size(2**22, 2**22, 64, 64, 64) < 1 << 32 and size(2**22 + 1, 1, 64, 64, 64) == no
+    assert size(2**16, 2**16, 4096, 1, 128) < 1 << 32 and size(2**16 + 1, 2**16, 4096, 1, 128) == no
     need = size(4, 2, 32, 8, 128)
     assert need < 1 << 32
     if need:
         assert attend(lib, ws_bytes=need - 1) == E_WS
         assert attend(lib, ws=NULL) == E_WS
         assert attend(lib, ws=P(0x1000010)) == E_ALIGN
+
+
+@pytest.mark.parametrize("group", [1, 2, 3, 16, 17, 32, 33, 64, 65, 100, 4096])
+@pytest.mark.parametrize("queries", [1, 1.001, 2, 2.001, 3, 5, 64, 1e6])
+def test_attention_launches_fit(lib, group, queries):
+    """The most rows a call may have: its grid has fewer than 2^32 threads, the units of the cut form have a size."""
+    form = lib.e2m1_mxfp4_attention_form
+    form.argtypes = [ctypes.c_int64] * 6
+    for kv in (1, 8, 64):
+        heads = group * kv
+        if heads > 4096:
+            continue
+        tokens = 2**28 // heads
+        seqs = max(1, int(tokens / queries))
+        for dim in (64, 128):
+            for length in (1, 100, 2**30):
+                f = form(tokens, seqs, heads, kv, dim, length)
+                kind, nq = f // 100 % 10, f // 10 % 10
+                bound = (tokens * group // (16 * nq) + min(seqs, tokens)) * kv
+                if kind == 0:
+                    tiles = tokens * group // (64 * nq) + min(seqs, tokens)
+                    each = max(1, 256 // kv)
+                    assert -(-tiles // each) * each * kv * 256 < 2**32
+                elif kind == 1:
+                    assert bound * 512 < 2**32
+                else:
+                    assert bound <= 2**29
 
 
 def test_binding_checks_its_tensors():
