@@ -78,6 +78,14 @@ __device__ __forceinline__ int divide(int n, const Divisor& d) {
 }
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// The same number, but nothing that is made of it is made earlier: addresses of results, which would be kept in registers (and
+// then out of them) through all steps. Two tiles of 128 channels: 50 spilled registers, 7 us a launch.
+__device__ __forceinline__ int not_before(int v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
 __device__ __forceinline__ float exp2_raw(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // ------------------------------------------------------------------- plan --
@@ -745,15 +753,15 @@ __global__ __launch_bounds__(kW * kWave, 2) void attention_split_kernel(Attentio
     __shared__ __attribute__((aligned(16))) float lo_m[kW][16];
     __shared__ f32x4 lo_l[kW][4];
     const int lane = threadIdx.x % kWave, wave = uniform(threadIdx.x / kWave);
-    // neighbours in the order of work on the same XCD, whose L2 then holds what they share
-    const int per_xcd = workers / 8;
-    const int id = (int)blockIdx.x < per_xcd * 8 ? (int)(blockIdx.x % 8) * per_xcd + (int)blockIdx.x / 8 : (int)blockIdx.x;
     const int group = a.heads / c.heads;
-    const Lane<D> ln(c, lane);
 
     auto segments = [&](const Span& s) { return tiles_of(s, group, kRows) * c.heads; };
     auto weight = [&](const Span& s) { return segments(s) * units_of(a, s, unit_bits); };
     const Plan plan(a, c.page_bits, lane, weight);
+    // neighbours in the order of work on the same XCD, whose L2 then holds what they share; of more workgroups than segments the
+    // first ones have work, so that all XCDs do
+    const int per_xcd = (records ? workers : (int)min(plan.total, (uint32_t)workers)) / 8;
+    const int id = (int)blockIdx.x < per_xcd * 8 ? (int)(blockIdx.x % 8) * per_xcd + (int)blockIdx.x / 8 : (int)blockIdx.x;
     if (!plan.ok) {
         if (threadIdx.x == 0 && id < record_count) records[id].from = records[id].to = 0;
         return;
@@ -795,7 +803,8 @@ __global__ __launch_bounds__(kW * kWave, 2) void attention_split_kernel(Attentio
         const int origin = first_seen(a, s, 0) / kStep, steps = unit_bits - 5;
         Sums<D, NQ> sums;
         run_steps<D, NQ>(a, c, a.page_table + seq * a.table_width, s, head, group, by, row0,
-                                          origin + (u0 << steps) + wave, origin + (u1 << steps), kW, sums, ln);
+                         origin + (u0 << steps) + wave, origin + (u1 << steps), kW, sums, Lane<D>(c, lane));
+        const Lane<D> ln(c, not_before(lane));
         const bool whole = u0 == 0 && u1 == (int)units;
         float* part = parts + (2 * (size_t)id + (u0 > 0 ? 0 : 1)) * part_floats<D, NQ>();
         const int rows_left = s.n * group - row0;
@@ -834,8 +843,8 @@ __global__ __launch_bounds__(kW * kWave, 2) void attention_split_kernel(Attentio
             } else {
                 __syncthreads();
 #pragma unroll
-                for (int j = 0; j < NJ; ++j) lo_o[wave][j][lane] = sums.o[i][j];
-                if (lane < 16) lo_m[wave][lane] = sums.top(i);
+                for (int j = 0; j < NJ; ++j) lo_o[wave][j][ln.lane] = sums.o[i][j];
+                if (ln.lane < 16) lo_m[wave][ln.lane] = sums.top(i);
                 if (ln.n == 0) lo_l[wave][ln.g] = sums.l[i];
                 __syncthreads();
                 // wave w joins channels [w kN, ..) of every run of NJ, for this lane's four rows
@@ -857,7 +866,7 @@ __global__ __launch_bounds__(kW * kWave, 2) void attention_split_kernel(Attentio
                         for (int r = 0; r < 4; ++r) f[r] = exp2_raw(v[r] - finite_or_zero(m[r]));
                         total += f * lo_l[w][ln.g];
 #pragma unroll
-                        for (int j = 0; j < kN; ++j) o[j] += f * lo_o[w][wave * kN + j][lane];
+                        for (int j = 0; j < kN; ++j) o[j] += f * lo_o[w][wave * kN + j][ln.lane];
                     }
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
@@ -969,7 +978,6 @@ __global__ __launch_bounds__(kRowWaves * kWave, 2) void attention_rows_kernel(At
     constexpr int kRows = 16 * NQ;
     const int lane = threadIdx.x % kWave, wave = uniform(threadIdx.x / kWave);
     const int group = a.heads / c.heads;
-    const Lane<D> ln(c, lane);
     auto weight = [&](const Span& s) { return tiles_of(s, group, kRows * kRowWaves); };
     const Plan plan(a, c.page_bits, lane, weight);
     // rounds of `round` tile groups, one a compute unit and head: every other one backwards, so that a unit that had the
@@ -986,7 +994,8 @@ __global__ __launch_bounds__(kRowWaves * kWave, 2) void attention_rows_kernel(At
     const int rows_left = s.n * group - row0;
     if (rows_left <= 0) return;
     Sums<D, NQ> sums;
-    run_steps<D, NQ>(a, c, a.page_table + seq * a.table_width, s, head, group, by, row0, 0, kFarRight, 1, sums, ln);
+    run_steps<D, NQ>(a, c, a.page_table + seq * a.table_width, s, head, group, by, row0, 0, kFarRight, 1, sums, Lane<D>(c, lane));
+    const Lane<D> ln(c, not_before(lane));
 #pragma unroll
     for (int i = 0; i < NQ; ++i)
 #pragma unroll
@@ -1010,7 +1019,10 @@ int64_t most_tiles(int64_t tokens, int64_t seqs, int64_t group, int64_t rows) {
     return tokens * group / rows + (seqs < tokens ? seqs : tokens);
 }
 
-// How a call is worked on, from what the host knows: numbers of rows and sequences, and how many tokens a row can see.
+// How a call is worked on, from what the host knows: the numbers of rows and sequences, and how many tokens a row can see. The
+// times below are of 32 query heads over 8 of 128 channels, in us; n: segments of 16 rows. The choice was taken from 70 calls
+// (heads of 64 and 128 channels, 1 to 2048 queries, 1 to 256 sequences of 64 to 131072 tokens) timed in every form: it is 0.2 %
+// above the fastest form on the mean, 14 % at most.
 enum Kind { kRowsForm, kWholeForm, kSplitForm };
 struct Form {
     Kind kind;
@@ -1022,9 +1034,11 @@ struct Form {
     int records() const { return kind == kSplitForm ? (int)(segments < workers ? segments : workers) : 0; }
 };
 
-Form split_of(int64_t tokens, int64_t seqs, int64_t heads, int64_t kv_heads, int64_t mean) {
-    const int64_t group = heads / kv_heads, cus = device_cu_count();
-    const int nq = mean > 16 ? 2 : 1;
+// Equal shares. Waves of their own where there are segments enough that a worker's share is about one (64 ragged sequences of
+// up to 8192: 69.5 against 77.8 in workgroups of four), else workgroups of four, with a quarter of the parts to join (four
+// queries after 131072 tokens: 36.2 against 45.3).
+Form split_of(int64_t tokens, int64_t seqs, int64_t heads, int64_t kv_heads, int nq) {
+    const int64_t group = heads / kv_heads, cus = device_cu_count(), mean = (tokens + seqs - 1) / seqs * group;
     const int64_t segments = most_tiles(tokens, seqs, group, 16 * nq) * kv_heads;
     const int waves = segments >= cus / 2 && nq == 1 ? 1 : 4;
     return {kSplitForm, nq, waves, (int)(8 / waves * cus), segments,
@@ -1034,24 +1048,44 @@ Form split_of(int64_t tokens, int64_t seqs, int64_t heads, int64_t kv_heads, int
 Form form_of(int64_t tokens, int64_t seqs, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t length) {
     const int64_t group = heads / kv_heads, cus = device_cu_count();
     const int64_t queries = (tokens + seqs - 1) / seqs, mean = queries * group;
+    const int64_t n = seqs * ((mean + 15) / 16) * kv_heads;   // if the sequences have alike many queries
+    const int64_t steps = (length + kStep - 1) / kStep;
     const int wide = head_dim == 128 ? 2 : 3;
-    if (mean > 64) {
-        if (most_tiles(tokens, seqs, group, 16 * wide * kRowWaves) * kv_heads >= 2 * cus) return {kRowsForm, wide, 0, 0, 0, 0};
-        if (most_tiles(tokens, seqs, group, 16 * kRowWaves) * kv_heads >= cus / 8 && length <= 4 * queries)
-            return {kRowsForm, 1, 0, 0, 0, 0};
-    }
-    Form f = split_of(tokens, seqs, heads, kv_heads, mean);
-    // Whole segments save the second launch and pay in longer chains of steps: 6.5 us and 1.1 a step for each round of workers
-    // against 12.4 and 1.1 a step of an equal share (one token of 777: 10.7 against 12.7; 16 of 2048: 16.5 against 17.2;
-    // of 2048 alone: 15.4 against 12.4).
-    const int waves = f.segments <= cus ? 8 : f.segments <= 2 * cus ? 4 : 1;
-    const int64_t steps = (length + kStep * waves - 1) / (kStep * waves);
-    const int64_t rounds = (f.segments * waves + 8 * cus - 1) / (8 * cus);
-    if (steps <= 8 && f.segments < 1 << 20 && rounds * (65 + 11 * steps) < 124 + 11 * f.segments * steps * waves / (8 * cus)) {
+    // Rows enough to fill the chip twice with two or three tiles a wave: a prompt of 2048 56.7 (one tile a wave 61.5, shares
+    // 95), 2048 tokens after 6144 242 (322, 304). With 64 rows a sequence or less half of a workgroup has none (16 queries of
+    // 256 sequences: 150, one tile 135).
+    if (mean > 64 && most_tiles(tokens, seqs, group, 16 * wide * kRowWaves) * kv_heads >= 2 * cus)
+        return {kRowsForm, wide, 0, 0, 0, 0};
+    // One tile a wave. Few segments and tokens: one token of 64 sequences of 192 8.4 (four waves a segment 10.2), of 16: 7.6
+    // (7.6). Many of both, as long as the chain of steps is short beside the number of tiles: 1024 tokens after 3072 88
+    // (shares 92.7), 512 after 1700 42.5 (35.8).
+    if (n <= 2 * cus ? steps <= (n <= cus ? 5 : 12) : mean >= 48 && 16 * steps <= n) return {kRowsForm, 1, 0, 0, 0, 0};
+    // Whole segments save the join, its launch and the parts' way through memory. With no more than two a compute unit all
+    // are under way at once: one token after 1000 in 64 sequences 17.7 (shares 28.1), of 2048 in 16 15.5 in eight waves (16.2
+    // in four, 16.9), of 2048 alone 14.2 (11.1: its eight segments leave the chip idle, which the estimates say, in 0.1 us). A
+    // segment longer than the others keeps the call waiting, so chains longer than 32 steps are cut (64 sequences of 4352:
+    // 63.5, whole 57). Of more segments, each a wave's: one token after 384 in 200 sequences 20.1 (30.8), 8 queries after 1000
+    // in 256 84.7 (92.7).
+    Form f = split_of(tokens, seqs, heads, kv_heads, 1);
+    auto whole = [&](int waves) {
         f.kind = kWholeForm;
         f.waves = waves;
         f.workers = (int)f.segments;
+        return f;
+    };
+    if (n <= 2 * cus) {
+        const int waves = n <= cus && steps > 32 ? 8 : 4;
+        const int64_t chain = (steps + waves - 1) / waves;
+        const int64_t as_whole = waves == 8 ? 93 + 7 * chain : 66 + 6 * chain;
+        const int64_t as_shares = 110 + 50 * (n < 64 ? n : 64) / 64 + 7 * n * steps / (8 * cus);
+        if (chain <= 32 && as_whole < as_shares) return whole(waves);
+    } else if (mean < 48 && steps <= 32 && f.segments < 1 << 20) {
+        return whole(1);
     }
+    // Two tiles share their tokens' bytes, and pay for it once a worker, with more to set up and to join: 512 tokens after
+    // 15872 154 (one tile 201), 8 queries of 4 sequences of 16384 30.2 (27.5).
+    if (mean > 16 && seqs * ((mean + 31) / 32) * kv_heads * steps >= 9 * 8 * cus)
+        return split_of(tokens, seqs, heads, kv_heads, 2);
     return f;
 }
 
@@ -1076,18 +1110,11 @@ hipError_t split_form(const Attention& a, const CacheView& c, const Form& f, voi
 }
 
 template <int D, int NQ>
-hipError_t split_waves(const Attention& a, const CacheView& c, const Form& f, void* workspace, hipStream_t stream) {
-    if (f.waves == 1) return split_form<D, NQ, 1>(a, c, f, workspace, stream);
-    if (f.waves == 4) return split_form<D, NQ, 4>(a, c, f, workspace, stream);
-    return split_form<D, NQ, 8>(a, c, f, workspace, stream);
-}
-
-template <int D, int NQ>
 hipError_t rows_form(const Attention& a, const CacheView& c, hipStream_t stream) {
     const int round = device_cu_count() > c.heads ? device_cu_count() / c.heads : 1;
     const int64_t tiles = most_tiles(a.tokens, a.seqs, a.heads / c.heads, 16 * NQ * kRowWaves);
-    // whole rounds: see the kernel's order. Of 2^28 rows, with more than 64 a sequence: under 2^24 workgroups (a launch may
-    // have 2^32 threads), at most 2^28 / 64 + 2^28 / 33 + 4096
+    // whole rounds: see the kernel's order. Of 2^28 rows, with 48 or more a sequence: under 2^24 workgroups (a launch may
+    // have 2^32 threads), at most 2^28 / 64 + 2^28 / 24 + 4096
     const int64_t grid = (tiles + round - 1) / round * round * c.heads;
     attention_rows_kernel<D, NQ><<<(unsigned)grid, kRowWaves * kWave, 0, stream>>>(a, c, round, divisor_of(a.heads / c.heads));
     return hipGetLastError();
@@ -1099,7 +1126,10 @@ hipError_t attend(const Attention& a, const CacheView& c, void* workspace, hipSt
     const Form f = form_of(a.tokens, a.seqs, a.heads, c.heads, D, a.window > 0 && seen < most ? seen : most);
     if (f.kind == kRowsForm)
         return f.nq == 1 ? rows_form<D, 1>(a, c, stream) : rows_form<D, (D == 128 ? 2 : 3)>(a, c, stream);
-    return f.nq == 2 ? split_waves<D, 2>(a, c, f, workspace, stream) : split_waves<D, 1>(a, c, f, workspace, stream);
+    if (f.nq == 2) return split_form<D, 2, 4>(a, c, f, workspace, stream);
+    if (f.waves == 1) return split_form<D, 1, 1>(a, c, f, workspace, stream);
+    if (f.waves == 4) return split_form<D, 1, 4>(a, c, f, workspace, stream);
+    return split_form<D, 1, 8>(a, c, f, workspace, stream);
 }
 
 }  // namespace

@@ -129,20 +129,21 @@ def ragged(seed, seqs, most, queries):
 
 # (form, heads, kv heads, head dim, page, sequences, table's extra pages)
 FORMS = [
-    (10, 8, 2, 128, 16, [(90, 90), (70, 70), (85, 85)], 0), (10, 16, 4, 64, 64, [(200, 300), (1, 5), (90, 90)], 0),
+    (10, 32, 8, 128, 16, ragged(1, 40, 300, 1), 0), (10, 16, 8, 64, 64, ragged(2, 40, 300, 2), 0),
+    (10, 8, 2, 128, 16, [(150, 150), (70, 70), (380, 380)], 0), (10, 16, 4, 64, 64, [(260, 260), (90, 200), (170, 170)], 0),
     (20, 32, 8, 128, 64, [(1500, 1500), (600, 700), (1, 900), (0, 8)], 0), (30, 64, 16, 64, 64, [(900, 900), (640, 700)], 0),
-    (118, 8, 2, 128, 16, ragged(1, 7, 900, 1), 0), (118, 8, 2, 64, 16, ragged(2, 20, 700, 2), 0),
-    (128, 16, 2, 128, 32, ragged(3, 5, 600, 4), 0), (128, 16, 2, 64, 32, ragged(4, 12, 600, 4), 0),
-    (114, 32, 8, 128, 16, ragged(5, 60, 300, 1), 0), (114, 16, 8, 64, 64, ragged(6, 50, 300, 2), 0),
-    (124, 64, 8, 128, 16, ragged(7, 24, 200, 4), 0), (111, 32, 8, 128, 16, ragged(8, 150, 90, 1), 0),
-    (111, 16, 8, 64, 16, ragged(9, 90, 60, 3), 0), (121, 64, 8, 64, 16, ragged(10, 70, 40, 4), 0),
-    (211, 16, 8, 128, 16, ragged(11, 160, 700, 1), 0), (211, 16, 8, 64, 64, ragged(12, 80, 500, 2), 0),
-    (1211, 16, 8, 128, 16, ragged(13, 600, 150, 1), 40), (1211, 32, 8, 64, 16, ragged(14, 600, 100, 1), 40),
+    (118, 8, 2, 128, 16, ragged(3, 30, 1900, 1), 0), (118, 8, 2, 64, 16, ragged(4, 60, 1500, 4), 0),
+    (118, 16, 2, 128, 32, ragged(10, 16, 1800, 4), 0),
+    (114, 8, 2, 128, 16, ragged(5, 20, 900, 1), 0), (114, 16, 4, 64, 64, ragged(6, 30, 700, 8), 0),
+    (114, 32, 8, 64, 16, ragged(7, 50, 1200, 1), 0),
+    (111, 32, 8, 128, 16, ragged(8, 200, 90, 1), 0), (111, 16, 8, 64, 16, ragged(9, 90, 600, 3), 0),
+    (211, 16, 8, 128, 16, ragged(11, 160, 1300, 1), 0), (211, 16, 8, 64, 64, ragged(12, 80, 1100, 2), 0),
+    (1211, 16, 8, 128, 16, ragged(13, 600, 150, 1), 60), (1211, 32, 8, 64, 16, ragged(14, 600, 100, 1), 60),
     (2214, 8, 2, 128, 64, ragged(15, 3, 5000, 2), 0), (2214, 8, 2, 64, 16, ragged(16, 4, 3000, 4), 0),
-    (214, 8, 4, 128, 16, ragged(17, 40, 2500, 1), 0), (224, 16, 4, 128, 16, ragged(18, 20, 2500, 8), 0),
-    (224, 16, 4, 64, 64, ragged(19, 24, 2500, 8), 0), (2224, 16, 2, 128, 16, [(30, 4000), (5, 2000)], 0),
-    (2224, 16, 2, 64, 16, [(9, 4000), (0, 9), (12, 2100)], 0), (1224, 32, 8, 128, 64, [(500, 700), (99, 2600)], 0),
-    (1224, 64, 8, 64, 64, [(300, 2500)], 0),
+    (214, 8, 4, 128, 16, ragged(17, 40, 9000, 1), 0), (214, 8, 4, 64, 64, [(2, 9000)] * 20, 0),
+    (224, 16, 4, 128, 16, ragged(18, 20, 9000, 8), 0), (224, 16, 4, 64, 64, ragged(19, 24, 9000, 8), 0),
+    (2224, 16, 2, 128, 16, [(30, 32000), (5, 2000)], 0), (2224, 16, 2, 64, 16, [(14, 40000), (0, 9), (12, 2100)], 0),
+    (1224, 32, 8, 128, 64, [(600, 900), (99, 4000)], 0), (1224, 64, 8, 64, 64, [(300, 2500)], 0),
 ]
 
 
