@@ -40,7 +40,23 @@
 // weight, in the sum as in the product, and the errors of a row's weights are
 // independent: the result's own rounding is larger.
 // No LDS and no barrier in the loop: the bytes of a step are few (4352 for 32
-// tokens of 128 channels), and waves that share tokens find them in the L1.
+// tokens of 128 channels), waves that share tokens find them in the L1, and the
+// loads of the next step are on their way into a second set of registers (a ring
+// of steps in LDS, filled by direct-to-LDS loads: 397 us instead of 376 for packed
+// prompts, 75 instead of 71 for 64 ragged sequences; three or four sets of
+// registers: 80 to 91).
+//
+// Bounds. One token of many sequences: HBM, 304 MB (64 sequences of 512 to 8192
+// tokens) in 69 us, 4.4 TB/s; 64 of 16384 tokens 200 us, 5.7 TB/s. Prompts: issue,
+// since vector instructions hardly overlap matrix ones here (a 16x16x32 product takes 20
+// cycles, with two fma 24; the conversion of two values 6.6, an exp 9): per 32 tokens
+// and 32 rows of 128 channels 12 + 16 + 2 matrix and about 100 vector instructions:
+// 8192 new tokens 543 us, 1.01 PFLOP/s where the library's bf16 product of 8192^3
+// reaches 1.23. Little of both: latency, of two reads one after the other (lengths,
+// page numbers), a step and the joins: 777 tokens 10.7 us, 32 tokens 4.7.
+// Two tiles of 128 channels (three of 64) fill 256 registers; four need the second
+// half of the register file, and 35 moves a tile and step (slower); three waves a
+// SIMD spill.
 #include "device.hpp"
 #include "kernels.hpp"
 
@@ -50,7 +66,7 @@ namespace {
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr int kRowWaves = 4;       // of a workgroup of attention_rows_kernel
 constexpr int kStep = 32;          // tokens a wave takes at a time
-constexpr float kSlack = 8.0f;     // how far a score may pass the maximum in use, in powers of two
+constexpr float kSlack = 8.0f;     // how far a score may pass the maximum in use, in powers of two; 0: prompts 423 us, not 350
 constexpr int kFarRight = 0x7FFFFFFF;
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
@@ -743,6 +759,7 @@ constexpr size_t part_floats() { return (size_t)16 * NQ * (D + 2); }
 
 // Split form: workers take equal shares of all units (2^unit_bits tokens of a tile), in a row. A worker is kW waves, which
 // take every kW-th step of its share and join in LDS. Without records every segment is one unit, and nothing is left to join.
+// Shares are cut at single steps: at every fourth, 64 sequences of 4352 tokens took 68.5 us instead of 63.5.
 template <int D, int NQ, int kW>
 __global__ __launch_bounds__(kW * kWave, 2) void attention_split_kernel(Attention a, CacheView c, float* parts,
                                                                         Record* records, int workers, int unit_bits,
@@ -894,7 +911,7 @@ __global__ __launch_bounds__(kW * kWave, 2) void attention_split_kernel(Attentio
 }
 
 constexpr int kJoinWaves = 4;
-constexpr int kSpreadRecords = 64;   // 8 segments of 64 parts: 4.5 us instead of 7; 520 of 3: 3 more
+constexpr int kSpreadRecords = 64;   // 16 segments of 64 parts: a call of 36.7 us instead of 39; 640 of 4: 71.1 instead of 69.4
 
 // Joins the parts of a segment: a wave a row, or, where there are few segments and so many parts of each, a workgroup a row
 // (kSpread). Two parts at a time, half a wave each, sixteen of them on their way.

@@ -24,6 +24,11 @@
 // a branch that the whole workgroup takes alike. The codes of a head are 64 (or
 // 32) contiguous bytes and its scales 4 (or 2): [page][head][place], the layout
 // in which attention reads a head's tokens in one run.
+//
+// Bounds. Many tokens: HBM; 8192 of 32 query and 8 + 8 kv heads of 128 through norm
+// and rotation 40.6 us (181 MB, 4.5 TB/s: half of the issue slots are taken as well),
+// 16384 of 8 heads of 128 read back 17.4 us (85 MB, 4.9 TB/s). Few: the latency of a
+// slot's load, a row's load and the store, 2.4 us.
 #include <limits.h>
 
 #include "device.hpp"
@@ -75,7 +80,7 @@ __device__ __forceinline__ uint32_t round_bf16x2(float lo, float hi) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
 }
 
-// Rows that a group has on their way at a time.
+// Rows that a group has on their way at a time (norm and rotation of 8192 tokens, read back: 50.8 us; 1: 52.8, 8: 51.9).
 constexpr int kAtOnce = 4;
 
 template <int kCtrl>
@@ -326,8 +331,9 @@ __global__ __launch_bounds__(kThreads) void cache_read_kernel(CacheView c, const
     }
 }
 
-// Heads a group takes one after another: all of a token's angles are read again by each of its groups, so a large call
-// takes several heads a group, and a small one a head each.
+// Heads a group takes one after another: all of a token's angles are read again by each of its groups, so a large call takes
+// several heads a group (8192 tokens through norm and rotation, read back: 50.8 us, a head a group 101), and a small one a
+// head each (64 tokens 5.8, eight a group 9.3).
 int rows_per_group(int64_t token_groups, int rows) {
     int per = 1;
     while (per < 8 && token_groups * ((rows + per - 1) / per) > 8 * device_cu_count()) per *= 2;
