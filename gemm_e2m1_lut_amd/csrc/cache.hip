@@ -210,7 +210,7 @@ __global__ __launch_bounds__(kThreads) void norm_rope_write_kernel(
     const int first = blockIdx.y * rows_per, last = min(first + rows_per, heads + 2 * c.heads);
 
     // angles of this lane's channels: eight of one half, or four pairs
-    const bool turns = lane * 8 < rot;
+    const bool turns = lane * 8 < rot && max_pos > 0;   // an empty table has no position, and nothing to read
     const bool high = !kInterleaved && lane * 8 >= rot / 2;
     const int partner = threadIdx.x % kWave + (high ? -rot / 16 : rot / 16);
     float cs[8], sn[8];

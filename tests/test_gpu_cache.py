@@ -264,6 +264,24 @@ def test_positions_outside_the_table(gpu):
     assert untouched(cache, torch.tensor([0]), 16, 0x22)
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_no_positions_at_all(gpu, interleaved):
+    """An angle table of no rows is not read: every position is outside it."""
+    say("norm rope write: an empty table")
+    r = np.random.default_rng(10)
+    x = rows(r, (5, 4 * 64), "bf16").to(DEV)
+    flag = torch.zeros(1, dtype=torch.int32, device=DEV)
+    cache = new_cache(1, 1, 16, 64, 0x22)
+    slots = torch.full((5,), -1, dtype=torch.int64, device=DEV)
+    pos = torch.zeros(5, dtype=torch.int64, device=DEV)
+    call = lambda: gpu.norm_rope_mxfp4_cache_write(x, torch.empty(0, 64, device=DEV), pos, slots, cache,   # noqa: E731
+                                                   interleaved=interleaved, err_flag=flag)
+    assert not call().any() and flag.item() == 0
+    slots[3] = 7
+    assert not call().any() and flag.item() == 1
+    assert untouched(cache, torch.tensor([], dtype=torch.int64), 16, 0x22)
+
+
 def test_streams_graphs_and_rows(gpu):
     """Strided rows, another stream, a graph replayed with poisoned outputs: the eager bits each time."""
     say("norm rope write: graph")
