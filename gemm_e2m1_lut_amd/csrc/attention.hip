@@ -727,7 +727,7 @@ __device__ __forceinline__ float last_factor(float m, float l, const float* sink
         const float s = sinks[head] * kLog2e;
         const float mn = finite_or_zero(fmaxf(m, s));
         f = exp2_raw(m - mn);
-        l = l * f + exp2_raw(s - mn);
+        l = l * f + exp2_raw(s == mn ? 0.0f : s - mn);   // equal: of infinities too
     }
     return l == 0.0f ? 0.0f : f * __builtin_amdgcn_rcpf(l);
 }

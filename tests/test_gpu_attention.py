@@ -226,6 +226,20 @@ def test_sinks_at_the_ends(gpu):
     assert not out[:, 4].any()      # nothing is left beside a sink that large
 
 
+def test_infinite_sinks(gpu):
+    """Nothing is left beside an infinite sink; a query that is not finite stays NaN."""
+    say("attention: infinite sinks")
+    for lens in ([(1, 100), (3, 0), (20, 50)], [(1, 5000)], [(300, 300)]):
+        case = Case(lens, 4, 2, 64, 16, 6)
+        d = case.device()
+        d["q"][0, 1] = float("nan")
+        d["q"][0, 3] = float("nan")
+        sinks = torch.tensor([0, float("inf"), float("inf"), 0], device=DEV)
+        out = gpu.mxfp4_attention(**d, sinks=sinks)
+        assert not out[1:, 1:3].any() and not out[0, 2].any() and out[0, [1, 3]].isnan().all()
+        assert not out[0, 0].isnan().any() and out[0, 0].any()
+
+
 @pytest.mark.parametrize("garbage", [255, 254, 252, 0])
 def test_what_is_not_seen_changes_nothing(gpu, garbage):
     """Whatever lies in unused places and in tokens that a query does not see."""
