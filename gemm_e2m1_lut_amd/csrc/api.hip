@@ -404,7 +404,7 @@ int mxfp4_attention(const uint16_t* q, int64_t q_stride, const uint8_t* k_codes,
     const e2m1::CacheView c = cache_view(k_codes, k_scales, v_codes, v_scales, kv_heads, head_dim, pages, page_size);
     const e2m1::Attention a = {q,   q_stride, page_table, kv_lens, q_offsets, sinks, scale, causal != 0, window < INT_MAX ? window : 0,
                                out, tokens,   seqs,       (int)heads, table_width, err_flag};
-    return launch_status(e2m1::launch_attention(a, c, workspace, as_stream(stream)));
+    return launch_status(e2m1::launch_attention(a, c, workspace, workspace_bytes, as_stream(stream)));
 }
 
 int ternary_gemv(const uint32_t* packed, const float* row_scale, const float* x, float* y,

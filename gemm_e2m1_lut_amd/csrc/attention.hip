@@ -113,9 +113,7 @@ struct Span {
     int len;     // cached tokens
 };
 
-__device__ __forceinline__ Span span_of(const Attention& a, int page_bits, int s) {
-    const int o0 = a.q_offsets[s], o1 = a.q_offsets[s + 1];
-    const int len = a.kv_lens[s];
+__device__ __forceinline__ Span make_span(const Attention& a, int page_bits, int o0, int o1, int len) {
     const int tokens = (int)a.tokens, most = (int)(a.table_width << page_bits);
     Span r;
     r.first = min(max(o0, 0), tokens);
@@ -123,6 +121,10 @@ __device__ __forceinline__ Span span_of(const Attention& a, int page_bits, int s
     r.len = min(max(len, 0), most);
     if (len > most && r.n > 0 && a.err_flag) *a.err_flag = 1;
     return r;
+}
+
+__device__ __forceinline__ Span span_of(const Attention& a, int page_bits, int s) {
+    return make_span(a, page_bits, a.q_offsets[s], a.q_offsets[s + 1], a.kv_lens[s]);
 }
 
 // The first token that query i of a sequence sees.
@@ -159,8 +161,9 @@ __device__ __forceinline__ uint32_t scan(uint32_t v) {
 
 __device__ __forceinline__ int from_lane(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
 
-// Sequences laid end to end by weight, a run of them a lane; a scan over the wave gives the runs' places. Up to 64 sequences
-// are read once and kept.
+// Sequences laid end to end by weight. Up to 64 are read once and kept, one a lane. Of more, a lane has the sum of a run of
+// whole rounds of the wave (64 sequences side by side, four rounds on their way), and the run that holds a place is gone
+// through again.
 struct Plan {
     const Attention& a;
     int page_bits, lane, per;
@@ -168,14 +171,40 @@ struct Plan {
     uint32_t before, total;
     bool ok;                   // no offset is below the one before it: then no query row belongs to two sequences
 
-    // The lane's sequences [lane per, ..).
     __device__ __forceinline__ int begin() const { return lane * per; }
-    __device__ __forceinline__ int end() const { return (int)min((int64_t)(lane + 1) * per, a.seqs); }
+    __device__ __forceinline__ int end(int owner) const { return (int)min((int64_t)(owner + 1) * per, a.seqs); }
+
+    // The weights of the lane's run.
+    template <typename F>
+    __device__ __forceinline__ uint32_t run_sum(F weight, bool& bad) const {
+        constexpr int kRounds = 4;
+        uint32_t sum = 0;
+        const int seqs = (int)a.seqs;
+        for (int s0 = 0; s0 < seqs; s0 += kRounds * kWave) {
+            int o0[kRounds], o1[kRounds], len[kRounds];
+#pragma unroll
+            for (int i = 0; i < kRounds; ++i) {
+                const int s = min(s0 + i * kWave + lane, seqs - 1);
+                o0[i] = a.q_offsets[s];
+                o1[i] = a.q_offsets[s + 1];
+                len[i] = a.kv_lens[s];
+            }
+#pragma unroll
+            for (int i = 0; i < kRounds; ++i) {
+                const int s = s0 + i * kWave;
+                const uint32_t w = s + lane < seqs ? weight(make_span(a, page_bits, o0[i], o1[i], len[i])) : 0;
+                const uint32_t all = (uint32_t)from_lane((int)scan(w), kWave - 1);
+                if (s >= begin() && s < begin() + per) sum += all;
+                bad |= o1[i] < o0[i];
+            }
+        }
+        return sum;
+    }
 
     template <typename F>
     __device__ __forceinline__ Plan(const Attention& a_, int page_bits_, int lane_, F weight)
         : a(a_), page_bits(page_bits_), lane(lane_) {
-        per = (int)((a.seqs + kWave - 1) / kWave);
+        per = a.seqs <= kWave ? 1 : (int)((a.seqs + kWave * kWave - 1) / (kWave * kWave)) * kWave;
         mine = {0, 0, 0};
         uint32_t sum = 0;
         bool bad = false;
@@ -186,10 +215,7 @@ struct Plan {
             }
             sum = weight(mine);
         } else {
-            for (int s = begin(); s < end(); ++s) {
-                sum += weight(span_of(a, page_bits, s));
-                bad |= a.q_offsets[s + 1] < a.q_offsets[s];
-            }
+            sum = run_sum(weight, bad);
         }
         ok = !__any(bad);
         if (bad && a.err_flag) *a.err_flag = 1;
@@ -201,20 +227,17 @@ struct Plan {
     // Another weight's sum over the sequences before `seq`, and over all.
     template <typename F>
     __device__ __forceinline__ uint32_t sum_before(int seq, F weight, uint32_t& all) const {
-        uint32_t sum = 0, part = 0;
-        if (per == 1) {
-            sum = weight(mine);
-        } else {
-            for (int s = begin(); s < end(); ++s) {
-                const uint32_t w = weight(span_of(a, page_bits, s));
-                sum += w;
-                if (s < seq) part += w;
-            }
-        }
-        const int owner = (int)((uint32_t)seq / (uint32_t)per);
+        bool bad = false;
+        const uint32_t sum = per == 1 ? weight(mine) : run_sum(weight, bad);
         const uint32_t after = scan(sum);
         all = (uint32_t)from_lane((int)after, kWave - 1);
-        return (uint32_t)from_lane((int)(after - sum + part), owner);
+        const int owner = (int)((uint32_t)seq / (uint32_t)per);
+        uint32_t part = (uint32_t)from_lane((int)(after - sum), owner);
+        for (int s = owner * per; s < seq; s += kWave) {
+            const uint32_t w = s + lane < seq ? weight(span_of(a, page_bits, s + lane)) : 0;
+            part += (uint32_t)from_lane((int)scan(w), kWave - 1);
+        }
+        return part;
     }
 
     // A sequence, the same for every lane.
@@ -228,19 +251,21 @@ struct Plan {
     template <typename F>
     __device__ __forceinline__ int find(uint32_t at, uint32_t& begins, F weight) const {
         // the last lane whose run begins at or before it: empty runs before it begin at the same place
-        const int owner = 63 - __builtin_clzll(__ballot(before <= at && begin() < end()));
-        int s = begin();
-        uint32_t b = before;
-        if (per > 1 && lane == owner) {
-            for (;;) {
-                const uint32_t w = weight(span_of(a, page_bits, s));
-                if (at < b + w) break;
-                b += w;
-                ++s;
+        const int owner = 63 - __builtin_clzll(__ballot(before <= at && begin() < end(lane)));
+        begins = (uint32_t)from_lane((int)before, owner);
+        if (per == 1) return owner;
+        const int last = end(owner);
+        for (int s = owner * per;; s += kWave) {
+            const uint32_t w = s + lane < last ? weight(span_of(a, page_bits, s + lane)) : 0;
+            const uint32_t after = scan(w);
+            const uint64_t past = __ballot(begins + after > at);
+            if (past != 0 || s + kWave >= last) {
+                const int i = past != 0 ? __builtin_ctzll(past) : last - 1 - s;
+                begins += (uint32_t)from_lane((int)(after - w), i);
+                return s + i;
             }
+            begins += (uint32_t)from_lane((int)after, kWave - 1);
         }
-        begins = (uint32_t)from_lane((int)b, owner);
-        return from_lane(s, owner);
     }
 };
 
@@ -1071,18 +1096,21 @@ Form form_of(int64_t tokens, int64_t seqs, int64_t heads, int64_t kv_heads, int6
     // Rows enough to fill the chip twice with two or three tiles a wave: a prompt of 2048 56.7 (one tile a wave 61.5, shares
     // 95), 2048 tokens after 6144 242 (322, 304). With 64 rows a sequence or less half of a workgroup has none (16 queries of
     // 256 sequences: 150, one tile 135).
-    if (mean > 64 && most_tiles(tokens, seqs, group, 16 * wide * kRowWaves) * kv_heads >= 2 * cus)
+    // Every workgroup looks for its rows among all sequences, 3 us of 1024: where a tile has less to do than that, the few
+    // workgroups of equal shares are better (64 tokens of 64 in 1024 sequences 436, tiles 522; in 256: 107, 100).
+    const bool few = seqs <= kWave + 16 * steps;
+    if (few && mean > 64 && most_tiles(tokens, seqs, group, 16 * wide * kRowWaves) * kv_heads >= 2 * cus)
         return {kRowsForm, wide, 0, 0, 0, 0};
     // One tile a wave. Few segments and tokens: one token of 64 sequences of 192 8.4 (four waves a segment 10.2), of 16: 7.6
     // (7.6). Many of both, as long as the chain of steps is short beside the number of tiles: 1024 tokens after 3072 88
     // (shares 92.7), 512 after 1700 42.5 (35.8).
-    if (n <= 2 * cus ? steps <= (n <= cus ? 5 : 12) : mean >= 48 && 16 * steps <= n) return {kRowsForm, 1, 0, 0, 0, 0};
+    if (n <= 2 * cus ? steps <= (n <= cus ? 5 : 12) : few && mean >= 48 && 16 * steps <= n) return {kRowsForm, 1, 0, 0, 0, 0};
     // Whole segments save the join, its launch and the parts' way through memory. With no more than two a compute unit all
     // are under way at once: one token after 1000 in 64 sequences 17.7 (shares 28.1), of 2048 in 16 15.5 in eight waves (16.2
     // in four, 16.9), of 2048 alone 14.2 (11.1: its eight segments leave the chip idle, which the estimates say, in 0.1 us). A
     // segment longer than the others keeps the call waiting, so chains longer than 32 steps are cut (64 sequences of 4352:
     // 63.5, whole 57). Of more segments, each a wave's: one token after 384 in 200 sequences 20.1 (30.8), 8 queries after 1000
-    // in 256 84.7 (92.7).
+    // in 256 84.7 (92.7), one token after 64 in 256 11.1 (13.2), in 1024 49.7 (32.8).
     Form f = split_of(tokens, seqs, heads, kv_heads, 1);
     auto whole = [&](int waves) {
         f.kind = kWholeForm;
@@ -1096,14 +1124,18 @@ Form form_of(int64_t tokens, int64_t seqs, int64_t heads, int64_t kv_heads, int6
         const int64_t as_whole = waves == 8 ? 93 + 7 * chain : 66 + 6 * chain;
         const int64_t as_shares = 110 + 50 * (n < 64 ? n : 64) / 64 + 7 * n * steps / (8 * cus);
         if (chain <= 32 && as_whole < as_shares) return whole(waves);
-    } else if (mean < 48 && steps <= 32 && f.segments < 1 << 20) {
+    } else if (mean < 48 && steps <= 32 && seqs <= 4 * kWave) {
         return whole(1);
     }
     // Two tiles share their tokens' bytes, and pay for it once a worker, with more to set up and to join: 512 tokens after
-    // 15872 154 (one tile 201), 8 queries of 4 sequences of 16384 30.2 (27.5).
-    if (mean > 16 && seqs * ((mean + 31) / 32) * kv_heads * steps >= 9 * 8 * cus)
+    // 15872 154 (one tile 201), 8 queries of 4 sequences of 16384 30.2 (27.5), 16 of 64 of 300 33.9 (21.5).
+    if (mean > 16 && steps >= 64 && seqs * ((mean + 31) / 32) * kv_heads * steps >= 9 * 8 * cus)
         return split_of(tokens, seqs, heads, kv_heads, 2);
     return f;
+}
+
+size_t bytes_of(const Form& f, int64_t head_dim) {
+    return f.records() * sizeof(Record) + (size_t)f.workers * 2 * 16 * f.nq * (head_dim + 2) * sizeof(float);
 }
 
 template <int D, int NQ, int kW>
@@ -1138,9 +1170,10 @@ hipError_t rows_form(const Attention& a, const CacheView& c, hipStream_t stream)
 }
 
 template <int D>
-hipError_t attend(const Attention& a, const CacheView& c, void* workspace, hipStream_t stream) {
+hipError_t attend(const Attention& a, const CacheView& c, void* workspace, size_t workspace_bytes, hipStream_t stream) {
     const int64_t most = a.table_width << c.page_bits, seen = a.window + (a.tokens + a.seqs - 1) / a.seqs;
     const Form f = form_of(a.tokens, a.seqs, a.heads, c.heads, D, a.window > 0 && seen < most ? seen : most);
+    if (f.kind == kSplitForm && bytes_of(f, D) > workspace_bytes) return hipErrorInvalidValue;
     if (f.kind == kRowsForm)
         return f.nq == 1 ? rows_form<D, 1>(a, c, stream) : rows_form<D, (D == 128 ? 2 : 3)>(a, c, stream);
     if (f.nq == 2) return split_form<D, 2, 4>(a, c, f, workspace, stream);
@@ -1151,14 +1184,18 @@ hipError_t attend(const Attention& a, const CacheView& c, void* workspace, hipSt
 
 }  // namespace
 
+// For any length: the form depends on it, and the bytes of the shares with it.
 size_t attention_workspace_bytes(int64_t tokens, int64_t seqs, int64_t heads, int64_t kv_heads, int64_t head_dim) {
-    const Form f = form_of(tokens, seqs, heads, kv_heads, head_dim, (int64_t)1 << 30);
-    if (f.kind != kSplitForm) return 0;
-    return f.records() * sizeof(Record) + (size_t)f.workers * 2 * 16 * f.nq * (head_dim + 2) * sizeof(float);
+    if (seqs <= kWave && form_of(tokens, seqs, heads, kv_heads, head_dim, 1).nq >= 2) return 0;   // wide rows whatever the length
+    const size_t one = bytes_of(split_of(tokens, seqs, heads, kv_heads, 1), head_dim);
+    const size_t two = bytes_of(split_of(tokens, seqs, heads, kv_heads, 2), head_dim);
+    return one > two ? one : two;
 }
 
-hipError_t launch_attention(const Attention& a, const CacheView& c, void* workspace, hipStream_t stream) {
-    return c.head_dim == 128 ? attend<128>(a, c, workspace, stream) : attend<64>(a, c, workspace, stream);
+hipError_t launch_attention(const Attention& a, const CacheView& c, void* workspace, size_t workspace_bytes,
+                            hipStream_t stream) {
+    return c.head_dim == 128 ? attend<128>(a, c, workspace, workspace_bytes, stream)
+                             : attend<64>(a, c, workspace, workspace_bytes, stream);
 }
 
 }  // namespace e2m1

@@ -104,7 +104,8 @@ struct Attention {
     int32_t* err_flag;
 };
 size_t attention_workspace_bytes(int64_t tokens, int64_t seqs, int64_t heads, int64_t kv_heads, int64_t head_dim);
-hipError_t launch_attention(const Attention& a, const CacheView& c, void* workspace, hipStream_t stream);
+hipError_t launch_attention(const Attention& a, const CacheView& c, void* workspace, size_t workspace_bytes,
+                            hipStream_t stream);
 
 hipError_t launch_ternary(const uint32_t* packed, const float* row_scale, const float* x, float* y,
                           int64_t n, int64_t k, hipStream_t stream);

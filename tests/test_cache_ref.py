@@ -213,6 +213,31 @@ def test_attention_launches_fit(lib, group, queries):
                     assert bound <= 2**29
 
 
+def test_attention_workspace_holds_every_form(lib):
+    """The size does not know how far a table reaches, the form does: it has to do for all of them."""
+    form = lib.e2m1_mxfp4_attention_form
+    form.argtypes = [ctypes.c_int64] * 6
+    seen = set()
+    for heads, kv in ((8, 8), (8, 2), (32, 8), (64, 8), (16, 1), (17, 1), (4096, 1)):
+        for seqs in (1, 2, 3, 8, 16, 40, 64, 65, 100, 256, 257, 1000, 5000):
+            for queries in (1, 2, 4, 5, 8, 12, 16, 30, 64, 300, 2000):
+                for tokens in (seqs * queries, seqs * queries - seqs // 2):
+                    if tokens * heads > 2**28:
+                        continue
+                    for dim in (64, 128):
+                        size = lib.mxfp4_attention_workspace_size(tokens, seqs, heads, kv, dim)
+                        for length in (1, 16, 32, 64, 100, 200, 500, 1000, 1600, 2000, 3000, 5000, 9000, 40000, 2**20, 2**30):
+                            f = form(tokens, seqs, heads, kv, dim, length)
+                            kind, nq, waves = f // 100 % 10, f // 10 % 10, f % 10
+                            seen.add(f)
+                            if kind == 2:
+                                workers = 8 // waves * 256
+                                segments = (tokens * (heads // kv) // (16 * nq) + min(seqs, tokens)) * kv
+                                need = 32 * min(segments, workers) + workers * 2 * 16 * nq * (dim + 2) * 4
+                                assert size >= need, (tokens, seqs, heads, kv, dim, length, f, size, need)
+    assert {10, 20, 30, 111, 114, 118, 211, 1211, 214, 2214, 224, 1224, 2224} <= seen
+
+
 def test_binding_checks_its_tensors():
     import gemm_e2m1_lut_amd as g
     t = torch.zeros
