@@ -1063,7 +1063,7 @@ int64_t most_tiles(int64_t tokens, int64_t seqs, int64_t group, int64_t rows) {
 
 // How a call is worked on, from what the host knows: the numbers of rows and sequences, and how many tokens a row can see. The
 // times below are of 32 query heads over 8 of 128 channels, in us; n: segments of 16 rows. The choice was taken from 70 calls
-// (heads of 64 and 128 channels, 1 to 2048 queries, 1 to 256 sequences of 64 to 131072 tokens) timed in every form: it is 0.2 %
+// (heads of 64 and 128 channels, 1 to 2048 queries, 1 to 256 sequences of 64 to 131072 tokens) timed in every form: it is 1 %
 // above the fastest form on the mean, 14 % at most.
 enum Kind { kRowsForm, kWholeForm, kSplitForm };
 struct Form {
