@@ -75,8 +75,8 @@ typedef uint32_t u32x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x32 __attribute__((ext_vector_type(32)));
 
-// Quotients of numbers below 2^29 by `d` below 2^13 (Granlund and Montgomery): with 2^bits >= d and mul = ceil(2^(29 + bits) / d),
-// n mul / 2^(29 + bits) exceeds n / d by less than 1 / d.
+// Quotients of numbers below 2^29 by `d` below 2^13 (Granlund and Montgomery): with 2^bits >= d and mul =
+// ceil(2^(29 + bits) / d), n mul / 2^(29 + bits) exceeds n / d by less than 1 / d.
 struct Divisor {
     uint32_t mul;
     int bits;
@@ -329,7 +329,7 @@ struct Lane {
     uint32_t k, ks, v, vs;
     uint32_t turn;   // rotation that brings the scale of the lane's channels to an exponent field
     int own;         // the block of its channels
-    __device__ __forceinline__ Lane(const CacheView&, int lane_) : lane(lane_) {
+    __device__ __forceinline__ Lane(int lane_) : lane(lane_) {
         n = lane % 16;
         g = lane / 16;
         const int block = D == 128 ? g : g & 1;
@@ -654,8 +654,8 @@ __device__ __forceinline__ void split_query(const u32x4 (&w)[4], float scale, in
 
 // The rows [row0, row0 + 16 NQ) of a sequence's (query, head of the group) pairs; rows past the last one see what it sees.
 template <int D, int NQ>
-__device__ __forceinline__ void set_ranges(Rows<NQ>& rows, const Attention& a, const Span& s, int group, const Divisor& by, int row0,
-                                           const Lane<D>& ln) {
+__device__ __forceinline__ void set_ranges(Rows<NQ>& rows, const Attention& a, const Span& s, int group, const Divisor& by,
+                                           int row0, const Lane<D>& ln) {
     const int last = s.n * group - 1;
     const int i_first = divide(row0, by), i_last = divide(min(row0 + 16 * NQ - 1, last), by);
     const int p0 = s.len - s.n;   // position of query 0
@@ -681,8 +681,7 @@ __device__ __forceinline__ void set_ranges(Rows<NQ>& rows, const Attention& a, c
 template <int D, int NQ>
 __device__ __forceinline__ void run_steps(const Attention& a, const CacheView& c, const int32_t* table, const Span& s,
                                           int kv_head, int group, const Divisor& by, int row0, int first, int last,
-                                          int stride,
-                                          Sums<D, NQ>& sums, const Lane<D>& ln) {
+                                          int stride, Sums<D, NQ>& sums, const Lane<D>& ln) {
     Rows<NQ> rows;
     set_ranges<D, NQ>(rows, a, s, group, by, row0, ln);
     sums.clear();
@@ -845,8 +844,8 @@ __global__ __launch_bounds__(kW * kWave, 2) void attention_split_kernel(Attentio
         const int origin = first_seen(a, s, 0) / kStep, steps = unit_bits - 5;
         Sums<D, NQ> sums;
         run_steps<D, NQ>(a, c, a.page_table + seq * a.table_width, s, head, group, by, row0,
-                         origin + (u0 << steps) + wave, origin + (u1 << steps), kW, sums, Lane<D>(c, lane));
-        const Lane<D> ln(c, not_before(lane));
+                         origin + (u0 << steps) + wave, origin + (u1 << steps), kW, sums, Lane<D>(lane));
+        const Lane<D> ln(not_before(lane));
         const bool whole = u0 == 0 && u1 == (int)units;
         float* part = parts + (2 * (size_t)id + (u0 > 0 ? 0 : 1)) * part_floats<D, NQ>();
         const int rows_left = s.n * group - row0;
@@ -1036,8 +1035,8 @@ __global__ __launch_bounds__(kRowWaves * kWave, 2) void attention_rows_kernel(At
     const int rows_left = s.n * group - row0;
     if (rows_left <= 0) return;
     Sums<D, NQ> sums;
-    run_steps<D, NQ>(a, c, a.page_table + seq * a.table_width, s, head, group, by, row0, 0, kFarRight, 1, sums, Lane<D>(c, lane));
-    const Lane<D> ln(c, not_before(lane));
+    run_steps<D, NQ>(a, c, a.page_table + seq * a.table_width, s, head, group, by, row0, 0, kFarRight, 1, sums, Lane<D>(lane));
+    const Lane<D> ln(not_before(lane));
 #pragma unroll
     for (int i = 0; i < NQ; ++i)
 #pragma unroll
@@ -1102,7 +1101,7 @@ Form form_of(int64_t tokens, int64_t seqs, int64_t heads, int64_t kv_heads, int6
     if (few && mean > 64 && most_tiles(tokens, seqs, group, 16 * wide * kRowWaves) * kv_heads >= 2 * cus)
         return {kRowsForm, wide, 0, 0, 0, 0};
     // One tile a wave. Few segments and tokens: one token of 64 sequences of 192 8.4 (four waves a segment 10.2), of 16: 7.6
-    // (7.6). Many of both, as long as the chain of steps is short beside the number of tiles: 1024 tokens after 3072 88
+    // (7.6). Many of both, as long as the chain of steps is short beside the number of tiles: the last 1024 of 4096 tokens 88
     // (shares 92.7), 512 after 1700 42.5 (35.8).
     if (n <= 2 * cus ? steps <= (n <= cus ? 5 : 12) : few && mean >= 48 && 16 * steps <= n) return {kRowsForm, 1, 0, 0, 0, 0};
     // Whole segments save the join, its launch and the parts' way through memory. With no more than two a compute unit all
@@ -1151,10 +1150,11 @@ hipError_t split_form(const Attention& a, const CacheView& c, const Form& f, voi
                                                                             divisor_of(a.heads / c.heads));
     if (hipError_t e = hipGetLastError(); e != hipSuccess || !records) return e;
     const Divisor by = divisor_of(a.heads / c.heads);
+    const int threads = kJoinWaves * kWave;
     if (f.records() <= kSpreadRecords)
-        attention_join_kernel<D, NQ, true><<<dim3(f.records(), 16 * NQ), kJoinWaves * kWave, 0, stream>>>(a, c, parts, records, by);
+        attention_join_kernel<D, NQ, true><<<dim3(f.records(), 16 * NQ), threads, 0, stream>>>(a, c, parts, records, by);
     else
-        attention_join_kernel<D, NQ, false><<<dim3(f.records(), f.join_rows), kJoinWaves * kWave, 0, stream>>>(a, c, parts, records, by);
+        attention_join_kernel<D, NQ, false><<<dim3(f.records(), f.join_rows), threads, 0, stream>>>(a, c, parts, records, by);
     return hipGetLastError();
 }
 
