@@ -73,7 +73,7 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x6 __attribute__((ext_vector_type(6)));
 typedef uint32_t u32x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x16 __attribute__((ext_vector_type(16)));
-typedef __bf16 bf16x32 __attribute__((ext_vector_type(32)));
+typedef _Float16 f16x32 __attribute__((ext_vector_type(32)));
 
 // Quotients of numbers below 2^29 by `d` below 2^13 (Granlund and Montgomery): with 2^bits >= d and mul =
 // ceil(2^(29 + bits) / d), n mul / 2^(29 + bits) exceeds n / d by less than 1 / d.
@@ -580,57 +580,52 @@ __device__ __forceinline__ void take_step(const Keys<D>& keys, Values<D>& s, con
 
 // ---------------------------------------------------------------- queries --
 
-typedef uint32_t u32x16 __attribute__((ext_vector_type(16)));
-
-// x <- x - part, the values of a part of them.
-__device__ __forceinline__ void take_off(float (&x)[32], const bf16x32& part) {
-    const u32x16 w = __builtin_bit_cast(u32x16, part);
+// x <- by x - part: what a part leaves, in units `by` times smaller.
+__device__ __forceinline__ void take_off(float (&x)[32], float by, const f16x32& part) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        x[2 * i] -= __uint_as_float(w[i] << 16);
-        x[2 * i + 1] -= __uint_as_float(w[i] & 0xFFFF0000u);
-    }
+    for (int i = 0; i < 32; ++i) x[i] = __builtin_fmaf(x[i], by, -(float)part[i]);
 }
 
-__device__ __forceinline__ bf16x32 as_bf16(const float (&x)[32]) {
-    u32x16 w;
+__device__ __forceinline__ f16x32 as_f16(const float (&x)[32]) {
+    f16x32 h;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) w[i] = pack_weights(x[2 * i], x[2 * i + 1]);
-    return __builtin_bit_cast(bf16x32, w);
+    for (int i = 0; i < 32; ++i) h[i] = (_Float16)x[i];
+    return h;
 }
 
 __device__ __forceinline__ i32x8 widen(const u32x6& v) {
     return i32x8{(int)v[0], (int)v[1], (int)v[2], (int)v[3], (int)v[4], (int)v[5], 0, 0};
 }
 
-// The three parts of a lane's 32 channels times `scale`. Their largest magnitude lies in [3.75, 7.5] of the first part's
-// unit 2^e (7.5 is E2M3's largest), so the first part leaves at most 1/4 (half of its largest step), the second, in units of
-// 2^(e-4), at most 2^-7, the third, in 2^(e-9), 2^-12: 2^-13 of the largest. Remainders are fp32; they go through bf16 on
-// their way to a part, which may choose the part next to the nearest and so only moves what the next one has to take.
-// A block that holds a NaN or an infinity gets the scale NaN.
+// The three parts of a lane's 32 channels times `scale`, in units 2^e where the largest magnitude lies in (3.75, 7.5] (7.5 is
+// E2M3's largest). The first part leaves at most 1/4 (half of its largest step), the second, in units of 2^-4, at most 2^-7,
+// the third, in 2^-9, 2^-12: less than 2^-13 of the largest. Remainders are fp32, each in its part's unit, and go through fp16
+// on their way to a part, which may pass a border between two of its values by no more than half a step of fp16: 2^-9 of the
+// first unit, 2^-10 of the others. What is left stays within 1/4 + 2^-9, 2^-7 + 2^-14 and 2^-12 + 2^-19: the next part's value
+// nearest to it is the last one before its steps grow (through bf16 2^-6 can be left for the third part, past its end, and 2^-10
+// by it). A block that holds a NaN or an infinity gets the scale NaN.
 template <int D>
 __device__ __forceinline__ void split_query(const u32x4 (&w)[4], float scale, int g, i32x8 (&q)[3], uint32_t& scales) {
+    u16x2 top = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 16; ++i) top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, w[i / 4][i % 4] & 0x7FFF7FFFu));
+    const float largest = __uint_as_float(max((uint32_t)top.x, (uint32_t)top.y) << 16) * scale;
+    const uint32_t most = __float_as_uint(largest) & 0x7FFFFFFFu;
+    const uint32_t field = (most + 0xFFFFFu) >> 23;   // past 1.875 2^n: of 2^(n+1)
+    const uint32_t e = max(field, 11u) - 2u;
+    const float unit = __uint_as_float((254u - e) << 23);   // 2^-e
     float x[32];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
         const uint32_t v = w[i / 4][i % 4];
-        x[2 * i] = __uint_as_float(v << 16) * scale;
-        x[2 * i + 1] = __uint_as_float(v & 0xFFFF0000u) * scale;
+        x[2 * i] = __uint_as_float(v << 16) * scale * unit;
+        x[2 * i + 1] = __uint_as_float(v & 0xFFFF0000u) * scale * unit;
     }
-    const bf16x32 b0 = as_bf16(x);
-    u16x2 top = {0, 0};
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-        top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, __builtin_bit_cast(u32x16, b0)[i] & 0x7FFF7FFFu));
-    const uint32_t most = max((uint32_t)top.x, (uint32_t)top.y);
-    const uint32_t field = (most + 0xFu) >> 7;   // past 1.875 2^n: of 2^(n+1)
-    const uint32_t e = max(field, 11u) - 2u;
-    const float s0 = __uint_as_float(e << 23), s1 = __uint_as_float((e - 4u) << 23), s2 = __uint_as_float((e - 9u) << 23);
-    const u32x6 p0 = __builtin_amdgcn_cvt_scalef32_pk32_fp6_bf16(b0, s0);
-    take_off(x, __builtin_amdgcn_cvt_scalef32_pk32_bf16_fp6(p0, s0));
-    const u32x6 p1 = __builtin_amdgcn_cvt_scalef32_pk32_fp6_bf16(as_bf16(x), s1);
-    take_off(x, __builtin_amdgcn_cvt_scalef32_pk32_bf16_fp6(p1, s1));
-    const u32x6 p2 = __builtin_amdgcn_cvt_scalef32_pk32_fp6_bf16(as_bf16(x), s2);
+    const u32x6 p0 = __builtin_amdgcn_cvt_scalef32_pk32_fp6_f16(as_f16(x), 1.0f);
+    take_off(x, 16.0f, __builtin_amdgcn_cvt_scalef32_pk32_f16_fp6(p0, 16.0f));
+    const u32x6 p1 = __builtin_amdgcn_cvt_scalef32_pk32_fp6_f16(as_f16(x), 1.0f);
+    take_off(x, 32.0f, __builtin_amdgcn_cvt_scalef32_pk32_f16_fp6(p1, 32.0f));
+    const u32x6 p2 = __builtin_amdgcn_cvt_scalef32_pk32_fp6_f16(as_f16(x), 1.0f);
     if constexpr (D == 128) {
         q[0] = widen(p0);
         q[1] = widen(p1);
@@ -649,7 +644,7 @@ __device__ __forceinline__ void split_query(const u32x4 (&w)[4], float scale, in
         q[2] = q[1];   // not used
         scales = (up ? e - 4u : e) | (e - 9u) << 8;
     }
-    if (most >= 0x7F80u) scales = 0xFFFFFFFFu;
+    if (most >= 0x7F800000u) scales = 0xFFFFFFFFu;
 }
 
 // The rows [row0, row0 + 16 NQ) of a sequence's (query, head of the group) pairs; rows past the last one see what it sees.

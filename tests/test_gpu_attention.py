@@ -537,3 +537,55 @@ def test_a_layer_of_a_decoder(gpu):
     q2, out2 = step(whole, 0, total)
     assert torch.equal(q, q2) and all(torch.equal(a, b) for a, b in zip(cache, whole))
     assert (np.abs(out2.double().cpu().numpy() - want) <= bound).all()
+
+
+def wide_head_case(dim, q, key, value):
+    """One token's queries q [heads, dim] of one kv head against one cached token."""
+    case = Case([(1, 1)], q.shape[0], 1, dim, 16, 30)
+    case.q = torch.from_numpy(q.astype(np.float32)).bfloat16()[None]
+    at = case.table[0, 0], 0, 0
+    for i, x in ((0, key), (2, value)):
+        case.host[i][at], case.host[i + 1][at] = ref.encode(x)
+    return case
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_what_the_parts_of_a_query_leave(gpu, dim):
+    """An element of scale q counts to within 2^-13 of its block's largest magnitude, also where a rounding on the way to a
+    part would pass a border between two of its values: elements beside the middles of E2M3 neighbours.
+
+    One token with the value 1 against a sink of the exact score: out = 1 / (1 + exp(sink - s)), so out shows the score's
+    error, of scores near 2^13 times it. Counted beside it: the products' sum and the scale's roundings, (dim + 12) fp32 half
+    steps of the score, 2 of the sink's way into powers of two, 2 half steps of bf16 for the weight, and out's own."""
+    say(f"attention: parts of queries, heads of {dim}")
+    r = np.random.default_rng(31)
+    heads = 1024
+    log2e = np.float64(np.float32(1.44269504088896340736))
+    middles = np.arange(4.25, 7.5, 0.5)
+    for middle in [*middles, 3.875, 3.9375]:
+        for side in (-1, 1):
+            first = 1 + r.integers(0, 128) / 128
+            target = middle + side * 2.0**-6 * (1 - 2.0**-9)
+            scale = np.float64(np.float32(target / 8 / (first * log2e)))
+            q = np.zeros((heads, dim))
+            c = 2 * r.integers(0, dim // 2, heads)            # even channels: the key's; odd ones: zeros in the key
+            size = (1 + r.integers(0, 128, heads) / 128) * np.exp2(-r.integers(0, 3, heads))
+            size[:heads // 2] = first
+            q[np.arange(heads), c] = size * np.sign(r.standard_normal(heads))
+            most = np.maximum(size, np.where(r.random(heads) < 0.5, 1.0, 1 + r.integers(0, 128, heads) / 128))
+            most[:heads // 4] = first                         # the element is its block's largest
+            beside = most > size
+            q[np.arange(heads)[beside], c[beside] + 1] = most[beside]
+            unit = 2.0 ** np.floor(np.log2(2.0**13 / (2 * scale)))
+            key = np.where(np.arange(dim) % 2 == 0, unit, 0.0)
+            s = scale * q[np.arange(heads), c] * unit
+            case = wide_head_case(dim, q, key, np.ones(dim))
+            sinks = s.astype(np.float32)
+            out = gpu.mxfp4_attention(**case.device(), scale=float(scale), causal=False,
+                                      sinks=torch.from_numpy(sinks).to(DEV))[0].double().cpu().numpy()
+            delta = 2.0**-13 * scale * most * unit + (dim + 14) * ref.U_F32 * np.abs(s) + 2 * ref.U_BF16
+            d = s - sinks.astype(np.float64)
+            lo, hi = (1 / (1 + np.exp(-(d + x))) for x in (-delta, delta))
+            assert (delta < 1.1).all() and (hi < 0.8).all()
+            off = np.maximum(lo[:, None] * (1 - ref.U_BF16) - out, out - hi[:, None] * (1 + ref.U_BF16)).max(1)
+            assert off.max() <= 0, (middle, side, scale, q[off.argmax(), c[off.argmax()]], off.max())
