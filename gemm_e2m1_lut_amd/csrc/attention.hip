@@ -18,7 +18,7 @@
 //     scales 2^e, 2^(e-4), 2^(e-9), which leave 2^-13 of a block's largest
 //     magnitude (two parts: 2^-9). 4- and 6-bit operands run at twice the rate of
 //     8-bit ones, so the three products take 3/4 of the time of bf16 keys, and no
-//     key is unpacked. The accumulator starts at minus the maximum in use: the
+//     key is unpacked. The accumulator starts at minus the top in use (below): the
 //     result is the exponent of the weight. Heads of 64 channels fill half of the
 //     instruction's 128: the other half takes the second part of the same keys.
 //   * The scores come out transposed (a lane has 8 tokens of one query row), which
@@ -33,9 +33,11 @@
 //     the same registers with two index words, in the time of dense ones over the
 //     tokens, and nothing is permuted. Half an operation an element, for all NQ
 //     tiles. The weights' sum is one more such product, with ones.
-//   * The maximum is replaced only when a score passes it by 2^8 (a vote per step):
-//     weights are then at most 2^8, the sums fp32, and the usual step has no
-//     exchange between lanes and no rescaling.
+//   * Weights are powers of two below a top that lies 8 above the maximum when it is
+//     set, and is set anew only when a score passes it (a vote per step): the usual
+//     step has no exchange between lanes and no rescaling. Weights are at most 1, so
+//     the fp32 sums stay below the sum of the values' magnitudes, and the largest is
+//     2^-8 or more: those that pass below the smallest normal number are 2^-118 of it.
 // Weights are rounded to bf16 for the matrix cores: half a step is 2^-8 of a
 // weight, in the sum as in the product, and the errors of a row's weights are
 // independent: the result's own rounding is larger.
@@ -66,7 +68,7 @@ namespace {
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr int kRowWaves = 4;       // of a workgroup of attention_rows_kernel
 constexpr int kStep = 32;          // tokens a wave takes at a time
-constexpr float kSlack = 8.0f;     // how far a score may pass the maximum in use, in powers of two; 0: prompts 423 us, not 350
+constexpr float kSlack = 8.0f;     // how far the top lies above the maximum when it is set, in powers of two; 0: prompts 423 us, not 350
 constexpr int kFarRight = 0x7FFFFFFF;
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
@@ -303,7 +305,7 @@ struct Rows {
 };
 
 // o: channels D / 16 (lane % 16) + 2 b + c of rows 4 g + r; l: the weights' sums of these rows. Of row lane % 16: minus the
-// maximum in use (four times, as the scores' accumulator) and how far above it a score may be: nothing before there is one.
+// top (four times, as the scores' accumulator) and how far above it a score may be: nothing before there is one, then 0.
 template <int D, int NQ>
 struct Sums {
     f32x4 o[NQ][D / 16];
@@ -424,7 +426,7 @@ __device__ __forceinline__ uint32_t pack_weights(float a, float b) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
 }
 
-// Scores of a step's tokens, less the maximum in use.
+// Scores of a step's tokens, less the top.
 template <int D, int NQ>
 __device__ __forceinline__ void score(f32x4 (&x)[NQ][2], const Keys<D>& s, const Rows<NQ>& rows, const Sums<D, NQ>& sums) {
 #pragma unroll
@@ -506,7 +508,7 @@ __device__ __forceinline__ void take_step(const Keys<D>& keys, Values<D>& s, con
             }
         if (__any(high)) values_not_finite<D, NQ>(s, rows, sums, p.base, ln);
     }
-    // the maximum is left alone until a score is 2^8 above it
+    // the top is left alone until a score is above it
     bool past = false;
     float top[NQ];
 #pragma unroll
@@ -523,9 +525,10 @@ __device__ __forceinline__ void take_step(const Keys<D>& keys, Values<D>& s, con
             float v = fmaxf(top[i], __shfl_xor(top[i], 16, kWave));
             v = fmaxf(v, __shfl_xor(v, 32, kWave));
             const bool none = sums.slack[i] < 0.0f;
-            const float by = v == -INFINITY ? 0.0f : none ? v : fmaxf(v, 0.0f);
+            v += kSlack;
+            const float by = v == -INFINITY ? 0.0f : none ? v : fmaxf(v, 0.0f);   // 16 rows at once: each to its maximum
             const float f = none ? 1.0f : exp2_raw(-by);
-            if (v != -INFINITY) sums.slack[i] = kSlack;
+            if (v != -INFINITY) sums.slack[i] = 0.0f;
             sums.less[i] -= by;
 #pragma unroll
             for (int t = 0; t < 2; ++t) x[i][t] -= by;

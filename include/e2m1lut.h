@@ -404,8 +404,9 @@ size_t mxfp4_attention_workspace_size(int64_t tokens, int64_t seqs, int64_t head
  * over the tokens it sees (no sink term where sinks is NULL), zeros where it
  * sees none. Scores, maxima and sums are fp32, an element of scale q counts to
  * within 2^-13 of the largest magnitude of its 32 channels (or 2^-130, if that is
- * more), the weights exp(s_j - max) are rounded to bf16, out is rounded to bf16
- * once. A query that sees a key with a scale byte 255 is NaN in that head, one that
+ * more), the weights exp(s_j - max) are rounded to bf16 (one below 2^-118 may count
+ * as zero), out is rounded to bf16 once. It is finite as long as the magnitudes of
+ * the values that a query sees in a channel add up to less than 2^128. A query that sees a key with a scale byte 255 is NaN in that head, one that
  * sees a value with it in that block's 32 channels; what is in tokens that it does not
  * see changes nothing.
  *   q           bf16 [tokens, heads, head_dim] (16-byte aligned), a token's heads dense, tokens q_stride

@@ -589,3 +589,34 @@ def test_what_the_parts_of_a_query_leave(gpu, dim):
             assert (delta < 1.1).all() and (hi < 0.8).all()
             off = np.maximum(lo[:, None] * (1 - ref.U_BF16) - out, out - hi[:, None] * (1 + ref.U_BF16)).max(1)
             assert off.max() <= 0, (middle, side, scale, q[off.argmax(), c[off.argmax()]], off.max())
+
+
+@pytest.mark.parametrize("lens", [[(1, 200)], [(1, 3000), (2, 40)], [(40, 300), (3, 70)], [(300, 300), (70, 90)]])
+@pytest.mark.parametrize("byte", [0, 3, 120, 247, 250, 251, 252])
+def test_rising_scores_of_values_at_the_ends(gpu, lens, byte):
+    """Scores that rise from step to step, by less and by more than what moves the maximum, beside values with scale bytes at
+    the ends of the range, as long as the magnitudes of a channel's values sum to less than 2^128: finite, and as exact."""
+    say(f"attention: rising scores, values of byte {byte}, {lens}")
+    dim = 64
+    for rises in ((0, 3, 6, 8, 12), (1, 8, 0.5), (0, 6, 6, -6, 12), (0, 64, 96)):
+        case = Case(lens, 4, 2, dim, 16, 32)
+        case.q[:] = 0
+        case.q[:, :, 5] = 1          # the score: channel 5 of the key, in powers of two
+        for s, (_, l) in enumerate(lens):
+            key, value = np.zeros((l, 2, dim)), np.zeros((l, 2, dim))
+            for i, x in enumerate(rises):
+                j = min(40 * i + 3, l - 1)
+                key[j, :, 5] = x
+                # magnitudes of a channel sum to less than 2^128: a 6, or a 1 and some 0.5, times 2^(byte - 127)
+                if byte == 252:
+                    value[j, :, i::len(rises)] = 6.0
+                else:
+                    value[j] = 1.0 if i == len(rises) - 1 else 0.5
+                    value[j, :, ::2] *= -1
+            page = case.table[s, np.arange(l) // 16]
+            j = np.arange(l)
+            case.host[0][page, :, j % 16], case.host[1][page, :, j % 16] = ref.encode(key)
+            code = ref.nearest(np.abs(value)) | (np.signbit(value).astype(np.uint8) << 3)
+            case.host[2][page, :, j % 16], case.host[3][page, :, j % 16] = code[..., ::2] | code[..., 1::2] << 4, byte
+        out = run(gpu, case, scale=float(np.log(2)))
+        assert torch.isfinite(out).all()
