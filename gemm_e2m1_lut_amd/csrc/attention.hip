@@ -112,16 +112,19 @@ __device__ __forceinline__ float exp2_raw(float x) { return __builtin_amdgcn_exp
 struct Span {
     int first;   // its first query row
     int n;       // queries
-    int len;     // cached tokens
+    int len;     // cached tokens, also where the table has no room for them: positions go by it
 };
 
+// The tokens that a sequence's pages have room for.
+__device__ __forceinline__ int table_room(const Attention& a, int page_bits) { return (int)(a.table_width << page_bits); }
+
 __device__ __forceinline__ Span make_span(const Attention& a, int page_bits, int o0, int o1, int len) {
-    const int tokens = (int)a.tokens, most = (int)(a.table_width << page_bits);
+    const int tokens = (int)a.tokens;
     Span r;
     r.first = min(max(o0, 0), tokens);
     r.n = min(max(o1, r.first), tokens) - r.first;
-    r.len = min(max(len, 0), most);
-    if (len > most && r.n > 0 && a.err_flag) *a.err_flag = 1;
+    r.len = max(len, 0);
+    if (len > table_room(a, page_bits) && r.n > 0 && a.err_flag) *a.err_flag = 1;
     return r;
 }
 
@@ -140,9 +143,9 @@ __device__ __forceinline__ uint32_t tiles_of(const Span& s, int group, int rows)
 }
 
 // Units of 2^unit_bits tokens of every tile of a sequence.
-__device__ __forceinline__ uint32_t units_of(const Attention& a, const Span& s, int unit_bits) {
-    const int lo = first_seen(a, s, 0) & ~(kStep - 1);
-    return max(1u, ((uint32_t)(s.len - lo) + (1u << unit_bits) - 1) >> unit_bits);
+__device__ __forceinline__ uint32_t units_of(const Attention& a, int page_bits, const Span& s, int unit_bits) {
+    const int hi = min(s.len, table_room(a, page_bits)), lo = min(first_seen(a, s, 0), hi) & ~(kStep - 1);
+    return max(1u, ((uint32_t)(hi - lo) + (1u << unit_bits) - 1) >> unit_bits);
 }
 
 template <int kCtrl, int kRowMask>
@@ -652,25 +655,25 @@ __device__ __forceinline__ void split_query(const u32x4 (&w)[4], float scale, in
 
 // The rows [row0, row0 + 16 NQ) of a sequence's (query, head of the group) pairs; rows past the last one see what it sees.
 template <int D, int NQ>
-__device__ __forceinline__ void set_ranges(Rows<NQ>& rows, const Attention& a, const Span& s, int group, const Divisor& by,
-                                           int row0, const Lane<D>& ln) {
+__device__ __forceinline__ void set_ranges(Rows<NQ>& rows, const Attention& a, int room, const Span& s, int group,
+                                           const Divisor& by, int row0, const Lane<D>& ln) {
     const int last = s.n * group - 1;
     const int i_first = divide(row0, by), i_last = divide(min(row0 + 16 * NQ - 1, last), by);
     const int p0 = s.len - s.n;   // position of query 0
     if (a.causal) {
         rows.lo_all = first_seen(a, s, i_first);
         rows.lo_max = first_seen(a, s, i_last);
-        rows.hi_all = max(0, p0 + i_last + 1);
-        rows.hi_min = max(0, p0 + i_first + 1);
+        rows.hi_all = max(0, min(p0 + i_last + 1, room));
+        rows.hi_min = max(0, min(p0 + i_first + 1, room));
     } else {
         rows.lo_all = rows.lo_max = 0;
-        rows.hi_all = rows.hi_min = s.len;
+        rows.hi_all = rows.hi_min = min(s.len, room);
     }
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
         const int q = divide(min(row0 + 16 * i + ln.n, last), by);
         rows.lo[i] = a.causal ? first_seen(a, s, q) : 0;
-        rows.hi[i] = a.causal ? max(0, p0 + q + 1) : s.len;
+        rows.hi[i] = max(0, min(a.causal ? p0 + q + 1 : s.len, room));
     }
 }
 
@@ -681,7 +684,7 @@ __device__ __forceinline__ void run_steps(const Attention& a, const CacheView& c
                                           int kv_head, int group, const Divisor& by, int row0, int first, int last,
                                           int stride, Sums<D, NQ>& sums, const Lane<D>& ln) {
     Rows<NQ> rows;
-    set_ranges<D, NQ>(rows, a, s, group, by, row0, ln);
+    set_ranges<D, NQ>(rows, a, table_room(a, c.page_bits), s, group, by, row0, ln);
     sums.clear();
     if (c.slots == 0) return;   // no page is there
     // steps with a token that some row sees
@@ -723,7 +726,10 @@ __device__ __forceinline__ void run_steps(const Attention& a, const CacheView& c
     load_keys<D>(keys[0], c, p0, ln);
     load_values<D>(values[0], c, p0, ln);
 #pragma unroll
-    for (int b = 0; b < NQ; ++b) split_query<D>(w[b], a.scale * kLog2e, ln.g, rows.q[b], rows.qs[b]);
+    for (int b = 0; b < NQ; ++b) {
+        split_query<D>(w[b], a.scale * kLog2e, ln.g, rows.q[b], rows.qs[b]);
+        __builtin_amdgcn_sched_barrier(0);   // a tile's parts after the other's: packed prompts 355 us, 361 without
+    }
     for (;;) {
         p1 = next_place();
         load_keys<D>(keys[1], c, p1, ln);
@@ -795,7 +801,7 @@ __global__ __launch_bounds__(kW * kWave, 2) void attention_split_kernel(Attentio
     const int group = a.heads / c.heads;
 
     auto segments = [&](const Span& s) { return tiles_of(s, group, kRows) * c.heads; };
-    auto weight = [&](const Span& s) { return segments(s) * units_of(a, s, unit_bits); };
+    auto weight = [&](const Span& s) { return segments(s) * units_of(a, c.page_bits, s, unit_bits); };
     const Plan plan(a, c.page_bits, lane, weight);
     // neighbours in the order of work on the same XCD, whose L2 then holds what they share; of more workgroups than segments the
     // first ones have work, so that all XCDs do
@@ -822,14 +828,14 @@ __global__ __launch_bounds__(kW * kWave, 2) void attention_split_kernel(Attentio
     }
     if (idle) return;
     Span s = plan.span(seq);
-    uint32_t units = units_of(a, s, unit_bits), segs = segments(s);
+    uint32_t units = units_of(a, c.page_bits, s, unit_bits), segs = segments(s);
     Record cut = {};
     while (u < u_end) {
         while (u >= begin + segs * units) {   // on to the next sequence that has queries
             begin += segs * units;
             segs_before += segs;
             s = plan.span(++seq);
-            units = units_of(a, s, unit_bits);
+            units = units_of(a, c.page_bits, s, unit_bits);
             segs = segments(s);
         }
         const uint32_t segment = units == 1 ? u - begin : (u - begin) / units;

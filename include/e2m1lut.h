@@ -422,7 +422,8 @@ size_t mxfp4_attention_workspace_size(int64_t tokens, int64_t seqs, int64_t head
  *               where that size is 0); the call writes it, so calls that overlap
  *               in time need workspaces of their own
  * A token on a page outside [0, pages) is not seen, tokens past table_width
- * pages neither, and err_flag is set for both. A negative length counts as 0,
+ * pages neither (positions go by kv_lens all the same), and err_flag is set for
+ * both. A negative length counts as 0,
  * an offset outside 0 .. tokens as the nearer end. Where an offset is below the
  * one before it nothing is written but err_flag.
  * Requires heads a multiple of kv_heads, at most E2M1_CACHE_MAX_HEADS, tokens *

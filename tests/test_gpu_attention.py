@@ -620,3 +620,32 @@ def test_rising_scores_of_values_at_the_ends(gpu, lens, byte):
             case.host[2][page, :, j % 16], case.host[3][page, :, j % 16] = code[..., ::2] | code[..., 1::2] << 4, byte
         out = run(gpu, case, scale=float(np.log(2)))
         assert torch.isfinite(out).all()
+
+
+@pytest.mark.parametrize("lens,room", [([(40, 200)], 112), ([(1, 200), (7, 30), (3, 118)], 112), ([(5, 5000), (2, 900)], 4000),
+                                       ([(150, 400), (150, 150)], 320), ([(300, 700), (200, 300), (1, 640)], 640),
+                                       ([(30, 33000)], 32000), ([(3, 2**31 - 1), (90, 2**31 - 1)], 640)])
+@pytest.mark.parametrize("causal,window", [(True, 0), (True, 50), (False, 0)])
+def test_lengths_past_the_table(gpu, lens, room, causal, window):
+    """The last query is at the length less 1 wherever the table ends; tokens past the table are not seen, and flagged."""
+    say(f"attention: lengths past a table of {room}, {lens}, causal {causal}, window {window}")
+    heads, kv, dim = 8, 2, 128
+    sinks = np.linspace(-1, 1, heads).astype(np.float32)
+    case = Case([(n, min(l, room)) for n, l in lens], heads, kv, dim, 16, 33)
+    case.table = case.table[:, :room // 16].copy()
+    case.kv_lens = np.array([l for _, l in lens], np.int32)
+    flag = torch.zeros(1, dtype=torch.int32, device=DEV)
+    got = gpu.mxfp4_attention(**case.device(), causal=causal, window=window, sinks=torch.from_numpy(sinks).to(DEV),
+                              err_flag=flag).double().cpu().numpy()
+    assert flag.item() == 1
+    for s, (n, length) in enumerate(lens):
+        k, v = case.rows_of(s)
+        for i in sorted({0, 1, n // 3, n // 2, n - 2, n - 1} & set(range(n))):
+            pos = length - n + i
+            lo = max(0, pos - window + 1) if window else 0
+            hi = min(pos + 1 if causal else length, room)
+            lo = min(lo, hi)
+            at = case.offsets[s] + i
+            want, bound = ref.attention(case.q[at:at + 1].double().numpy(), k[lo:hi], v[lo:hi], dim ** -0.5, False, 0, sinks)
+            assert (np.abs(got[at:at + 1] - want) <= bound).all(), (s, i)
+            assert hi > lo or not got[at].any()
