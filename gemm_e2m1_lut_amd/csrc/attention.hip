@@ -686,13 +686,16 @@ __device__ __forceinline__ void run_steps(const Attention& a, const CacheView& c
     Rows<NQ> rows;
     set_ranges<D, NQ>(rows, a, table_room(a, c.page_bits), s, group, by, row0, ln);
     sums.clear();
-    if (c.slots == 0) return;   // no page is there
     // steps with a token that some row sees
     int at = first;
     const int low = rows.lo_all / kStep;
     if (at < low) at += (low - at + stride - 1) & ~(stride - 1);   // stride: a power of two
     const int end = min(last, (int)(((uint32_t)rows.hi_all + kStep - 1) / kStep));
     if (at >= end) return;
+    if (c.slots == 0) {   // no page is there
+        if (a.err_flag) *a.err_flag = 1;
+        return;
+    }
     // the queries' bytes first: their parts are made while the first tokens are on their way
     u32x4 w[NQ][4];
 #pragma unroll

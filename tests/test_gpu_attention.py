@@ -649,3 +649,21 @@ def test_lengths_past_the_table(gpu, lens, room, causal, window):
             want, bound = ref.attention(case.q[at:at + 1].double().numpy(), k[lo:hi], v[lo:hi], dim ** -0.5, False, 0, sinks)
             assert (np.abs(got[at:at + 1] - want) <= bound).all(), (s, i)
             assert hi > lo or not got[at].any()
+
+
+def test_pages_missing_from_an_empty_cache(gpu):
+    """A token on a page that an empty cache does not have sets the flag, as on any other page that is not there; queries that
+    see no token do not."""
+    say("attention: an empty cache and its flag")
+    for lens in ([(2, 40), (1, 5)], [(90, 100)], [(1, 5000)], [(300, 300), (300, 600)]):
+        case = Case(lens, 4, 2, 64, 16, 34)
+        d = case.device()
+        d["cache"] = tuple(t[:0] for t in d["cache"])
+        flag = torch.zeros(1, dtype=torch.int32, device=DEV)
+        assert not gpu.mxfp4_attention(**d, err_flag=flag).any() and flag.item() == 1
+        flag.zero_()
+        d["kv_lens"].zero_()
+        assert not gpu.mxfp4_attention(**d, err_flag=flag).any() and flag.item() == 0
+        gpu.mxfp4_attention(**{**case.device(), "cache": d["cache"], "q_offsets": torch.zeros_like(d["q_offsets"])},
+                            err_flag=flag)
+        assert flag.item() == 0
