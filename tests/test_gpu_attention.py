@@ -667,3 +667,18 @@ def test_pages_missing_from_an_empty_cache(gpu):
         gpu.mxfp4_attention(**{**case.device(), "cache": d["cache"], "q_offsets": torch.zeros_like(d["q_offsets"])},
                             err_flag=flag)
         assert flag.item() == 0
+
+
+@pytest.mark.parametrize("first", [True, False])
+@pytest.mark.parametrize("form,heads,kv,dim,chunk", [(20, 32, 8, 128, (1900, 2600)), (30, 64, 16, 64, (1300, 1400)),
+                                                     (1224, 32, 8, 128, (1300, 2000)), (224, 16, 4, 128, (100, 9000))])
+def test_prompts_beside_long_contexts(gpu, form, heads, kv, dim, chunk, first):
+    """A chunk of a prompt, drafts and single tokens after contexts of all lengths in one call, whatever its form."""
+    say(f"attention: a chunk of {chunk} beside single tokens, form {form}, {first}")
+    others = [(1, 12000), (1, 40), (4, 6001), (0, 700), (1, 1), (1, 2500)]
+    case = Case([chunk, *others] if first else [*others, chunk], heads, kv, dim, 64, 35)
+    choose = gpu.load_library().e2m1_mxfp4_attention_form
+    choose.argtypes = [ctypes.c_int64] * 6
+    assert choose(case.tokens, len(case.lens), heads, kv, dim, case.table.shape[1] * 64) == form
+    run(gpu, case)
+    run(gpu, case, window=1500, sinks=np.linspace(-2, 2, heads).astype(np.float32))
