@@ -43,19 +43,19 @@
 // independent: the result's own rounding is larger.
 // No LDS and no barrier in the loop: the bytes of a step are few (4352 for 32
 // tokens of 128 channels), waves that share tokens find them in the L1, and the
-// loads of the next step are on their way into a second set of registers (a ring
-// of steps in LDS, filled by direct-to-LDS loads: 397 us instead of 376 for packed
-// prompts, 75 instead of 71 for 64 ragged sequences; three or four sets of
-// registers: 80 to 91).
+// loads of the next step are on their way into a second set of registers. (Measured
+// before the offsets and shares of today, all else alike: a ring of steps in LDS,
+// filled by direct-to-LDS loads, took 6 % longer for packed prompts and for 64
+// ragged sequences, three or four sets of registers 13 to 28 % for the latter.)
 //
 // Bounds. One token of many sequences: HBM, 304 MB (64 sequences of 512 to 8192
 // tokens) in 69 us, 4.4 TB/s; 64 of 16384 tokens 200 us, 5.7 TB/s. Prompts: issue,
 // since vector instructions hardly overlap matrix ones here (a 16x16x32 product takes 20
 // cycles, with two fma 24; the conversion of two values 6.6, an exp 9): per 32 tokens
 // and 32 rows of 128 channels 12 + 16 + 2 matrix and about 100 vector instructions:
-// 8192 new tokens 543 us, 1.01 PFLOP/s where the library's bf16 product of 8192^3
+// 8192 new tokens 545 us, 1.01 PFLOP/s where the library's bf16 product of 8192^3
 // reaches 1.23. Little of both: latency, of two reads one after the other (lengths,
-// page numbers), a step and the joins: 777 tokens 10.7 us, 32 tokens 4.7.
+// page numbers), a step and the joins: 777 tokens 10.8 us, 32 tokens 4.7.
 // Two tiles of 128 channels (three of 64) fill 256 registers; four need the second
 // half of the register file, and 35 moves a tile and step (slower); three waves a
 // SIMD spill.
@@ -68,7 +68,7 @@ namespace {
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr int kRowWaves = 4;       // of a workgroup of attention_rows_kernel
 constexpr int kStep = 32;          // tokens a wave takes at a time
-constexpr float kSlack = 8.0f;     // how far the top lies above the maximum when it is set, in powers of two; 0: prompts 423 us, not 350
+constexpr float kSlack = 8.0f;     // how far the top lies above the maximum when it is set (0: packed prompts 419 us, not 355)
 constexpr int kFarRight = 0x7FFFFFFF;
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
@@ -1019,7 +1019,9 @@ __global__ __launch_bounds__(kJoinWaves * kWave) void attention_join_kernel(Atte
     }
 }
 
-// Many rows: a wave has a tile of its own and goes through all that it sees; the tiles with the most tokens first.
+// Many rows: a wave has a tile of its own and goes through all that it sees. Tile groups are taken from the last to the first,
+// of a sequence those with the most tokens first, of sequences the last one, whatever its length: packed prompts of 5000, 3334,
+// 1667 and 1 tokens 356 us, in the other order 350.
 template <int D, int NQ>
 __global__ __launch_bounds__(kRowWaves * kWave, 2) void attention_rows_kernel(Attention a, CacheView c, int round, Divisor by) {
     constexpr int NJ = D / 16;
@@ -1070,7 +1072,10 @@ int64_t most_tiles(int64_t tokens, int64_t seqs, int64_t group, int64_t rows) {
 // How a call is worked on, from what the host knows: the numbers of rows and sequences, and how many tokens a row can see. The
 // times below are of 32 query heads over 8 of 128 channels, in us; n: segments of 16 rows. The choice was taken from 70 calls
 // (heads of 64 and 128 channels, 1 to 2048 queries, 1 to 256 sequences of 64 to 131072 tokens) timed in every form: it is 1 %
-// above the fastest form on the mean, 14 % at most.
+// above the fastest form on the mean, 14 % at most. In all of them the sequences had alike many queries and filled their
+// tables. The host knows the mean of the queries and the width of the table only, and where they say little the choice is far
+// off: 2048 queries after 6144 tokens beside 30 single ones after 8192 to 131072 go in tiles, each long sequence a wave's alone,
+// 2770 us (in two calls 242 + 262); 64 single ones after 1000 take 22.0 with a table of 131072, 17.2 with one of their length.
 enum Kind { kRowsForm, kWholeForm, kSplitForm };
 struct Form {
     Kind kind;

@@ -405,10 +405,11 @@ size_t mxfp4_attention_workspace_size(int64_t tokens, int64_t seqs, int64_t head
  * sees none. Scores, maxima and sums are fp32, an element of scale q counts to
  * within 2^-13 of the largest magnitude of its 32 channels (or 2^-130, if that is
  * more), the weights exp(s_j - max) are rounded to bf16 (one below 2^-118 may count
- * as zero), out is rounded to bf16 once. It is finite as long as the magnitudes of
- * the values that a query sees in a channel add up to less than 2^128. A query that sees a key with a scale byte 255 is NaN in that head, one that
- * sees a value with it in that block's 32 channels; what is in tokens that it does not
- * see changes nothing.
+ * as zero), out is rounded to bf16 once. With finite scores it is finite as long as
+ * the magnitudes of the values that a query sees in a channel add up to less than
+ * 2^128. A query that sees a key with a scale byte 255 is NaN in that head, one that
+ * sees a value with it in that block's 32 channels; what is in tokens that it does
+ * not see changes nothing.
  *   q           bf16 [tokens, heads, head_dim] (16-byte aligned), a token's heads dense, tokens q_stride
  *               elements apart (at least heads * head_dim, a multiple of 8)
  *   page_table  int32 [seqs, table_width]; entries past a sequence's tokens are not read
@@ -423,9 +424,12 @@ size_t mxfp4_attention_workspace_size(int64_t tokens, int64_t seqs, int64_t head
  *               in time need workspaces of their own
  * A token on a page outside [0, pages) is not seen, tokens past table_width
  * pages neither (positions go by kv_lens all the same), and err_flag is set for
- * both. A negative length counts as 0,
- * an offset outside 0 .. tokens as the nearer end. Where an offset is below the
- * one before it nothing is written but err_flag.
+ * both. A negative length counts as 0, an offset outside 0 .. tokens as the
+ * nearer end. Where an offset is below the one before it nothing is written but
+ * err_flag.
+ * How the work is cut is chosen by the mean number of queries a sequence and by
+ * table_width: a prompt beside single tokens after long contexts is faster in two
+ * calls, a table no wider than its sequences need faster than a wide one.
  * Requires heads a multiple of kv_heads, at most E2M1_CACHE_MAX_HEADS, tokens *
  * heads <= E2M1_ATTENTION_MAX_ROWS, 0 <= seqs <= E2M1_CACHE_MAX_TOKENS,
  * table_width * page_size <= E2M1_ATTENTION_MAX_LENGTH, 0 <= scale <= 2^126, window >= 0 (0: none) and
