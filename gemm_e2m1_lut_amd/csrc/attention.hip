@@ -609,7 +609,8 @@ __device__ __forceinline__ i32x8 widen(const u32x6& v) {
 // on their way to a part, which may pass a border between two of its values by no more than half a step of fp16: 2^-9 of the
 // first unit, 2^-10 of the others. What is left stays within 1/4 + 2^-9, 2^-7 + 2^-14 and 2^-12 + 2^-19: the next part's value
 // nearest to it is the last one before its steps grow (through bf16 2^-6 can be left for the third part, past its end, and 2^-10
-// by it). A block that holds a NaN or an infinity gets the scale NaN.
+// by it; the conversion from fp32, 2xpk16, gets its result on its operands' registers from this compiler, and spoils two of them).
+// A block that holds a NaN or an infinity gets the scale NaN.
 template <int D>
 __device__ __forceinline__ void split_query(const u32x4 (&w)[4], float scale, int g, i32x8 (&q)[3], uint32_t& scales) {
     u16x2 top = {0, 0};
